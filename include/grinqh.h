@@ -276,6 +276,161 @@ grinqh_status grinqh_prefill_gemm(const grinqh_layout* L, const void* x, grinqh_
                                   grinqh_dtype y_dtype, void* workspace, size_t workspace_bytes,
                                   void* stream);
 
+/* ---- Key-value cache ----------------------------------------------------
+ *
+ * The pages of keys and values that a decoder's attention reads, one cache
+ * per layer.  A row is the head_dim values of one token and one key-value
+ * head.  At 4 and 8 bits a row is quantised as it is written, onto the grid
+ * that grinqh_quantize_rtn uses for a row of weights (KD3 at b = b_max):
+ *   lo, hi = min and max of the row (NaN ignored);
+ *   s = fp16((hi - lo) / 2^bits), z = fp16(lo) (zeros stored as +0);
+ *   c = min(max(floor((w - z) / s), 0), 2^bits - 1) in fp32 with the stored
+ *       s and z (a NaN quotient gives 0; a row with s = 0 gets 0),
+ * and stands for s * (c + 1/2) + z.  At 16 bits a row is kept as bf16 (fp32
+ * input rounded to nearest even).  Values outside fp16's range overflow s
+ * and z to Inf, and the row then reads as Inf or NaN.
+ *
+ * A pool holds n_pages pages of page_size tokens:
+ *   codes  uint8 [n_pages][n_kv_heads][page_size][row_bytes], 16-byte
+ *          aligned; at 4 bits byte i of a row holds values 2i (low half)
+ *          and 2i + 1, at 16 bits the row is head_dim bf16.
+ *   grid   fp16 [n_pages][n_kv_heads][page_size][2]: s, z of every row,
+ *          16-byte aligned; NULL at 16 bits.
+ * Slot page * page_size + t names token t of a page, in every head. */
+typedef struct {
+    int32_t n_kv_heads;   /* 1 .. 1024 */
+    int32_t head_dim;     /* 64, 128 or 256 */
+    int32_t page_size;    /* 16, 32, 64, 128 or 256 tokens */
+    int32_t n_pages;      /* 1 .. 2^24 */
+    int32_t bits;         /* 4, 8 or 16 */
+    int32_t row_bytes;    /* head_dim * bits / 8 */
+} grinqh_kv_layout;
+
+/* Device pointers of one cache: a pool of keys and one of values. */
+typedef struct {
+    uint8_t* k_codes;
+    uint8_t* v_codes;
+    uint16_t* k_grid;
+    uint16_t* v_grid;
+} grinqh_kv_pools;
+
+/* Fill *out (host pointer); EINVAL for a value outside the ranges above. */
+grinqh_status grinqh_kv_layout_init(int32_t n_kv_heads, int32_t head_dim, int32_t page_size, int32_t n_pages,
+                                    int32_t bits, grinqh_kv_layout* out);
+
+/* Bytes of one pool's codes and of its grid (0 at 16 bits); 0 if L is NULL or
+ * invalid.  Host only. */
+size_t grinqh_kv_code_bytes(const grinqh_kv_layout* L);
+size_t grinqh_kv_grid_bytes(const grinqh_kv_layout* L);
+
+/* Write the keys and values of n_tokens tokens into their slots.
+ *   k, v       [n_tokens][n_kv_heads][head_dim] of dtype, 16-byte aligned; the
+ *              tokens lie k_stride and v_stride elements apart (multiples of
+ *              16 bytes, at least n_kv_heads * head_dim), so both can be
+ *              slices of a fused projection's output.
+ *   n_tokens   0 .. 2^24 (0: nothing is launched).
+ *   slots      int64 [n_tokens]; a token whose slot is negative or not below
+ *              n_pages * page_size is not written (padding).  The slots
+ *              written by one call must differ: a slot named twice is left
+ *              holding a mixture of the rows.
+ * k and v must not overlap the pools. */
+grinqh_status grinqh_kv_write(const grinqh_kv_layout* L, const grinqh_kv_pools* pools, const void* k,
+                              const void* v, grinqh_dtype dtype, int64_t k_stride, int64_t v_stride,
+                              int32_t n_tokens, const int64_t* slots, void* stream);
+
+/* Read the values of n_tokens slots back, in any order and any number of
+ * times each.
+ *   k, v   [n_tokens][n_kv_heads][head_dim] of dtype out, contiguous, 16-byte
+ *          aligned: s * (c + 1/2) + z in fp32 (one rounding), bf16 output
+ *          rounded to nearest even; zeros for a slot outside the pool. */
+grinqh_status grinqh_kv_read(const grinqh_kv_layout* L, const grinqh_kv_pools* pools, const int64_t* slots,
+                             int32_t n_tokens, void* k, void* v, grinqh_dtype dtype, void* stream);
+
+/* Test call, host only: the row index (of row_bytes codes, and of one s, z
+ * pair) that the kernels use for a slot and head; -1 for a slot outside the
+ * pool, a head outside 0 .. n_kv_heads - 1 or an invalid layout. */
+int64_t grinqh_debug_kv_row(const grinqh_kv_layout* L, int64_t slot, int32_t head);
+
+/* ---- Attention -----------------------------------------------------------
+ *
+ * For every query head h of a query token, with key-value head
+ * g = h / (n_q_heads / n_kv_heads),
+ *   o_h = sum_t p_t v_gt,  p_t = exp(a_t) / sum_u exp(a_u),  a_t = scale * q_h . k_gt,
+ * over the tokens t that the query sees.  A query that sees none gets zeros.
+ * lse_h = log(sum_t exp(a_t)) (-Inf where no token is seen).  Scores, softmax
+ * statistics and sums are fp32.  Infinities and NaN in a token that is seen go
+ * into the outputs of its heads as the formula says; in tokens that are not seen
+ * they have no effect.
+ *
+ * Decode stage: one new token of every sequence attends to its cached
+ * tokens (the new one among them, if it was written first).
+ *   q           [batch][n_q_heads][head_dim] of q_dtype, 16-byte aligned; the
+ *               sequences' tokens lie q_stride elements apart (a multiple of
+ *               16 bytes, at least n_q_heads * head_dim).
+ *   n_q_heads   a multiple of L->n_kv_heads, up to 1024.
+ *   page_table  int32 [batch][max_pages], rows table_stride entries apart: the
+ *               pages of a sequence in order.  A page outside 0 .. n_pages - 1
+ *               is absent: its tokens are not seen.
+ *   seq_lens    int32 [batch]: cached tokens of each sequence, taken as 0 if
+ *               negative and as min(max_len, max_pages * page_size) if above.
+ *   batch       0 .. 2^20 (0: nothing is launched); max_len 1 .. 2^28, the
+ *               host's bound on the lengths.
+ *   scale       finite.
+ *   out         [batch][n_q_heads][head_dim] of out_dtype, contiguous, 16-byte
+ *               aligned.
+ *   lse         fp32 [batch][n_q_heads] or NULL.
+ *   workspace   >= grinqh_attention_workspace_bytes(...) bytes, 256-byte
+ *               aligned, zero-filled before its first use by this call; every
+ *               call leaves it ready for the next, of any layout and sizes.
+ *               Calls that share it must not overlap in time, and
+ *               grinqh_gemv must have its own.
+ * The result of a call does not depend on timing: the parts of a long
+ * cache are joined in their order.  q and out must not overlap. */
+size_t grinqh_attention_workspace_bytes(const grinqh_kv_layout* L, int32_t n_q_heads, int32_t batch,
+                                        int32_t max_len);
+grinqh_status grinqh_decode_attention(const grinqh_kv_layout* L, const grinqh_kv_pools* pools, const void* q,
+                                      grinqh_dtype q_dtype, int64_t q_stride, int32_t n_q_heads,
+                                      const int32_t* page_table, int64_t table_stride, int32_t max_pages,
+                                      const int32_t* seq_lens, int32_t batch, int32_t max_len, float scale,
+                                      void* out, grinqh_dtype out_dtype, float* lse, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
+/* Prefill stage: whole prompts, packed behind one another without padding.
+ * Sequence b has the query rows cu_q[b] .. cu_q[b+1] - 1 and the key rows
+ * cu_k[b] .. cu_k[b+1] - 1.  With causal nonzero the last query sees every key
+ * and each earlier one a key less: query i of n sees the keys 0 .. i + m - n of
+ * m (so with more keys than queries the first keys are the cached
+ * beginning, and with fewer the first queries see nothing).
+ *   q          bf16 [total_q][n_q_heads][head_dim], token rows q_stride elements
+ *              apart; k, v bf16 [total_k][n_kv_heads][head_dim], k_stride and
+ *              v_stride apart (multiples of 8; rows may be slices of a fused
+ *              projection's output); all 16-byte aligned.
+ *   cu_q, cu_k int32 [batch + 1], ascending from 0; entries are clamped to
+ *              0 .. total_q (total_k).
+ *   total_q, total_k  0 .. 2^24 rows (total_q 0: nothing is launched).
+ *   n_q_heads  a multiple of n_kv_heads, up to 1024; head_dim 64, 128 or 256.
+ *   scale      finite.
+ *   out        [total_q][n_q_heads][head_dim] of out_dtype, contiguous, 16-byte
+ *              aligned; rows behind the last sequence are left as they are.
+ *   lse        fp32 [total_q][n_q_heads] or NULL.
+ * The weights p_t are rounded to bf16 for the product with the values. */
+typedef struct {
+    const void* q;
+    const void* k;
+    const void* v;
+    int64_t q_stride, k_stride, v_stride;
+    const int32_t* cu_q;
+    const int32_t* cu_k;
+    int32_t batch, total_q, total_k;
+    int32_t n_q_heads, n_kv_heads, head_dim;
+    int32_t causal;
+    float scale;
+    void* out;
+    grinqh_dtype out_dtype;
+    float* lse;
+} grinqh_prefill_attention_args;
+grinqh_status grinqh_prefill_attention(const grinqh_prefill_attention_args* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

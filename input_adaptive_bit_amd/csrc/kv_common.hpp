@@ -1,0 +1,55 @@
+// The key-value cache's addressing and row values, shared by the kernels that
+// write, read and attend to it and by the host's checks.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "device_common.hpp"
+#include "grinqh.h"
+
+namespace grinqh {
+
+// What a kernel needs of a layout (page_size is a power of two).
+struct KvDims {
+    int heads, page_shift, n_pages;
+};
+
+inline int log2_of(int v) {
+    int s = 0;
+    while ((1 << s) < v) ++s;
+    return s;
+}
+
+inline KvDims kv_dims(const grinqh_kv_layout& L) { return KvDims{L.n_kv_heads, log2_of(L.page_size), L.n_pages}; }
+
+// Row of (slot, head), or -1 for a slot outside the pool.  64 bits: a pool
+// may hold more than 2^31 rows and 2^32 bytes.
+__host__ __device__ __forceinline__ int64_t kv_row(const KvDims& d, int64_t slot, int head) {
+    if (static_cast<uint64_t>(slot) >= static_cast<uint64_t>(d.n_pages) << d.page_shift) return -1;
+    const int64_t page = slot >> d.page_shift;
+    const int64_t t = slot & ((int64_t{1} << d.page_shift) - 1);
+    return ((page * d.heads + head) << d.page_shift) + t;
+}
+
+// Largest sizes the calls accept.
+constexpr int kMaxKvHeads = 1024, kMaxQHeads = 1024;
+constexpr int64_t kMaxStride = int64_t{1} << 32;   // elements between tokens
+constexpr int kMaxBatch = 1 << 20, kMaxCacheLen = 1 << 28, kMaxPacked = 1 << 24;
+
+inline bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+inline bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+    return na > 0 && nb > 0 && a0 < b0 + nb && b0 < a0 + na;
+}
+
+bool valid_kv_layout(const grinqh_kv_layout* L);
+// Host checks of a cache: GRINQH_OK, or the status a call returns.
+grinqh_status check_kv_pools(const grinqh_kv_layout* L, const grinqh_kv_pools* pools);
+
+__device__ __forceinline__ uint16_t f32_to_bf16(float f) {
+    return __builtin_bit_cast(uint16_t, static_cast<__bf16>(f));   // round to nearest even
+}
+
+}  // namespace grinqh

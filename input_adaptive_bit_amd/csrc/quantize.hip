@@ -12,10 +12,8 @@
 // so that s_j * (q + 1/2) + z_j, the key-design-3 value at b = b_max, is the
 // midpoint of w's interval.  One workgroup per output row: a min/max pass,
 // then the codes (the row is read again from L2).
-#include <hip/hip_fp16.h>
-#include <math.h>
-
 #include "internal.h"
+#include "rtn.hpp"
 
 namespace grinqh {
 namespace {
@@ -23,13 +21,6 @@ namespace {
 constexpr int kRtnThreads = 256;
 
 __device__ __forceinline__ float bf16_value(uint32_t b) { return __uint_as_float(b << 16); }
-
-__device__ __forceinline__ uint8_t rtn_code(float w, float z, float s, float top) {
-    float u = floorf(__fdiv_rn(w - z, s));
-    u = fmaxf(u, 0.f);                         // a NaN quotient becomes 0 here
-    u = fminf(u, top);
-    return static_cast<uint8_t>(u);
-}
 
 __global__ __launch_bounds__(kRtnThreads) void rtn_kernel(const uint16_t* __restrict__ w, int d_in, int b_max,
                                                           uint8_t* __restrict__ q, uint16_t* __restrict__ s_out,
@@ -74,8 +65,8 @@ __global__ __launch_bounds__(kRtnThreads) void rtn_kernel(const uint16_t* __rest
     }
     if (tid == 0) {
         const float rlo = red_lo[0], rhi = red_hi[0];
-        const __half sh = __float2half_rn((rhi - rlo) * __uint_as_float(static_cast<uint32_t>(127 - b_max) << 23) + 0.f);
-        const __half zh = __float2half_rn(rlo + 0.f);
+        const __half sh = rtn_scale(rlo, rhi, b_max);
+        const __half zh = rtn_zero(rlo);
         s_out[j] = __half_as_ushort(sh);
         z_out[j] = __half_as_ushort(zh);
         sz[0] = __half2float(sh);

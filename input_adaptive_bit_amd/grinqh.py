@@ -41,6 +41,31 @@ class Operands(ctypes.Structure):
                 ("s", ctypes.c_void_p), ("z", ctypes.c_void_p), ("y", ctypes.c_void_p)]
 
 
+class KVLayout(ctypes.Structure):
+    """Shape of one layer's key-value cache (grinqh_kv_layout_init)."""
+    _fields_ = [("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("bits", ctypes.c_int32), ("row_bytes", ctypes.c_int32)]
+
+    def __repr__(self):
+        return (f"KVLayout(n_kv_heads={self.n_kv_heads}, head_dim={self.head_dim}, page_size={self.page_size}, "
+                f"n_pages={self.n_pages}, bits={self.bits})")
+
+
+class KVPools(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("k_grid", ctypes.c_void_p),
+                ("v_grid", ctypes.c_void_p)]
+
+
+class PrefillAttentionArgs(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("cu_q", ctypes.c_void_p), ("cu_k", ctypes.c_void_p),
+                ("batch", ctypes.c_int32), ("total_q", ctypes.c_int32), ("total_k", ctypes.c_int32),
+                ("n_q_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("causal", ctypes.c_int32), ("scale", ctypes.c_float), ("out", ctypes.c_void_p),
+                ("out_dtype", ctypes.c_int), ("lse", ctypes.c_void_p)]
+
+
 MAX_GROUP = 8
 
 EXPORTS = ("grinqh_version", "grinqh_status_string", "grinqh_layout_init", "grinqh_packed_bytes",
@@ -48,7 +73,10 @@ EXPORTS = ("grinqh_version", "grinqh_status_string", "grinqh_layout_init", "grin
            "grinqh_gemv_group_workspace_bytes", "grinqh_gemv_group", "grinqh_debug_codes",
            "grinqh_debug_force_launch", "grinqh_gemv_noalloc",
            "grinqh_calibrate_workspace_bytes", "grinqh_calibrate_thresholds", "grinqh_quantize_rtn",
-           "grinqh_prefill_workspace_bytes", "grinqh_prefill_gemm")
+           "grinqh_prefill_workspace_bytes", "grinqh_prefill_gemm",
+           "grinqh_kv_layout_init", "grinqh_kv_code_bytes", "grinqh_kv_grid_bytes", "grinqh_kv_write",
+           "grinqh_kv_read", "grinqh_debug_kv_row", "grinqh_attention_workspace_bytes",
+           "grinqh_decode_attention", "grinqh_prefill_attention")
 
 _lib = None
 
@@ -109,6 +137,26 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.grinqh_prefill_workspace_bytes.restype = sz
     lib.grinqh_prefill_gemm.argtypes = [LP, vp, ctypes.c_int, i32, vp, vp, vp, vp, ctypes.c_int, vp, sz, vp]
     lib.grinqh_prefill_gemm.restype = ctypes.c_int
+    KP, PP, i64 = ctypes.POINTER(KVLayout), ctypes.POINTER(KVPools), ctypes.c_int64
+    lib.grinqh_kv_layout_init.argtypes = [i32, i32, i32, i32, i32, KP]
+    lib.grinqh_kv_layout_init.restype = ctypes.c_int
+    lib.grinqh_kv_code_bytes.argtypes = [KP]
+    lib.grinqh_kv_code_bytes.restype = sz
+    lib.grinqh_kv_grid_bytes.argtypes = [KP]
+    lib.grinqh_kv_grid_bytes.restype = sz
+    lib.grinqh_kv_write.argtypes = [KP, PP, vp, vp, ctypes.c_int, i64, i64, i32, vp, vp]
+    lib.grinqh_kv_write.restype = ctypes.c_int
+    lib.grinqh_kv_read.argtypes = [KP, PP, vp, i32, vp, vp, ctypes.c_int, vp]
+    lib.grinqh_kv_read.restype = ctypes.c_int
+    lib.grinqh_debug_kv_row.argtypes = [KP, i64, i32]
+    lib.grinqh_debug_kv_row.restype = i64
+    lib.grinqh_attention_workspace_bytes.argtypes = [KP, i32, i32, i32]
+    lib.grinqh_attention_workspace_bytes.restype = sz
+    lib.grinqh_decode_attention.argtypes = [KP, PP, vp, ctypes.c_int, i64, i32, vp, i64, i32, vp, i32, i32,
+                                            ctypes.c_float, vp, ctypes.c_int, vp, vp, sz, vp]
+    lib.grinqh_decode_attention.restype = ctypes.c_int
+    lib.grinqh_prefill_attention.argtypes = [ctypes.POINTER(PrefillAttentionArgs), vp]
+    lib.grinqh_prefill_attention.restype = ctypes.c_int
     if path is None:
         _lib = lib
     return lib

@@ -1,0 +1,245 @@
+"""The cache's and attention's oracle, addressing, host checks and binding
+refusals; no GPU (every library call here is host arithmetic or fails a host
+check, so no kernel is launched)."""
+
+import ctypes
+
+import numpy as np
+import pytest
+
+import input_adaptive_bit_amd as G
+from input_adaptive_bit_amd import grinqh as B
+from oracle import attention_oracle as A
+
+K64 = 1 << 16
+
+
+# --------------------------------------------------------------- the oracle --
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_cached_rows_are_the_nearest_midpoints(bits):
+    """Each value reads back as the midpoint of its interval: within half a
+    step of it, up to the grid's own rounding to fp16."""
+    rng = np.random.default_rng(bits)
+    w = rng.standard_normal((50, 64)).astype(np.float32)
+    stored, grid = A.quantise_rows(w, bits)
+    assert stored.shape == (50, 64 * bits // 8)
+    s = grid[:, :1].astype(np.float64)
+    lo, hi = w.min(1, keepdims=True).astype(np.float64), w.max(1, keepdims=True).astype(np.float64)
+    # half a step; z off by 2^-11 |lo|; s by 2^-11 s over 2^bits steps
+    slack = np.abs(lo) * 2.0 ** -11 + (hi - lo) * 2.0 ** -11
+    assert np.all(np.abs(A.row_values(stored, grid, bits) - w) <= s / 2 + slack)
+
+
+def test_four_bit_rows_hold_even_values_in_the_low_half():
+    w = np.arange(16, dtype=np.float32)[None] + 0.5
+    w[0, 0], w[0, 15] = 0.0, 16.0
+    stored, grid = A.quantise_rows(w, 4)
+    assert grid.tolist() == [[1.0, 0.0]]
+    assert stored[0].tolist() == [0x10, 0x32, 0x54, 0x76, 0x98, 0xBA, 0xDC, 0xFE]
+    assert A.codes_of(stored, 4)[0].tolist() == list(range(16))
+
+
+def test_sixteen_bit_rows_are_bf16():
+    w = np.array([[1.0, 1.00390625, -2.5, 3.0e38]], np.float32)
+    stored, grid = A.quantise_rows(w, 16)
+    assert grid is None and A.row_values(stored, None, 16)[0, :3].tolist() == [1.0, 1.0, -2.5]
+
+
+def test_attention_of_equal_scores_is_the_mean_and_of_one_token_its_value():
+    v = np.arange(12.0).reshape(4, 3)
+    o, lse, p = A.attend(np.zeros((2, 3)), np.ones((4, 3)), v, 1.0)
+    assert np.allclose(o, v.mean(0)) and np.allclose(lse, np.log(4)) and np.allclose(p, 0.25)
+    o, lse, _ = A.attend([[2.0]], [[3.0]], [[7.0]], 0.5)
+    assert o[0, 0] == 7.0 and lse[0] == 3.0
+
+
+def test_attention_matches_the_weighted_sum_written_out():
+    rng = np.random.default_rng(0)
+    q, k, v = rng.standard_normal((3, 5)), rng.standard_normal((6, 5)), rng.standard_normal((6, 5))
+    seen = A.causal_mask(3, 6)
+    o, lse, _ = A.attend(q, k, v, 0.7, seen)
+    for i in range(3):
+        w = [np.exp(0.7 * sum(q[i] * k[j])) for j in range(6) if j <= i + 3]
+        want = sum(x * v[j] for j, x in enumerate(w)) / sum(w)
+        assert np.allclose(o[i], want) and np.isclose(lse[i], np.log(sum(w)))
+
+
+def test_causal_mask_ends_at_the_last_key_and_leaves_rows_empty():
+    assert A.causal_mask(2, 4).tolist() == [[True, True, True, False], [True] * 4]
+    assert A.causal_mask(3, 1).tolist() == [[False], [False], [True]]
+    o, lse, _ = A.attend(np.ones((3, 2)), np.full((1, 2), np.nan), np.full((1, 2), np.nan), 1.0, np.zeros((3, 1), bool))
+    assert np.all(o == 0) and np.all(np.isneginf(lse))
+
+
+# --------------------------------------------------------------- addressing --
+
+@pytest.mark.parametrize("heads,page,n_pages", [(1, 16, 1), (8, 64, 1000), (5, 256, 1 << 24), (1024, 128, 70000)])
+def test_rows_of_slots(heads, page, n_pages):
+    """The row the kernels use, and -1 for every slot outside the pool; pools
+    of more than 2^32 rows among them."""
+    L = G.grinqh_kv_layout_init(heads, 128, page, n_pages, 8)
+    total = page * n_pages
+    rng = np.random.default_rng(page)
+    slots = [0, 1, page - 1, page, total - 1, total, total + 1, -1, -page, 2 ** 62, -2 ** 63, 2 ** 32, 2 ** 31 - 1]
+    slots += [int(x) for x in rng.integers(0, total, 200)]
+    for slot in slots:
+        for head in {0, heads // 2, heads - 1}:
+            want = A.row_index(slot, head, heads, page, n_pages)
+            assert G.grinqh_debug_kv_row(L, slot, head) == want
+            assert -1 <= want < heads * total
+    assert G.grinqh_debug_kv_row(L, 0, -1) == -1 and G.grinqh_debug_kv_row(L, 0, heads) == -1
+    rows = [G.grinqh_debug_kv_row(L, s, h) for s in range(min(total, 40)) for h in range(min(heads, 9))]
+    assert len(set(rows)) == len(rows)
+
+
+def test_layout_sizes():
+    L = G.grinqh_kv_layout_init(8, 128, 64, 10, 4)
+    assert (L.row_bytes, G.grinqh_kv_code_bytes(L), G.grinqh_kv_grid_bytes(L)) == (64, 10 * 8 * 64 * 64, 10 * 8 * 64 * 4)
+    L = G.grinqh_kv_layout_init(1, 256, 16, 1 << 24, 16)
+    assert (L.row_bytes, G.grinqh_kv_code_bytes(L), G.grinqh_kv_grid_bytes(L)) == (512, (1 << 28) * 512, 0)
+    bad = B.KVLayout(8, 128, 64, 10, 4, 63)
+    assert G.grinqh_kv_code_bytes(bad) == 0 and G.grinqh_kv_grid_bytes(bad) == 0
+    assert G.grinqh_debug_kv_row(bad, 0, 0) == -1
+
+
+@pytest.mark.parametrize("bad", [(0, 128, 64, 1, 8), (1025, 128, 64, 1, 8), (1, 96, 64, 1, 8), (1, 0, 64, 1, 8),
+                                 (1, 128, 8, 1, 8), (1, 128, 48, 1, 8), (1, 128, 512, 1, 8), (1, 128, 64, 0, 8),
+                                 (1, 128, 64, (1 << 24) + 1, 8), (1, 128, 64, 1, 2), (1, 128, 64, 1, 32),
+                                 (1, 1 << 30, 64, 1, 8), (1, 128, 64, 1, -8)])
+def test_layouts_outside_the_ranges_are_refused(bad):
+    with pytest.raises(G.GrinqhError):
+        G.grinqh_kv_layout_init(*bad)
+    assert B.load().grinqh_kv_layout_init(1, 128, 64, 1, 8, None) == B.GRINQH_EINVAL
+
+
+# -------------------------------------------------------------- host checks --
+
+def _pools(a=16):
+    return B.KVPools(a * K64 * 16, (a + 16) * K64 * 16, (a + 32) * K64 * 16, (a + 48) * K64 * 16)
+
+
+def test_cache_calls_check_their_arguments_before_any_device_call():
+    lib = G.load()
+    L = G.grinqh_kv_layout_init(2, 64, 16, 8, 8)
+    P = _pools()
+    K, V, S = K64, 2 * K64, 3 * K64
+
+    def write(L=L, P=P, k=K, v=V, dt=0, ks=128, vs=128, n=4, s=S):
+        return lib.grinqh_kv_write(None if L is None else ctypes.byref(L), None if P is None else ctypes.byref(P), k, v,
+                                   dt, ks, vs, n, s, None)
+
+    def read(L=L, P=P, k=K, v=V, dt=0, n=4, s=S):
+        return lib.grinqh_kv_read(None if L is None else ctypes.byref(L), None if P is None else ctypes.byref(P), s, n,
+                                  k, v, dt, None)
+
+    for call in (write, read):
+        for key in ("L", "P", "k", "v", "s"):
+            assert call(**{key: None}) == B.GRINQH_EINVAL, key
+        assert call(dt=2) == B.GRINQH_EINVAL
+        assert call(n=-1) == B.GRINQH_EINVAL and call(n=(1 << 24) + 1) == B.GRINQH_EINVAL
+        assert call(n=0) == B.GRINQH_OK                       # nothing to do, nothing launched
+        assert call(k=K + 8) == B.GRINQH_EALIGN and call(v=V + 2) == B.GRINQH_EALIGN
+        assert call(s=S + 4) == B.GRINQH_EALIGN
+        for field in ("k_codes", "v_codes", "k_grid", "v_grid"):
+            for value, status in ((None, B.GRINQH_EINVAL), (getattr(P, field) + 8, B.GRINQH_EALIGN)):
+                bad = B.KVPools(P.k_codes, P.v_codes, P.k_grid, P.v_grid)
+                setattr(bad, field, value)
+                assert call(P=bad) == status, field
+            assert call(k=getattr(P, field) + 64) == B.GRINQH_EINVAL, field      # overlaps the pool
+            assert call(v=getattr(P, field) + 64) == B.GRINQH_EINVAL, field
+        assert call(L=B.KVLayout(2, 64, 16, 8, 8, 63)) == B.GRINQH_EINVAL
+    for key in ("ks", "vs"):
+        assert write(**{key: 127}) == B.GRINQH_EINVAL                             # tokens would overlap
+        assert write(**{key: 132}) == B.GRINQH_EALIGN
+        assert write(**{key: (1 << 32) + 8}) == B.GRINQH_EINVAL
+        assert write(dt=1, **{key: 130}) == B.GRINQH_EALIGN
+    assert read(v=K + 512) == B.GRINQH_EINVAL                                     # outputs overlap
+
+
+def test_decode_attention_checks_its_arguments_before_any_device_call():
+    lib = G.load()
+    L = G.grinqh_kv_layout_init(2, 64, 16, 8, 8)
+    P = _pools()
+    Q, T, N, OUT, LSE, WS = (K64 * k for k in range(1, 7))
+
+    def call(L=L, P=P, q=Q, qd=0, qs=8 * 64, nq=8, t=T, ts=4, mp=4, n=N, b=3, ml=64, sc=0.1, o=OUT, od=0, lse=LSE,
+             ws=WS, wsb=1 << 40):
+        return lib.grinqh_decode_attention(None if L is None else ctypes.byref(L), None if P is None else ctypes.byref(P),
+                                           q, qd, qs, nq, t, ts, mp, n, b, ml, sc, o, od, lse, ws, wsb, None)
+
+    for key in ("L", "P", "q", "t", "n", "o", "ws"):
+        assert call(**{key: None}) == B.GRINQH_EINVAL, key
+    for key, value in (("qd", 3), ("od", -1), ("nq", 7), ("nq", 0), ("nq", 1026), ("mp", 0), ("ts", 3), ("b", -1),
+                       ("b", (1 << 20) + 1), ("ml", 0), ("ml", (1 << 28) + 1), ("sc", float("nan")),
+                       ("sc", float("inf")), ("qs", 8 * 64 - 8), ("qs", (1 << 32) + 8), ("o", Q + 64)):
+        assert call(**{key: value}) == B.GRINQH_EINVAL, (key, value)
+    for key, value in (("q", Q + 8), ("qs", 8 * 64 + 4), ("t", T + 2), ("n", N + 1), ("o", OUT + 8), ("lse", LSE + 2),
+                       ("ws", WS + 64)):
+        assert call(**{key: value}) == B.GRINQH_EALIGN, (key, value)
+    assert call(wsb=0) == B.GRINQH_ENOSPACE
+    assert call(b=0) == B.GRINQH_OK
+    for bad in (dict(n_q_heads=7), dict(batch=-1), dict(max_len=0), dict(L=B.KVLayout(2, 64, 16, 8, 8, 60))):
+        a = dict(dict(L=L, n_q_heads=8, batch=3, max_len=64), **bad)
+        assert G.grinqh_attention_workspace_bytes(**a) == 0
+    assert G.grinqh_attention_workspace_bytes(L, 8, 3, 64) % 256 == 0
+
+
+def test_prefill_attention_checks_its_arguments_before_any_device_call():
+    lib = G.load()
+    Q, K, V, CQ, CK, OUT, LSE = (K64 * 16 * k for k in range(1, 8))
+    good = dict(q=Q, k=K, v=V, q_stride=512, k_stride=128, v_stride=128, cu_q=CQ, cu_k=CK, batch=2, total_q=10,
+                total_k=12, n_q_heads=8, n_kv_heads=2, head_dim=64, causal=1, scale=0.1, out=OUT, out_dtype=0, lse=LSE)
+
+    def call(**kw):
+        return lib.grinqh_prefill_attention(ctypes.byref(B.PrefillAttentionArgs(**dict(good, **kw))), None)
+
+    assert lib.grinqh_prefill_attention(None, None) == B.GRINQH_EINVAL
+    for key in ("q", "k", "v", "cu_q", "cu_k", "out"):
+        assert call(**{key: None}) == B.GRINQH_EINVAL, key
+    for key, value in (("batch", -1), ("batch", (1 << 20) + 1), ("total_q", -1), ("total_q", (1 << 24) + 1),
+                       ("total_k", -1), ("total_k", (1 << 24) + 1), ("n_q_heads", 7), ("n_q_heads", 1026),
+                       ("n_kv_heads", 0), ("head_dim", 96), ("scale", float("nan")), ("out_dtype", 2),
+                       ("q_stride", 504), ("k_stride", 120), ("v_stride", 64), ("q_stride", (1 << 32) + 8),
+                       ("out", Q + 64), ("out", K + 64), ("out", V + 64)):
+        assert call(**{key: value}) == B.GRINQH_EINVAL, (key, value)
+    for key, value in (("q", Q + 8), ("k", K + 2), ("v", V + 4), ("cu_q", CQ + 2), ("cu_k", CK + 1), ("out", OUT + 8),
+                       ("lse", LSE + 1), ("q_stride", 516), ("k_stride", 132), ("v_stride", 129)):
+        assert call(**{key: value}) == B.GRINQH_EALIGN, (key, value)
+    assert call(total_q=0) == B.GRINQH_OK and call(batch=0) == B.GRINQH_OK
+
+
+def test_binding_refuses_host_tensors_and_wrong_shapes():
+    import torch
+    x = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    cu = torch.tensor([0, 4], dtype=torch.int32)
+    with pytest.raises(ValueError, match="GPU"):
+        G.prefill_attention(x, x, x, cu)
+    with pytest.raises(TypeError):
+        G.prefill_attention([1], x, x, cu)
+    L = G.grinqh_kv_layout_init(2, 64, 16, 8, 16)
+    pool = torch.zeros(G.grinqh_kv_code_bytes(L), dtype=torch.uint8)
+    with pytest.raises(ValueError, match="GPU"):
+        G.KVCache(L, pool, pool)
+    with pytest.raises(G.GrinqhError):
+        G.KVCache(B.KVLayout(2, 64, 16, 8, 16, 1), pool, pool)
+    with pytest.raises(G.GrinqhError):
+        G.new_attention_workspace(L, 3, 1, 10)
+
+
+def test_binding_takes_the_stride_of_a_token_and_refuses_other_views():
+    import torch
+    from input_adaptive_bit_amd import attention as N
+    device = torch.device("cpu")
+    orig, N._tensor = N._tensor, lambda t, name, device=None: t.device
+    try:
+        fused = torch.zeros(5, 12, 64)
+        assert N._rows(fused[:, 8:10], "k", 2, 64, device) == 12 * 64
+        assert N._rows(fused[:1, 8:10], "k", 2, 64, device) == 2 * 64        # one token has no next
+        assert N._rows(torch.zeros(5, 1, 64).transpose(0, 1).transpose(0, 1), "k", 1, 64, device) == 64
+        assert N._rows(torch.zeros(0, 2, 64), "k", 2, 64, device) == 128
+        for bad in (fused.transpose(1, 2), fused[:, ::2], fused[..., ::2], torch.zeros(1, 2, 64).expand(5, 2, 64)):
+            with pytest.raises(ValueError):
+                N._rows(bad, "k", bad.shape[1], bad.shape[2], device)
+    finally:
+        N._tensor = orig

@@ -1,0 +1,450 @@
+"""GPU parity of decode_attention and prefill_attention with the fp64 oracle;
+bounds from the roundings the calls document (tests/attention_util.py)."""
+
+import numpy as np
+import pytest
+
+from oracle import attention_oracle as A
+from tests.attention_util import Cache, decode_reference, inside, prefill_reference, rows, to_bf16, to_type
+from tests.gpu_util import require_gpu, say
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dev():
+    import input_adaptive_bit_amd as G
+    G.load()
+    return require_gpu()
+
+
+def _dt(name):
+    import torch
+    return torch.bfloat16 if name == "bf16" else torch.float32
+
+
+def _np(t):
+    return t.float().cpu().numpy()
+
+
+def _decode(c, q, q_dtype, out_dtype, dev, max_len=None, scale=None, lens=None, workspace=None, what=""):
+    import input_adaptive_bit_amd as G
+    import torch
+    scale = c.dim ** -0.5 if scale is None else scale
+    out, lse = G.decode_attention(c.dev, to_type(q, q_dtype, dev), c.dev_table, c.dev_lens, max_len, scale,
+                                  _dt(out_dtype), True, workspace)
+    torch.cuda.synchronize()
+    o, bound, l, l_bound = decode_reference(c, q, scale, out_dtype, lens)
+    inside(_np(out), o, bound, what + " out")
+    inside(_np(lse), l, l_bound, what + " lse")
+    return out
+
+
+def _queries(rng, batch, n_q, dim, q_dtype):
+    q = rng.standard_normal((batch, n_q, dim)).astype(np.float32)
+    return A.bf16(q) if q_dtype == "bf16" else q
+
+
+# ------------------------------------------------------------------- decode --
+
+@pytest.mark.parametrize("bits", [4, 8, 16])
+@pytest.mark.parametrize("heads,group,dim,page,lens", [
+    (8, 4, 128, 64, [500]),
+    (2, 1, 64, 16, [1, 2, 15, 16, 17, 31, 32, 33, 0]),
+    (1, 7, 128, 32, [127, 128, 129, 0, 1]),
+    (3, 8, 256, 128, [255, 257, 64]),
+    (2, 16, 64, 256, [300, 5]),
+    (1, 24, 128, 16, [100, 65]),
+    (1, 64, 64, 32, [70]),
+    (5, 2, 128, 16, [63, 64, 65, 191, 193]),
+])
+def test_decode_matches_the_oracle(dev, bits, heads, group, dim, page, lens):
+    say(f"decode bits={bits} heads={heads}x{group} dim={dim} page={page} lens={lens}")
+    rng = np.random.default_rng(heads * 100 + group + dim + bits)
+    c = Cache(rng, lens, heads, dim, bits, page, dev)
+    for q_dtype, out_dtype in (("bf16", "bf16"), ("f32", "f32")):
+        _decode(c, _queries(rng, len(lens), heads * group, dim, q_dtype), q_dtype, out_dtype, dev)
+
+
+@pytest.mark.parametrize("bits,heads,group,dim,page,n", [(8, 2, 4, 128, 64, 20011), (4, 1, 8, 128, 128, 30001),
+                                                         (16, 1, 2, 64, 16, 9000), (8, 1, 3, 256, 32, 5003)])
+def test_decode_over_a_long_cache(dev, bits, heads, group, dim, page, n):
+    """One sequence, many parts, joined."""
+    say(f"decode long bits={bits} n={n}")
+    rng = np.random.default_rng(n)
+    c = Cache(rng, [n], heads, dim, bits, page, dev)
+    q = _queries(rng, 1, heads * group, dim, "bf16")
+    first = _decode(c, q, "bf16", "f32", dev)
+    _decode(c, q, "bf16", "f32", dev, max_len=n)
+    import torch
+    assert torch.equal(first, _decode(c, q, "bf16", "f32", dev)), "the same call twice, the same bits"
+
+
+def test_decode_of_many_sequences_of_very_different_lengths(dev):
+    rng = np.random.default_rng(8)
+    lens = [int(x) for x in rng.integers(0, 700, 40)] + [3001, 0, 1]
+    c = Cache(rng, lens, 2, 64, 8, 32, dev)
+    _decode(c, _queries(rng, len(lens), 6, 64, "bf16"), "bf16", "bf16", dev)
+
+
+@pytest.mark.parametrize("bits", [4, 8, 16])
+def test_absent_pages_are_not_seen(dev, bits):
+    """Entries below 0 or past the pool, at the start, inside and at the end;
+    one sequence has no page at all."""
+    import torch
+    rng = np.random.default_rng(bits)
+    c = Cache(rng, [100, 70, 90, 16, 400], 2, 64, bits, 16, dev)
+    c.table[0, [0, 3, 6]] = [-1, c.n_pages, 2 ** 31 - 1]
+    c.table[1, 4] = -2 ** 31
+    c.table[2, :3] = -5
+    c.table[3, 0] = c.n_pages + 100
+    c.table[4, 5:20] = -1
+    c.dev_table.copy_(torch.from_numpy(c.table))
+    out = _decode(c, _queries(rng, 5, 4, 64, "bf16"), "bf16", "f32", dev)
+    assert not out[3].any()
+
+
+def test_lengths_outside_the_host_bound_are_clamped(dev):
+    import torch
+    rng = np.random.default_rng(1)
+    c = Cache(rng, [96, 96, 96, 96], 2, 64, 8, 32, dev)
+    q = _queries(rng, 4, 4, 64, "bf16")
+    c.dev_lens.copy_(torch.tensor([-3, 2 ** 31 - 1, 50, -2 ** 31]))
+    _decode(c, q, "bf16", "f32", dev, max_len=96, lens=[0, 96, 50, 0])
+    _decode(c, q, "bf16", "f32", dev, max_len=40, lens=[0, 40, 40, 0])
+    _decode(c, q, "bf16", "f32", dev, max_len=1 << 28, lens=[0, 96, 50, 0])       # the page table ends at 96
+
+
+def test_decode_scales_and_extreme_scores(dev):
+    """No, negative and very large scales: equal weights, one weight alone."""
+    rng = np.random.default_rng(2)
+    c = Cache(rng, [300, 33], 1, 128, 8, 64, dev)
+    q = _queries(rng, 2, 5, 128, "bf16")
+    for scale in (0.0, -0.05, 1e-20, 30.0, 1e4):
+        _decode(c, q, "bf16", "f32", dev, scale=scale, what=f"scale {scale}")
+    _decode(c, A.bf16(q * 100), "bf16", "f32", dev)
+
+
+def test_queries_are_slices_of_a_fused_projection_and_the_table_is_wider(dev):
+    import input_adaptive_bit_amd as G
+    import torch
+    rng = np.random.default_rng(4)
+    c = Cache(rng, [100, 37, 64], 2, 128, 8, 32, dev)
+    fused = rows(rng, 3, 6 + 4, 128)
+    t = to_bf16(fused, dev)
+    wide = torch.full((3, 50), -1, dtype=torch.int32, device=dev)
+    wide[:, 7:7 + c.table.shape[1]] = c.dev_table
+    out = G.decode_attention(c.dev, t[:, :6], wide[:, 7:7 + c.table.shape[1]], c.dev_lens, 100,
+                             out_dtype=torch.float32)
+    o, bound, _, _ = decode_reference(c, fused[:, :6], 128 ** -0.5, "f32")
+    inside(_np(out), o, bound)
+
+
+def test_what_is_not_finite_in_unseen_tokens_has_no_effect_and_in_seen_ones_stays_in_its_head(dev):
+    """The Cache helper fills every unused row with NaN; here a seen row of one
+    head is NaN too."""
+    import input_adaptive_bit_amd as G
+    import torch
+    for bits in (8, 16):
+        rng = np.random.default_rng(6)
+        c = Cache(rng, [77], 3, 64, bits, 32, dev)
+        q = _queries(rng, 1, 6, 64, "bf16")
+        base = _decode(c, q, "bf16", "f32", dev)
+        page, t = c.row(0, 40)
+        if bits == 16:
+            c.dev.v_codes[page, 1, t] = 0xFF
+        else:
+            c.dev.v_grid[page, 1, t] = float("nan")
+        out = G.decode_attention(c.dev, to_bf16(q, dev), c.dev_table, c.dev_lens, out_dtype=torch.float32)
+        assert torch.isnan(out[0, 2:4]).all()
+        assert torch.equal(out[0, :2], base[0, :2]) and torch.equal(out[0, 4:], base[0, 4:])
+
+
+def test_one_workspace_for_calls_of_different_sizes_and_in_two_graphs(dev):
+    import input_adaptive_bit_amd as G
+    import torch
+    rng = np.random.default_rng(12)
+    a = Cache(rng, [5000, 17], 2, 128, 8, 64, dev)
+    b = Cache(rng, [900] * 7, 1, 64, 4, 16, dev)
+    ws = torch.zeros(max(G.grinqh_attention_workspace_bytes(a.dev.layout, 8, 2, 5000),
+                         G.grinqh_attention_workspace_bytes(b.dev.layout, 5, 7, 912)), dtype=torch.uint8, device=dev)
+    qa, qb = _queries(rng, 2, 8, 128, "bf16"), _queries(rng, 7, 5, 64, "bf16")
+    for _ in range(3):
+        _decode(a, qa, "bf16", "f32", dev, workspace=ws, max_len=5000)
+        _decode(b, qb, "bf16", "f32", dev, workspace=ws)
+    graphs = []
+    for c, q in ((a, qa), (b, qb)):
+        q_dev = to_bf16(q, dev)
+        out = torch.empty(q.shape, dtype=torch.float32, device=dev)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            G.grinqh_decode_attention(c.dev, q_dev, c.dev_table, c.dev_lens, c.table.shape[1] * c.page, out, ws)
+        graphs.append((c, q_dev, out, g))
+    for turn in range(4):
+        for c, q_dev, out, g in graphs:
+            q = _queries(rng, *out.shape, "bf16")
+            q_dev.copy_(to_bf16(q, dev))
+            lens = [max(0, n - 13 * turn) for n in c.lens]
+            c.dev_lens.copy_(torch.tensor(lens))
+            out.fill_(float("nan"))
+            g.replay()
+            torch.cuda.synchronize()
+            o, bound, _, _ = decode_reference(c, q, c.dim ** -0.5, "f32", lens)
+            inside(_np(out), o, bound, f"turn {turn}")
+
+
+def test_decode_on_another_stream(dev):
+    import input_adaptive_bit_amd as G
+    import torch
+    rng = np.random.default_rng(13)
+    c = Cache(rng, [3000], 2, 64, 8, 64, dev)
+    q = _queries(rng, 1, 4, 64, "bf16")
+    q_dev = to_bf16(q, dev)
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    out = G.decode_attention(c.dev, q_dev, c.dev_table, c.dev_lens, out_dtype=torch.float32, stream=other)
+    other.synchronize()
+    o, bound, _, _ = decode_reference(c, q, 0.125, "f32")
+    inside(_np(out), o, bound)
+
+
+def test_decode_reads_pages_past_four_gigabytes(dev):
+    import input_adaptive_bit_amd as G
+    import torch
+    heads, dim, page, n_pages = 8, 256, 256, 4400
+    c = G.new_kv_cache(heads, dim, page, n_pages, 16, dev)
+    table = torch.tensor([[n_pages - 1, 4096, 0, n_pages - 2]], dtype=torch.int32, device=dev)
+    g = torch.Generator(device=dev).manual_seed(2)
+    kv = torch.randn(2, 900, heads, dim, generator=g, device=dev).bfloat16()
+    at = torch.arange(900, device=dev)
+    G.kv_write(c, kv[0], kv[1], table[0].long()[at // page] * page + at % page)
+    q = _queries(np.random.default_rng(0), 1, heads, dim, "bf16")
+    out = G.decode_attention(c, to_bf16(q, dev), table, torch.tensor([900], dtype=torch.int32, device=dev),
+                             out_dtype=torch.float32)
+    k, v = (x.float().cpu().numpy() for x in kv)
+    o, bound, _, _ = prefill_reference(q, k, v, [0, 1], [0, 900], dim ** -0.5, False, "f32")
+    inside(_np(out), o, bound)
+
+
+def test_no_sequences(dev):
+    import input_adaptive_bit_amd as G
+    import torch
+    c = G.new_kv_cache(2, 64, 16, 1, 8, dev)
+    out = G.decode_attention(c, torch.zeros(0, 4, 64, dtype=torch.bfloat16, device=dev),
+                             torch.zeros(0, 3, dtype=torch.int32, device=dev),
+                             torch.zeros(0, dtype=torch.int32, device=dev))
+    assert out.shape == (0, 4, 64)
+
+
+# ------------------------------------------------------------------ prefill --
+
+def _packed(rng, n_q, n_kv, dim, lens_q, lens_k, extra=0):
+    cu_q, cu_k = np.concatenate([[0], np.cumsum(lens_q)]), np.concatenate([[0], np.cumsum(lens_k)])
+    q, k, v = rows(rng, cu_q[-1] + extra, n_q, dim), rows(rng, cu_k[-1] + extra, n_kv, dim), \
+        rows(rng, cu_k[-1] + extra, n_kv, dim)
+    return q, k, v, cu_q.astype(np.int32), cu_k.astype(np.int32)
+
+
+def _prefill(q, k, v, cu_q, cu_k, dev, causal=True, out_dtype="bf16", scale=None, what=""):
+    import input_adaptive_bit_amd as G
+    import torch
+    scale = q.shape[2] ** -0.5 if scale is None else scale
+    out = torch.full(q.shape, 7.5, dtype=_dt(out_dtype), device=dev)
+    lse = torch.full(q.shape[:2], 7.5, dtype=torch.float32, device=dev)
+    G.grinqh_prefill_attention(to_bf16(q, dev), to_bf16(k, dev), to_bf16(v, dev), torch.from_numpy(cu_q).to(dev),
+                               torch.from_numpy(cu_k).to(dev), out, causal, scale, lse)
+    torch.cuda.synchronize()
+    o, bound, l, l_bound = prefill_reference(q, k, v, cu_q, cu_k, scale, causal, out_dtype)
+    n = cu_q[-1]
+    inside(_np(out)[:n], o[:n], bound[:n], what + " out")
+    inside(_np(lse)[:n], l[:n], l_bound[:n], what + " lse")
+    assert bool((out[n:] == 7.5).all()) and bool((lse[n:] == 7.5).all()), "rows behind the last sequence"
+    return out
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("n_kv,group,dim,lens", [
+    (2, 4, 128, [130]),
+    (1, 1, 64, [1]),
+    (2, 2, 64, [1, 2, 31, 32, 33, 63, 64, 65]),
+    (1, 7, 128, [127, 128, 129, 0, 5]),
+    (3, 1, 256, [255, 100, 1]),
+    (2, 3, 128, [300, 0, 0, 17, 257]),
+    (1, 5, 64, [513]),
+    (1, 2, 256, [385]),
+])
+def test_prefill_matches_the_oracle(dev, causal, n_kv, group, dim, lens):
+    say(f"prefill heads={n_kv}x{group} dim={dim} lens={lens} causal={causal}")
+    rng = np.random.default_rng(sum(lens) + dim + group)
+    args = _packed(rng, n_kv * group, n_kv, dim, lens, lens)
+    for out_dtype in ("bf16", "f32"):
+        _prefill(*args, dev, causal, out_dtype)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dim,lens_q,lens_k", [
+    (64, [5, 130, 1], [300, 131, 1000]),          # cached beginnings
+    (128, [64, 1, 200], [640, 65, 329]),
+    (128, [100, 7, 40], [30, 0, 40]),             # fewer keys than queries: rows that see nothing
+    (256, [33, 70], [200, 3]),
+    (64, [0, 3, 0], [50, 3, 0]),                  # keys without queries
+])
+def test_prefill_with_other_numbers_of_keys_than_queries(dev, causal, dim, lens_q, lens_k):
+    say(f"prefill dim={dim} q={lens_q} k={lens_k} causal={causal}")
+    rng = np.random.default_rng(sum(lens_k) + dim)
+    _prefill(*_packed(rng, 4, 2, dim, lens_q, lens_k), dev, causal, "f32")
+
+
+def test_rows_behind_the_last_sequence_and_batches_of_many(dev):
+    rng = np.random.default_rng(3)
+    _prefill(*_packed(rng, 2, 1, 64, [3, 50], [3, 50], extra=150), dev)
+    lens = [int(x) for x in rng.integers(0, 20, 150)]              # more sequences than a wave has lanes
+    _prefill(*_packed(rng, 2, 1, 64, lens, lens), dev)
+    lens = [1] * 300 + [140]
+    _prefill(*_packed(rng, 1, 1, 64, lens, lens), dev)
+
+
+def test_prefill_scales_and_extreme_scores(dev):
+    rng = np.random.default_rng(4)
+    args = _packed(rng, 2, 1, 128, [150], [150])
+    for scale in (0.0, -0.05, 1e-20, 30.0, 1e4):
+        _prefill(*args, dev, True, "f32", scale, f"scale {scale}")
+    q, k, v, cu_q, cu_k = args
+    _prefill(A.bf16(q * 100), k, v, cu_q, cu_k, dev, True, "f32")
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_keys_that_are_not_seen_may_be_anything(dev, dim):
+    """NaN and infinities in later keys, other sequences and rows behind the
+    last: the queries that do not see them are those of a call without."""
+    import input_adaptive_bit_amd as G
+    import torch
+    rng = np.random.default_rng(5)
+    q, k, v, cu_q, cu_k = _packed(rng, 2, 1, dim, [200, 90], [200, 90], extra=70)
+    base = _prefill(q, k, v, cu_q, cu_k, dev, True, "f32")
+    for bad in (np.nan, np.inf, -np.inf):
+        k2, v2 = k.copy(), v.copy()
+        k2[150:200], v2[150:200], k2[290:], v2[290:] = bad, bad, bad, bad
+        out = G.prefill_attention(to_bf16(q, dev), to_bf16(k2, dev), to_bf16(v2, dev), torch.from_numpy(cu_q).to(dev),
+                                  torch.from_numpy(cu_k).to(dev), out_dtype=torch.float32)
+        assert torch.equal(out[:150], base[:150]) and torch.equal(out[200:290], base[200:290])
+        if bad is np.nan:
+            assert torch.isnan(out[150:200]).all()
+
+
+def test_prefill_takes_slices_of_a_fused_projection(dev):
+    import input_adaptive_bit_amd as G
+    import torch
+    rng = np.random.default_rng(6)
+    lens = [100, 33]
+    fused = rows(rng, 133, 6 + 2 * 2, 128)
+    t = to_bf16(fused, dev)
+    cu = torch.tensor([0, 100, 133], dtype=torch.int32, device=dev)
+    out, lse = G.prefill_attention(t[:, :6], t[:, 6:8], t[:, 8:], cu, return_lse=True)
+    o, bound, l, l_bound = prefill_reference(fused[:, :6], fused[:, 6:8], fused[:, 8:], [0, 100, 133], [0, 100, 133],
+                                             128 ** -0.5, True, "bf16")
+    inside(_np(out), o, bound)
+    inside(_np(lse), l, l_bound)
+
+
+def test_sequence_bounds_outside_the_rows_are_clamped(dev):
+    """Entries past the packed rows are taken as their end, so nothing outside
+    the tensors is read or written."""
+    import input_adaptive_bit_amd as G
+    import torch
+    rng = np.random.default_rng(7)
+    q, k, v, _, _ = _packed(rng, 2, 1, 64, [100], [100])
+    t = [to_bf16(x, dev) for x in (q, k, v)]
+    cu = torch.tensor([0, 40, 2 ** 31 - 1], dtype=torch.int32, device=dev)
+    out = G.prefill_attention(*t, cu, out_dtype=torch.float32)
+    o, bound, _, _ = prefill_reference(q, k, v, [0, 40, 100], [0, 40, 100], 0.125, True, "f32")
+    inside(_np(out), o, bound)
+
+
+def test_prefill_in_a_graph_and_on_another_stream(dev):
+    import input_adaptive_bit_amd as G
+    import torch
+    rng = np.random.default_rng(8)
+    q, k, v, cu_q, cu_k = _packed(rng, 4, 2, 128, [140, 60], [140, 60])
+    t = [to_bf16(x, dev) for x in (q, k, v)]
+    cu = torch.from_numpy(cu_q).to(dev)
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    out = G.prefill_attention(*t, cu, out_dtype=torch.float32, stream=other)
+    other.synchronize()
+    o, bound, _, _ = prefill_reference(q, k, v, cu_q, cu_k, 128 ** -0.5, True, "f32")
+    inside(_np(out), o, bound)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        G.grinqh_prefill_attention(*t, cu, cu, out)
+    for cut in (140, 1, 77, 199):
+        cu.copy_(torch.tensor([0, cut, 200]))
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        o, bound, _, _ = prefill_reference(q, k, v, [0, cut, 200], [0, cut, 200], 128 ** -0.5, True, "f32")
+        inside(_np(out), o, bound, f"cut {cut}")
+
+
+def test_no_rows(dev):
+    import input_adaptive_bit_amd as G
+    import torch
+    none = torch.zeros(0, 2, 64, dtype=torch.bfloat16, device=dev)
+    cu = torch.zeros(3, dtype=torch.int32, device=dev)
+    assert G.prefill_attention(none, none, none, cu).shape == (0, 2, 64)
+    q = torch.ones(4, 2, 64, dtype=torch.bfloat16, device=dev)
+    out = G.prefill_attention(q, none, none, torch.tensor([0, 1, 4], dtype=torch.int32, device=dev), cu)
+    assert not out.any()
+
+
+# ----------------------------------------------------------------- together --
+
+@pytest.mark.parametrize("bits", [4, 8, 16])
+def test_a_conversation(dev, bits):
+    """A prompt, some tokens and a second prompt through one cache, as a decoder
+    runs them: every token's output is that of attention over the whole text
+    (its own keys in full during its prompt, the cached ones otherwise)."""
+    import input_adaptive_bit_amd as G
+    import torch
+    rng = np.random.default_rng(bits)
+    n_q, n_kv, dim, page = 8, 2, 128, 16
+    prompt, steps, second = 150, 20, 45
+    total = prompt + steps + second
+    fused = rows(rng, total, n_q + 2 * n_kv, dim)
+    t = to_bf16(fused, dev)
+    q, k, v = t[:, :n_q], t[:, n_q:n_q + n_kv], t[:, n_q + n_kv:]
+    n_pages = -(-total // page)
+    c = G.new_kv_cache(n_kv, dim, page, n_pages + 2, bits, dev)
+    table = torch.randperm(n_pages + 2, device=dev)[:n_pages].int()[None]
+    at = torch.arange(total, device=dev)
+    slots = table[0].long()[at // page] * page + at % page
+    ws = G.new_attention_workspace(c.layout, n_q, 1, total, dev)
+    got = torch.empty(total, n_q, dim, device=dev)
+
+    cu = torch.tensor([0, prompt], dtype=torch.int32, device=dev)
+    got[:prompt] = G.prefill_attention(q[:prompt], k[:prompt], v[:prompt], cu, out_dtype=torch.float32)
+    G.kv_write(c, k[:prompt], v[:prompt], slots[:prompt])
+    for i in range(prompt, prompt + steps):
+        G.kv_write(c, k[i:i + 1], v[i:i + 1], slots[i:i + 1])
+        got[i] = G.decode_attention(c, q[i:i + 1], table, torch.tensor([i + 1], dtype=torch.int32, device=dev), total,
+                                    out_dtype=torch.float32, workspace=ws)[0]
+    past = prompt + steps
+    old_k, old_v = G.kv_read(c, slots[:past])
+    got[past:] = G.prefill_attention(q[past:], torch.cat([old_k, k[past:]]), torch.cat([old_v, v[past:]]),
+                                     torch.tensor([0, second], dtype=torch.int32, device=dev),
+                                     torch.tensor([0, total], dtype=torch.int32, device=dev), out_dtype=torch.float32)
+    torch.cuda.synchronize()
+
+    def cached(x):
+        return A.row_values(*A.quantise_rows(x, bits), bits).astype(np.float32)
+
+    qf, kf, vf = fused[:, :n_q], fused[:, n_q:n_q + n_kv], fused[:, n_q + n_kv:]
+    o, bound, _, _ = prefill_reference(qf[:prompt], kf[:prompt], vf[:prompt], [0, prompt], [0, prompt], dim ** -0.5, True,
+                                       "f32")
+    inside(_np(got[:prompt]), o, bound, "prompt")
+    kc, vc = cached(kf[:past]), cached(vf[:past])
+    o, bound, _, _ = prefill_reference(qf[prompt:past], kc, vc, [0, steps], [0, past], dim ** -0.5, True, "f32")
+    inside(_np(got[prompt:past]), o, bound, "tokens")
+    kc, vc = np.concatenate([A.bf16(kc), kf[past:]]), np.concatenate([A.bf16(vc), vf[past:]])
+    o, bound, _, _ = prefill_reference(qf[past:], kc, vc, [0, second], [0, total], dim ** -0.5, True, "f32")
+    inside(_np(got[past:]), o, bound, "second prompt")
