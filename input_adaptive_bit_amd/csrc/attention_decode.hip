@@ -3,16 +3,55 @@
 // For query head h with key-value head g = h / group,
 //   o = sum_t p_t v_t,  p_t = exp(a_t - m) / l,  a_t = scale * q . k_t.
 //
-// One wave per (sequence, query head) walks the tokens 64 at a time with the
-// running maximum m and sum l: a lane forms one token's score, then every
-// lane owns D / 64 values of the output and adds the 64 tokens' values to them.
+// One pass over the cache with a running maximum and sum, on the bf16 matrix
+// cores.  A workgroup of four waves takes one part of one sequence's tokens for
+// up to 16 query heads of one key-value head; its waves take tiles of 32 tokens
+// in turn, each with its own maximum, sum and output, joined at the end.
+//
+// Scores.  S = K Q^T as 16 tokens x 16 heads (v_mfma_f32_16x16x32_bf16).  Any
+// order of the head's dimensions serves as the contraction's as long as K and
+// Q agree, so a lane loads its token's row in 16-byte pieces as they lie and
+// Q is laid out to match.  Keys enter as their integer codes (exact in bf16):
+// q . k = s (sum q c + sum q / 2) + z sum q.
+//
+// Values.  O^T = V^T P^T as 16 dimensions x 16 heads over the 32 tokens.  The
+// lane that holds a head's scores of 8 tokens (rows 4 g .. 4 g + 3 of both score
+// tiles, g = lane / 16) takes just these tokens as its share of the contraction,
+// so the weights never leave their lane; and any dimension may stand for a row
+// of the product, so a lane loads D / 16 neighbouring dimensions of its 8 tokens
+// and has the transposed operand in its own registers.  The codes' scale goes
+// into the weights, p' = p s, and
+//   sum p v = sum p' (c - mid) + sum p (z + s (mid + 1/2)),
+// with the products sum p' c - mid sum p' (mid = 2^(bits - 1): the rounding of
+// p' then weighs the distance from the grid's middle only).  p' (p at 16 bits)
+// is used as the sum of two bf16, a relative error of 2^-16: the matrix cores
+// have the time, and outputs keep the precision of fp32 weights.
+//
+// Long caches are cut into parts (plan_decode); each part's output, maximum
+// and sum go to the workspace and the part that arrives last joins them in
+// their order.
 #include <math.h>
+
+#include <algorithm>
 
 #include "internal.h"
 #include "kv_common.hpp"
 
 namespace grinqh {
 namespace {
+
+constexpr int kTileTokens = 32;                        // tokens of a wave's tile
+constexpr int kBatch = 16;                             // parts joined at a time
+constexpr int kHeadTile = 16;                          // query heads of a workgroup
+constexpr int64_t kMaxDecodeGroups = 1 << 23;          // workgroups of a launch
+constexpr int kCounters = 4096;                        // arrival counters at the start of the workspace
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 struct DecodeArgs {
     KvDims d;
@@ -25,92 +64,620 @@ struct DecodeArgs {
     const int32_t* seq_lens;
     void* out;
     float* lse;
+    unsigned* counters;
+    float* parts;            // [item][split][heads_here][D], then the statistics
     int64_t q_stride, table_stride;
-    int n_q_heads, group, longest, q_dtype, out_dtype;   // longest: min(max_len, max_pages * page_size)
-    float scale;
+    int n_q_heads, group, head_tiles, items, splits, chunk, max_pages;
+    int longest;             // min(max_len, max_pages * page_size)
+    int q_dtype, out_dtype;
+    float scale_log2;        // scale * log2(e): exponents are of base 2
 };
 
-template <int BITS>
-__device__ __forceinline__ float cached(const uint8_t* codes, float s, float z, int d) {
-    if constexpr (BITS == 16) return bf16_to_f32(reinterpret_cast<const uint16_t*>(codes)[d]);
-    const int c = BITS == 8 ? codes[d] : (codes[d >> 1] >> (4 * (d & 1))) & 15;
-    return __builtin_fmaf(s, static_cast<float>(c) + 0.5f, z);
+// Bytes at p, `N` a power of two, as dwords (16 bits in the low half for N = 2).
+template <int N>
+__device__ __forceinline__ void load_bytes(const uint8_t* p, uint32_t* r) {
+    if constexpr (N == 2) {
+        r[0] = *reinterpret_cast<const uint16_t*>(p);
+    } else if constexpr (N == 4) {
+        r[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else if constexpr (N == 8) {
+        const u32x2 v = *reinterpret_cast<const u32x2*>(p);
+        r[0] = v.x;
+        r[1] = v.y;
+    } else {
+#pragma unroll
+        for (int n = 0; n < N / 16; ++n) {
+            const u32x4 v = reinterpret_cast<const u32x4*>(p)[n];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r[4 * n + i] = v[i];
+        }
+    }
 }
 
 template <int D, int BITS>
-__global__ __launch_bounds__(kWave) void decode_kernel(DecodeArgs a) {
-    constexpr int kRow = D * BITS / 8, kOwn = D / kWave;
-    const int64_t item = blockIdx.x;
-    const int b = static_cast<int>(item / a.n_q_heads), h = static_cast<int>(item % a.n_q_heads), g = h / a.group;
-    const int lane = threadIdx.x;
-    __shared__ float qs[D], ps[kWave];
-    __shared__ int64_t rows[kWave];
-    const int64_t q0 = b * a.q_stride + static_cast<int64_t>(h) * D;
-    for (int d = lane; d < D; d += kWave)
-        qs[d] = a.q_dtype == GRINQH_BF16 ? bf16_to_f32(static_cast<const uint16_t*>(a.q)[q0 + d])
-                                         : static_cast<const float*>(a.q)[q0 + d];
-    __syncthreads();
+struct Shape {
+    static constexpr int kRow = D * BITS / 8;                        // bytes of a row
+    static constexpr int kKBytes = kRow / 4;                         // of a key row in one lane
+    static constexpr int kPiece = kKBytes < 16 ? kKBytes : 16;       // loaded at a time
+    static constexpr int kPieces = kKBytes / kPiece;
+    static constexpr int kPerPiece = kPiece * 8 / BITS;              // dimensions of a piece
+    static constexpr int kSteps = D / 32;                            // contraction steps of a score tile
+    static constexpr int kVBytes = kRow / 16;                        // of a value row in one lane
+    static constexpr int kVDwords = kVBytes < 4 ? 1 : kVBytes / 4;
+    static constexpr int kVDims = D / 16;
+};
+
+// A wave's 32 tokens as loaded: keys of two score tiles, values of this lane's
+// 8 tokens, grids of the same 8 tokens.
+template <int D, int BITS>
+struct Tile {
+    uint32_t k[2][D * BITS / 128];
+    uint32_t v[8][Shape<D, BITS>::kVDwords];
+    u32x4 kg[2], vg[2];
+};
+
+// Row of the first token of each half of the tile at t0 (pages that are not
+// there read page 0, and nothing of it is used).
+__device__ __forceinline__ void tile_rows(int64_t (&row)[2], const DecodeArgs& a, int t0, const int (&page)[2], int head) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        row[h] = ((static_cast<int64_t>(max(page[h], 0)) * a.d.heads + head) << a.d.page_shift) +
+                 ((t0 + 16 * h) & ((1 << a.d.page_shift) - 1));
+}
+
+template <int D, int BITS>
+__device__ __forceinline__ void load_keys(Tile<D, BITS>& T, const DecodeArgs& a, const int64_t (&row)[2], int lane) {
+    using S = Shape<D, BITS>;
+    const int i = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint8_t* k = a.k_codes + row[h] * S::kRow;
+#pragma unroll
+        for (int n = 0; n < S::kPieces; ++n)
+            load_bytes<S::kPiece>(k + static_cast<uint32_t>(i * S::kRow + (4 * n + g) * S::kPiece),
+                                  &T.k[h][n * S::kPiece / 4]);
+        if constexpr (BITS < 16) T.kg[h] = *reinterpret_cast<const u32x4*>(a.k_grid + row[h] * 2 + 8 * g);
+    }
+}
+
+template <int D, int BITS>
+__device__ __forceinline__ void load_values(Tile<D, BITS>& T, const DecodeArgs& a, const int64_t (&row)[2], int lane) {
+    using S = Shape<D, BITS>;
+    const int i = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint8_t* v = a.v_codes + row[h] * S::kRow;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            load_bytes<S::kVBytes>(v + static_cast<uint32_t>((4 * g + j) * S::kRow + i * S::kVBytes), T.v[4 * h + j]);
+        if constexpr (BITS < 16) T.vg[h] = *reinterpret_cast<const u32x4*>(a.v_grid + row[h] * 2 + 8 * g);
+    }
+}
+
+__device__ __forceinline__ uint32_t pack_high(float lo, float hi) {   // bf16 of two floats that have one exactly
+    return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    return __builtin_bit_cast(uint32_t, bf16x2{static_cast<__bf16>(lo), static_cast<__bf16>(hi)});
+}
+
+__device__ __forceinline__ float ubyte(uint32_t w, int b) { return static_cast<float>((w >> (8 * b)) & 0xFFu); }
+
+// Four codes 0 .. 15, one to a byte, as bf16: read as FP8 E4M3 a byte c is
+// c * 2^-9 (the subnormals and the first binade are evenly spaced).
+__device__ __forceinline__ void nibbles_bf16(uint32_t bytes, uint32_t& lo, uint32_t& hi) {
+    lo = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(bytes, 512.f, false));
+    hi = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(bytes, 512.f, true));
+}
+
+// Contraction step `st` of a key row's share as 8 bf16.  At 4 bits the 8
+// dimensions of a dword come as 0, 2, 4, 6, 1, 3, 5, 7 (q_order).
+template <int BITS>
+__device__ __forceinline__ bf16x8 key_step(const uint32_t* k, int st) {
+    u32x4 f;
+    if constexpr (BITS == 16) {
+        f = u32x4{k[4 * st], k[4 * st + 1], k[4 * st + 2], k[4 * st + 3]};
+    } else if constexpr (BITS == 8) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const uint32_t w = k[2 * st + x];
+            f[2 * x] = pack_high(ubyte(w, 0), ubyte(w, 1));
+            f[2 * x + 1] = pack_high(ubyte(w, 2), ubyte(w, 3));
+        }
+    } else {
+        const uint32_t w = k[st];
+        uint32_t r[4];
+        nibbles_bf16(w & 0x0F0F0F0Fu, r[0], r[1]);
+        nibbles_bf16((w >> 4) & 0x0F0F0F0Fu, r[2], r[3]);
+        f = u32x4{r[0], r[1], r[2], r[3]};
+    }
+    return __builtin_bit_cast(bf16x8, f);
+}
+
+template <int BITS>
+__device__ __forceinline__ constexpr int q_order(int e) {
+    return BITS == 4 ? (e < 4 ? 2 * e : 2 * (e - 4) + 1) : e;
+}
+
+// Two rows of the transposed operand (dimensions 2 m2 and 2 m2 + 1 of this
+// lane's D / 16): its 8 tokens' values (codes below 16 bits) as bf16.
+template <int D, int BITS>
+__device__ __forceinline__ void value_pair(const Tile<D, BITS>& T, int m2, bf16x8 (&f)[2]) {
+    u32x4 r[2];
+    if constexpr (BITS == 16) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            r[0][x] = __builtin_amdgcn_perm(T.v[2 * x + 1][m2], T.v[2 * x][m2], 0x05040100u);
+            r[1][x] = __builtin_amdgcn_perm(T.v[2 * x + 1][m2], T.v[2 * x][m2], 0x07060302u);
+        }
+    } else if constexpr (BITS == 8) {
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                r[y][x] = pack_high(ubyte(T.v[2 * x][m2 / 2], 2 * (m2 % 2) + y), ubyte(T.v[2 * x + 1][m2 / 2], 2 * (m2 % 2) + y));
+    } else {
+        const int w = m2 / 4, b = m2 % 4;                         // dword and byte
+        const uint32_t two = b == 0 ? 0x0C0C0400u : b == 1 ? 0x0C0C0501u : b == 2 ? 0x0C0C0602u : 0x0C0C0703u;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {                    // tokens 0 .. 3, 4 .. 7: byte b of each
+            const uint32_t t01 = __builtin_amdgcn_perm(T.v[4 * half + 1][w], T.v[4 * half][w], two);
+            const uint32_t t23 = __builtin_amdgcn_perm(T.v[4 * half + 3][w], T.v[4 * half + 2][w], two);
+            const uint32_t by = t01 | t23 << 16;
+            uint32_t lo, hi;
+            nibbles_bf16(by & 0x0F0F0F0Fu, lo, hi);
+            r[0][2 * half] = lo;
+            r[0][2 * half + 1] = hi;
+            nibbles_bf16((by >> 4) & 0x0F0F0F0Fu, lo, hi);
+            r[1][2 * half] = lo;
+            r[1][2 * half + 1] = hi;
+        }
+    }
+    f[0] = __builtin_bit_cast(bf16x8, r[0]);
+    f[1] = __builtin_bit_cast(bf16x8, r[1]);
+}
+
+// Maximum (or sum) over the four lanes that hold one head's tokens (lane,
+// lane ^ 16, lane ^ 32, lane ^ 48).
+__device__ __forceinline__ float over_groups_max(float x) {
+    x = fmaxf(x, __shfl_xor(x, 16));
+    return fmaxf(x, __shfl_xor(x, 32));
+}
+__device__ __forceinline__ float over_groups_sum(float x) {
+    x += __shfl_xor(x, 16);
+    return x + __shfl_xor(x, 32);
+}
+
+// A wave's state: the output sums of its head (lane % 16), the head's maximum,
+// this lane's share of the sum and of the constant part.
+template <int D>
+struct State {
+    f32x4 o[D / 16];
+    float m, l, konst;
+};
+
+// The scores of a tile (exponents of base 2) of this lane's 8 tokens.
+template <int D, int BITS, int QP>
+__device__ __forceinline__ void tile_scores(float (&a)[8], const Tile<D, BITS>& T, const bf16x8 (&qf)[QP][D / 32],
+                                            float q_sum, float scale_log2) {
+    f32x4 sc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+    for (int s = 0; s < D / 32; ++s)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const bf16x8 kf = key_step<BITS>(T.k[h], s);
+#pragma unroll
+            for (int x = 0; x < QP; ++x) sc[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[x][s], sc[h], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int h = e / 4, r = e % 4;
+        if constexpr (BITS < 16) {
+            const float s = f16_to_f32(static_cast<uint16_t>(T.kg[h][r])), z = f16_to_f32(static_cast<uint16_t>(T.kg[h][r] >> 16));
+            a[e] = scale_log2 * __builtin_fmaf(s, sc[h][r], __builtin_fmaf(0.5f, s, z) * q_sum);
+        } else {
+            a[e] = scale_log2 * sc[h][r];
+        }
+    }
+}
+
+// Folds a tile's scores and values into the state.
+template <int D, int BITS>
+__device__ __forceinline__ void use_values(State<D>& st, Tile<D, BITS>& T, float (&a)[8], int t0, int end,
+                                           const int (&page)[2], int lane) {
+    const int g = lane >> 4;
+    float vs[8], vz[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if constexpr (BITS < 16) {
+            vs[e] = f16_to_f32(static_cast<uint16_t>(T.vg[e / 4][e % 4]));
+            vz[e] = f16_to_f32(static_cast<uint16_t>(T.vg[e / 4][e % 4] >> 16));
+        }
+    // A tile with tokens that are not there: no score, no value, whatever the memory holds.
+    if (t0 + kTileTokens > end || page[0] < 0 || page[1] < 0) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const bool seen = page[e / 4] >= 0 && t0 + 16 * (e / 4) + 4 * g + e % 4 < end;
+            a[e] = seen ? a[e] : -INFINITY;
+            if constexpr (BITS < 16) {
+                vs[e] = seen ? vs[e] : 0.f;
+                vz[e] = seen ? vz[e] : 0.f;
+            } else {
+#pragma unroll
+                for (int w = 0; w < Shape<D, BITS>::kVDwords; ++w) T.v[e][w] = seen ? T.v[e][w] : 0u;
+            }
+        }
+    }
+    float top = a[0];
+#pragma unroll
+    for (int e = 1; e < 8; ++e) top = fmaxf(top, a[e]);
+    const float m_new = fmaxf(st.m, over_groups_max(top));
+    const float base = m_new == -INFINITY ? 0.f : m_new;
+    const float keep = __builtin_amdgcn_exp2f(st.m - base);
+    st.m = m_new;
+    constexpr float mid = static_cast<float>(1 << (BITS - 1));
+    float p[8], l = 0.f, konst = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        p[e] = __builtin_amdgcn_exp2f(a[e] - base);
+        l += p[e];
+        if constexpr (BITS < 16) {
+            konst = __builtin_fmaf(p[e], __builtin_fmaf(mid + 0.5f, vs[e], vz[e]), konst);
+            p[e] *= vs[e];
+        }
+    }
+    u32x4 hi, lo;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        hi[x] = pack_bf16(p[2 * x], p[2 * x + 1]);
+        const float r0 = __uint_as_float(hi[x] << 16), r1 = __uint_as_float(hi[x] & 0xFFFF0000u);
+        lo[x] = pack_bf16(p[2 * x] - r0, p[2 * x + 1] - r1);
+        if constexpr (BITS < 16) {
+            const float s0 = r0 + __uint_as_float(lo[x] << 16), s1 = r1 + __uint_as_float(lo[x] & 0xFFFF0000u);
+            konst = __builtin_fmaf(-mid, s0 + s1, konst);
+        }
+    }
+    st.l = __builtin_fmaf(st.l, keep, l);
+    st.konst = __builtin_fmaf(st.konst, keep, konst);
+    if (__any(keep != 1.f)) {
+#pragma unroll
+        for (int m = 0; m < D / 16; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) st.o[m][r] *= keep;
+    }
+#pragma unroll
+    for (int m2 = 0; m2 < D / 32; ++m2) {
+        bf16x8 vf[2];
+        value_pair<D, BITS>(T, m2, vf);
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            f32x4& o = st.o[2 * m2 + y];
+            o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[y], __builtin_bit_cast(bf16x8, hi), o, 0, 0, 0);
+            o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[y], __builtin_bit_cast(bf16x8, lo), o, 0, 0, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+// Two neighbouring values of an output row.
+__device__ __forceinline__ void store_pair(void* out, int dtype, int64_t at, float x, float y) {
+    if (dtype == GRINQH_F32)
+        *reinterpret_cast<float2*>(static_cast<float*>(out) + at) = make_float2(x, y);
+    else
+        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(out) + at) = pack_bf16(x, y);
+}
+
+__device__ __forceinline__ float2 agent_load(const float* p) {
+    const uint64_t w = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return __builtin_bit_cast(float2, w);
+}
+__device__ __forceinline__ void agent_store(float* p, float2 v) {
+    __hip_atomic_store(reinterpret_cast<uint64_t*>(p), __builtin_bit_cast(uint64_t, v), __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_AGENT);
+}
+
+template <int D, int BITS, int QP, int W>
+__global__ __launch_bounds__(W * kWave, W == 8 || D == 256 || QP == 2 ? 2 : 3) void decode_kernel(DecodeArgs a) {
+    using S = Shape<D, BITS>;
+    constexpr int kDecWaves = W, kDecThreads = W * kWave, kUnit = W * kTileTokens;   // tokens of one round
+    constexpr int kStride = D + 4;                       // floats of a head's row in LDS
+    extern __shared__ float lds[];                       // [wave][head][kStride], then m and l [wave][head]
+    __shared__ int is_last;
+    // Parts are the slow index: workgroups go to the 8 XCDs in turn, and with
+    // the items as the fast one every XCD gets early and late parts alike (late
+    // parts of short sequences are empty).
+    const int item = blockIdx.x % a.items, split = blockIdx.x / a.items;
+    const int tile = item % a.head_tiles, bg = item / a.head_tiles;
+    const int b = bg / a.d.heads, head = bg % a.d.heads;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int i = lane & 15, g = lane >> 4;
+    const int here = min(kHeadTile, a.group - tile * kHeadTile);      // query heads of this workgroup
+    const int h0 = head * a.group + tile * kHeadTile;                 // first query head
+    const int begin = split * a.chunk;
+    int t = begin + wave * kTileTokens;
+
+    // What does not hang on the sequence's length is asked for with it: the
+    // first tile's pages and the queries.
+    const int32_t* table = a.page_table + b * a.table_stride;
+    const auto raw_pages = [&](int t0, int (&page)[2]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) page[h] = table[min((t0 + 16 * h) >> a.d.page_shift, a.max_pages - 1)];
+    };
+    int page[2];
+    raw_pages(t, page);
+    u32x4 raw_q[S::kSteps][QP];
+    {
+        const int64_t q0 = b * a.q_stride + static_cast<int64_t>(h0 + (i < here ? i : 0)) * D;
+#pragma unroll
+        for (int s = 0; s < S::kSteps; ++s) {
+            constexpr int kPer = S::kPerPiece / 8;                    // steps of a piece
+            const int64_t at = q0 + (4 * (s / kPer) + g) * S::kPerPiece + 8 * (s % kPer);
+#pragma unroll
+            for (int x = 0; x < QP; ++x)
+                raw_q[s][x] = QP == 1 ? *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.q) + at)
+                                      : *reinterpret_cast<const u32x4*>(static_cast<const float*>(a.q) + at + 4 * x);
+        }
+    }
     const int len = min(max(a.seq_lens[b], 0), a.longest);
-    float m = -INFINITY, l = 0.f, o[kOwn];
-    for (int i = 0; i < kOwn; ++i) o[i] = 0.f;
-    for (int t0 = 0; t0 < len; t0 += kWave) {
-        const int t = t0 + lane;
-        int64_t row = -1;
-        if (t < len) {
-            const int64_t page = a.page_table[b * a.table_stride + (t >> a.d.page_shift)];
-            row = kv_row(a.d, (page << a.d.page_shift) + (t & ((1 << a.d.page_shift) - 1)), g);
-        }
-        float score = -INFINITY;
-        if (row >= 0) {
-            float s = 0.f, z = 0.f, sum = 0.f;
-            if (BITS < 16) {
-                s = f16_to_f32(a.k_grid[2 * row]);
-                z = f16_to_f32(a.k_grid[2 * row + 1]);
-            }
-            for (int d = 0; d < D; ++d) sum = __builtin_fmaf(qs[d], cached<BITS>(a.k_codes + row * kRow, s, z, d), sum);
-            score = sum * a.scale;
-        }
-        float top = score;
-        for (int x = 1; x < kWave; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
-        const float m_new = fmaxf(m, top), base = m_new == -INFINITY ? 0.f : m_new;
-        const float p = row >= 0 ? expf(score - base) : 0.f, keep = expf(m - base);
-        float total = p;
-        for (int x = 1; x < kWave; x <<= 1) total += __shfl_xor(total, x);
-        l = l * keep + total;
-        m = m_new;
-        __syncthreads();
-        ps[lane] = p;
-        rows[lane] = row;
-        __syncthreads();
-        for (int i = 0; i < kOwn; ++i) o[i] *= keep;
-        for (int j = 0; j < min(kWave, len - t0); ++j) {
-            const int64_t r = rows[j];
-            if (r < 0) continue;
-            float s = 0.f, z = 0.f;
-            if (BITS < 16) {
-                s = f16_to_f32(a.v_grid[2 * r]);
-                z = f16_to_f32(a.v_grid[2 * r + 1]);
-            }
-            for (int i = 0; i < kOwn; ++i)
-                o[i] = __builtin_fmaf(ps[j], cached<BITS>(a.v_codes + r * kRow, s, z, lane + i * kWave), o[i]);
+    const int parts = max(1, (len + a.chunk - 1) / a.chunk);
+    if (split >= parts) return;
+    const int end = min(len, begin + a.chunk);
+
+    // Pages of the two halves of the tile at t0; -1 past the end or absent.
+    const auto check_pages = [&](int t0, int (&page)[2]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (t0 + 16 * h >= end || static_cast<unsigned>(page[h]) >= static_cast<unsigned>(a.d.n_pages)) page[h] = -1;
+    };
+    Tile<D, BITS> T;
+    int64_t row[2];
+    check_pages(t, page);
+    if (t < end) {
+        tile_rows(row, a, t, page, head);
+        load_keys(T, a, row, lane);
+        load_values(T, a, row, lane);
+    }
+
+    // Q, in the order of the key pieces; heads that are not there are zeros.
+    bf16x8 qf[QP][S::kSteps];
+    float q_sum = 0.f;
+#pragma unroll
+    for (int s = 0; s < S::kSteps; ++s) {
+        float w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            w[e] = QP == 2 ? __uint_as_float(raw_q[s][QP == 2 ? e / 4 : 0][e % 4])
+                           : __uint_as_float(e % 2 ? raw_q[s][0][e / 2] & 0xFFFF0000u : raw_q[s][0][e / 2] << 16);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float x = i < here ? w[q_order<BITS>(e)] : 0.f;
+            const __bf16 part = static_cast<__bf16>(x);
+            qf[0][s][e] = part;
+            q_sum += x;
+            if constexpr (QP == 2) qf[1][s][e] = static_cast<__bf16>(x - static_cast<float>(part));
         }
     }
-    const int64_t o0 = (static_cast<int64_t>(b) * a.n_q_heads + h) * D;
-    for (int i = 0; i < kOwn; ++i) {
-        const float y = l == 0.f ? 0.f : o[i] / l;
-        if (a.out_dtype == GRINQH_F32)
-            static_cast<float*>(a.out)[o0 + lane + i * kWave] = y;
+    q_sum = over_groups_sum(q_sum);
+
+    State<D> st;
+    st.m = -INFINITY;
+    st.l = st.konst = 0.f;
+#pragma unroll
+    for (int m = 0; m < D / 16; ++m) st.o[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    if (t < end) {
+        // A tile's keys are free once its scores are formed, its values once
+        // they are added: the next tile's are loaded into the same registers.
+        for (;;) {
+            const bool more = t + kUnit < end;
+            int next[2];
+            raw_pages(t + kUnit, next);
+            float sc[8];
+            tile_scores<D, BITS, QP>(sc, T, qf, q_sum, a.scale_log2);
+            __builtin_amdgcn_sched_barrier(0);
+            check_pages(t + kUnit, next);
+            if (more) {
+                tile_rows(row, a, t + kUnit, next, head);
+                load_keys(T, a, row, lane);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            use_values<D, BITS>(st, T, sc, t, end, page, lane);
+            if (!more) break;
+            load_values(T, a, row, lane);
+            t += kUnit;
+            page[0] = next[0];
+            page[1] = next[1];
+        }
+    }
+
+    // Join the waves.
+    st.l = over_groups_sum(st.l);
+    st.konst = over_groups_sum(st.konst);
+    float* stats = lds + kDecWaves * here * kStride;
+    if (i < here) {
+        float* o = lds + (wave * here + i) * kStride;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int m = 0; m < D / 16; ++m) o[(4 * g + r) * (D / 16) + m] = st.o[m][r] + st.konst;
+        if (g == 0) {
+            stats[(wave * here + i) * 2] = st.m;
+            stats[(wave * here + i) * 2 + 1] = st.l;
+        }
+    }
+    __syncthreads();
+    const bool whole = parts == 1;
+    float* part = a.parts + (static_cast<int64_t>(item) * a.splits + split) * min(a.group, kHeadTile) * (D + 2);
+    for (int e = threadIdx.x * 2; e < here * D; e += kDecThreads * 2) {
+        const int h = e / D, x = e % D;
+        float m = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kDecWaves; ++w) m = fmaxf(m, stats[(w * here + h) * 2]);
+        const float base = m == -INFINITY ? 0.f : m;
+        float l = 0.f, y0 = 0.f, y1 = 0.f;
+#pragma unroll
+        for (int w = 0; w < kDecWaves; ++w) {
+            const float f = __builtin_amdgcn_exp2f(stats[(w * here + h) * 2] - base);
+            const float* o = lds + (w * here + h) * kStride + x;
+            l = __builtin_fmaf(f, stats[(w * here + h) * 2 + 1], l);
+            y0 = __builtin_fmaf(f, o[0], y0);
+            y1 = __builtin_fmaf(f, o[1], y1);
+        }
+        if (whole) {
+            const float r = l == 0.f ? 0.f : 1.f / l;
+            store_pair(a.out, a.out_dtype, (static_cast<int64_t>(b) * a.n_q_heads + h0 + h) * D + x, y0 * r, y1 * r);
+            if (a.lse != nullptr && x == 0)
+                a.lse[static_cast<int64_t>(b) * a.n_q_heads + h0 + h] = kLn2 * (m + __builtin_amdgcn_logf(l));
+        } else {
+            agent_store(part + h * D + x, make_float2(y0, y1));
+            if (x == 0) agent_store(part + here * D + 2 * h, make_float2(m, l));
+        }
+    }
+    if (whole) return;
+
+    // The part that arrives last joins all of them.  Every access to the parts
+    // and the counter is an agent-scope atomic, performed past the XCDs' own
+    // caches; a wave's stores are done when its memory counter says so, the
+    // barrier waits for every wave's, and the arrival is counted after it, so
+    // the last arrival's loads, issued after the count, find every part.  (No
+    // fence: at agent scope it would write back the XCD's whole L2.)
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_s_waitcnt(0);
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const unsigned prev = __hip_atomic_fetch_add(a.counters + item, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        is_last = prev == static_cast<unsigned>(parts - 1);
+    }
+    __syncthreads();
+    if (!is_last) return;
+    if (threadIdx.x == 0) __hip_atomic_store(a.counters + item, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    // Every thread weighs the parts by itself: a batch's statistics and values
+    // are asked for at once, one trip to memory.  Where two outputs to a thread
+    // leave threads over, `sets` of them share the parts.
+    const int64_t step = static_cast<int64_t>(min(a.group, kHeadTile)) * (D + 2);
+    const float* first = a.parts + static_cast<int64_t>(item) * a.splits * step;
+    const int pairs = here * (D / 2);
+    const int sets = max(1, kDecThreads / pairs);
+    const auto finish = [&](int h, int x, f32x4 r) {      // r: m, l and two outputs
+        const float inv = r[1] == 0.f ? 0.f : 1.f / r[1];
+        store_pair(a.out, a.out_dtype, (static_cast<int64_t>(b) * a.n_q_heads + h0 + h) * D + x, r[2] * inv, r[3] * inv);
+        if (a.lse != nullptr && x == 0)
+            a.lse[static_cast<int64_t>(b) * a.n_q_heads + h0 + h] = kLn2 * (r[0] + __builtin_amdgcn_logf(r[1]));
+    };
+    const auto fold = [](f32x4& r, float m, float l, float y0, float y1) {
+        const float top = fmaxf(r[0], m), base = top == -INFINITY ? 0.f : top;
+        const float f = __builtin_amdgcn_exp2f(r[0] - base), g = __builtin_amdgcn_exp2f(m - base);
+        r = f32x4{top, r[1] * f + l * g, r[2] * f + y0 * g, r[3] * f + y1 * g};
+    };
+    f32x4* shared = reinterpret_cast<f32x4*>(lds);        // [set][pair]
+    for (int u = threadIdx.x; u < sets * pairs; u += kDecThreads) {
+        const int e = u % pairs, set = u / pairs, h = e / (D / 2), x = e % (D / 2) * 2;
+        f32x4 r{-INFINITY, 0.f, 0.f, 0.f};
+        for (int s0 = set; s0 < parts; s0 += kBatch * sets) {
+            float2 ml[kBatch], v[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                ml[k] = make_float2(-INFINITY, 0.f);
+                v[k] = make_float2(0.f, 0.f);
+                if (s0 + k * sets < parts) {
+                    const float* p = first + (s0 + k * sets) * step;
+                    ml[k] = agent_load(p + here * D + 2 * h);
+                    v[k] = agent_load(p + h * D + x);
+                }
+            }
+            float top = r[0];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) top = fmaxf(top, ml[k].x);
+            const float base = top == -INFINITY ? 0.f : top;
+            r *= __builtin_amdgcn_exp2f(r[0] - base);
+            r[0] = top;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const float f = __builtin_amdgcn_exp2f(ml[k].x - base);
+                r[1] = __builtin_fmaf(f, ml[k].y, r[1]);
+                r[2] = __builtin_fmaf(f, v[k].x, r[2]);
+                r[3] = __builtin_fmaf(f, v[k].y, r[3]);
+            }
+        }
+        if (sets == 1)
+            finish(h, x, r);
         else
-            static_cast<uint16_t*>(a.out)[o0 + lane + i * kWave] = f32_to_bf16(y);
+            shared[u] = r;
     }
-    if (a.lse != nullptr && lane == 0) a.lse[static_cast<int64_t>(b) * a.n_q_heads + h] = m + logf(l);
+    if (sets == 1) return;
+    __syncthreads();
+    for (int e = threadIdx.x; e < pairs; e += kDecThreads) {
+        f32x4 r = shared[e];
+        for (int k = 1; k < sets; ++k) {
+            const f32x4 y = shared[k * pairs + e];
+            fold(r, y[0], y[1], y[2], y[3]);
+        }
+        finish(e / (D / 2), e % (D / 2) * 2, r);
+    }
+}
+
+// How a call is cut up (host arithmetic on its sizes alone).  Measured in us a
+// call, four and eight waves, 8 bits, 8 heads of 128, groups of 4, one sequence:
+//   500 tokens 8.3 and 10.2; 2000 10.0 and 10.6; 4000 12.8 and 11.8; 32768 24 and 22;
+// 32 sequences of 17 .. 8192 tokens, four waves: one workgroup to a CU 79, twelve
+// 66 (eight waves, one to a CU: 73); 32 of 2048 each: 34 and 37.
+constexpr int kCus = 256, kFewItems = 48, kOneRound = 128;
+
+struct DecodePlan {
+    int waves, head_tiles, splits, chunk;
+    int64_t items;
+    size_t ws_bytes;
+};
+
+DecodePlan plan_decode(const grinqh_kv_layout& L, int n_q_heads, int batch, int max_len) {
+    DecodePlan p;
+    const int group = n_q_heads / L.n_kv_heads;
+    p.head_tiles = (group + kHeadTile - 1) / kHeadTile;
+    p.items = static_cast<int64_t>(batch) * L.n_kv_heads * p.head_tiles;
+    // Few sequences and heads: parts for one round of a short cache (four waves,
+    // 128 tokens), else one workgroup of eight waves to a CU.  Many: workgroups
+    // of four waves, three to a CU, of 512 tokens and more, enough of them that
+    // sequences of different lengths fill the card evenly.
+    const bool few = p.items <= kFewItems;
+    const auto units_of = [&](int waves) { return (static_cast<int64_t>(max_len) + waves * kTileTokens - 1) / (waves * kTileTokens); };
+    p.waves = few && p.items * units_of(4) > kOneRound ? 8 : 4;
+    const int64_t units = units_of(p.waves);
+    const auto at_most = [&](int64_t groups) {          // units of a part, for that many workgroups in all
+        const int64_t parts = std::max<int64_t>(1, groups / std::max<int64_t>(p.items, 1));
+        return (units + parts - 1) / parts;
+    };
+    int64_t per = few ? at_most(kCus) : std::max<int64_t>(at_most(12 * kCus), 4);
+    if (!few && p.items * ((units + per - 1) / per) < 3 * kCus) per = std::min(per, at_most(3 * kCus));
+    if (p.items > kCounters) per = units;
+    p.chunk = static_cast<int>(per * p.waves * kTileTokens);
+    p.splits = static_cast<int>((units + per - 1) / per);
+    const size_t part = static_cast<size_t>(std::min(group, kHeadTile)) * (L.head_dim + 2) * sizeof(float);
+    p.ws_bytes = kCounters * sizeof(unsigned) + (p.splits > 1 ? p.items * p.splits * part : 0);
+    p.ws_bytes = (p.ws_bytes + 255) / 256 * 256;
+    return p;
+}
+
+template <int D, int BITS>
+void launch_queries(const DecodeArgs& a, int waves, unsigned n, hipStream_t stream) {
+    const int here = a.group < kHeadTile ? a.group : kHeadTile;
+    const size_t lds = static_cast<size_t>(waves) * std::max<size_t>(here * (D + 4 + 2) * sizeof(float), kWave * sizeof(f32x4));
+    if (waves == 8) {
+        if (a.q_dtype == GRINQH_BF16) decode_kernel<D, BITS, 1, 8><<<dim3(n), dim3(512), lds, stream>>>(a);
+        else decode_kernel<D, BITS, 2, 8><<<dim3(n), dim3(512), lds, stream>>>(a);
+        return;
+    }
+    if (a.q_dtype == GRINQH_BF16) decode_kernel<D, BITS, 1, 4><<<dim3(n), dim3(256), lds, stream>>>(a);
+    else decode_kernel<D, BITS, 2, 4><<<dim3(n), dim3(256), lds, stream>>>(a);
 }
 
 template <int D>
-void launch_bits(const DecodeArgs& a, int bits, unsigned n, hipStream_t stream) {
-    if (bits == 4) decode_kernel<D, 4><<<dim3(n), dim3(kWave), 0, stream>>>(a);
-    else if (bits == 8) decode_kernel<D, 8><<<dim3(n), dim3(kWave), 0, stream>>>(a);
-    else decode_kernel<D, 16><<<dim3(n), dim3(kWave), 0, stream>>>(a);
+void launch_bits(const DecodeArgs& a, int bits, int waves, unsigned n, hipStream_t stream) {
+    if (bits == 4) launch_queries<D, 4>(a, waves, n, stream);
+    else if (bits == 8) launch_queries<D, 8>(a, waves, n, stream);
+    else launch_queries<D, 16>(a, waves, n, stream);
 }
 
 bool valid_heads(const grinqh_kv_layout* L, int n_q_heads, int batch, int max_len) {
@@ -127,8 +694,7 @@ extern "C" {
 
 size_t grinqh_attention_workspace_bytes(const grinqh_kv_layout* L, int32_t n_q_heads, int32_t batch,
                                         int32_t max_len) {
-    if (!valid_heads(L, n_q_heads, batch, max_len)) return 0;
-    return 256;
+    return valid_heads(L, n_q_heads, batch, max_len) ? plan_decode(*L, n_q_heads, batch, max_len).ws_bytes : 0;
 }
 
 grinqh_status grinqh_decode_attention(const grinqh_kv_layout* L, const grinqh_kv_pools* pools, const void* q,
@@ -153,7 +719,9 @@ grinqh_status grinqh_decode_attention(const grinqh_kv_layout* L, const grinqh_kv
     if (!aligned_to(q, 16) || q_stride * qb % 16 != 0 || !aligned_to(page_table, 4) || !aligned_to(seq_lens, 4) ||
         !aligned_to(out, 16) || !aligned_to(lse, 4) || !aligned_to(workspace, 256))
         return GRINQH_EALIGN;
-    if (workspace_bytes < grinqh_attention_workspace_bytes(L, n_q_heads, batch, max_len)) return GRINQH_ENOSPACE;
+    const DecodePlan plan = plan_decode(*L, n_q_heads, batch, max_len);
+    if (workspace_bytes < plan.ws_bytes) return GRINQH_ENOSPACE;
+    if (plan.items * plan.splits > kMaxDecodeGroups) return GRINQH_EINVAL;
     if (overlaps(q, static_cast<size_t>(((batch - 1) * q_stride + width) * qb), out,
                  static_cast<size_t>(batch * width * ob)))
         return GRINQH_EINVAL;
@@ -161,13 +729,37 @@ grinqh_status grinqh_decode_attention(const grinqh_kv_layout* L, const grinqh_kv
     hipError_t e;
     if (!current_device_info(&dev, &e)) return map_hip_error(e);
     const int64_t reach = static_cast<int64_t>(max_pages) * L->page_size;
-    const DecodeArgs a{kv_dims(*L), pools->k_codes, pools->v_codes, pools->k_grid, pools->v_grid, q, page_table,
-                       seq_lens, out, lse, q_stride, table_stride, n_q_heads, n_q_heads / L->n_kv_heads,
-                       static_cast<int>(reach < max_len ? reach : max_len), q_dtype, out_dtype, scale};
-    const unsigned n = static_cast<unsigned>(batch) * n_q_heads;
-    if (L->head_dim == 64) launch_bits<64>(a, L->bits, n, static_cast<hipStream_t>(stream));
-    else if (L->head_dim == 128) launch_bits<128>(a, L->bits, n, static_cast<hipStream_t>(stream));
-    else launch_bits<256>(a, L->bits, n, static_cast<hipStream_t>(stream));
+    DecodeArgs a;
+    a.d = kv_dims(*L);
+    a.k_codes = pools->k_codes;
+    a.v_codes = pools->v_codes;
+    a.k_grid = pools->k_grid;
+    a.v_grid = pools->v_grid;
+    a.q = q;
+    a.page_table = page_table;
+    a.seq_lens = seq_lens;
+    a.out = out;
+    a.lse = lse;
+    a.counters = static_cast<unsigned*>(workspace);
+    a.parts = reinterpret_cast<float*>(a.counters + kCounters);
+    a.q_stride = q_stride;
+    a.table_stride = table_stride;
+    a.n_q_heads = n_q_heads;
+    a.group = n_q_heads / L->n_kv_heads;
+    a.head_tiles = plan.head_tiles;
+    a.items = static_cast<int>(plan.items);
+    a.splits = plan.splits;
+    a.max_pages = max_pages;
+    a.chunk = plan.chunk;
+    a.longest = static_cast<int>(reach < max_len ? reach : max_len);
+    a.q_dtype = q_dtype;
+    a.out_dtype = out_dtype;
+    a.scale_log2 = scale * kLog2e;
+    const unsigned n = static_cast<unsigned>(plan.items * plan.splits);
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    if (L->head_dim == 64) launch_bits<64>(a, L->bits, plan.waves, n, s);
+    else if (L->head_dim == 128) launch_bits<128>(a, L->bits, plan.waves, n, s);
+    else launch_bits<256>(a, L->bits, plan.waves, n, s);
     return map_hip_error(hipGetLastError());
 }
 

@@ -56,6 +56,7 @@ def _queries(rng, batch, n_q, dim, q_dtype):
     (2, 16, 64, 256, [300, 5]),
     (1, 24, 128, 16, [100, 65]),
     (1, 64, 64, 32, [70]),
+    (1, 16, 256, 64, [200, 70]),
     (5, 2, 128, 16, [63, 64, 65, 191, 193]),
 ])
 def test_decode_matches_the_oracle(dev, bits, heads, group, dim, page, lens):
