@@ -5,8 +5,24 @@
 //   o = sum_j p_j v_j,  p_j = exp(a_j - max) / sum,  a_j = scale * q . k_j,
 // over the keys j <= i + m - n (all keys where not causal).
 //
-// One wave per (query, head) walks the keys 64 at a time with the running
-// maximum and sum.
+// One pass over the keys with a running maximum and sum.  The rows of a
+// key-value head are its (query, head of the group) pairs, query by query, so a
+// tile of rows spans few queries: short prompts fill tiles, and little of a
+// causal tile is masked.  A workgroup of four waves takes 128 rows, 32 to a
+// wave; tiles of keys and values go through LDS for all of them, the next
+// tile's loads under way while this one is used.
+//
+// Scores.  S^T = K Q^T (32 keys x 32 rows, v_mfma_f32_32x32x16_bf16): a lane
+// holds 16 of a row's 32 scores, the lane 32 further the others, so maximum and
+// sum need one exchange between the two.  The exponent is one fused
+// multiply-add, exp2(s c - max c) with c = scale log2 e.
+//
+// Values.  O^T = V^T P^T.  The scores a lane holds are its share of the
+// contraction as they are (the contraction's order is free), rounded to bf16
+// in place; V^T comes from LDS with transposing reads (ds_read_b64_tr_b16).
+//
+// The maximum follows only when a row's scores exceed it by 2^8: weights up to
+// 2^8 lose nothing in fp32 and bf16, and the sums are rarely rescaled.
 #include <math.h>
 
 #include "internal.h"
@@ -16,61 +32,396 @@ namespace grinqh {
 namespace {
 
 typedef grinqh_prefill_attention_args Args;
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kPreWaves = 4;
+constexpr int kPreThreads = kPreWaves * kWave;
+constexpr int64_t kMaxPreGroups = 1 << 23;              // workgroups of a launch
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr float kSlack = 8.f;                           // log2 by which scores may exceed the maximum in use
 
 template <int D>
-__global__ __launch_bounds__(kWave) void prefill_attention_kernel(Args a) {
-    constexpr int kOwn = D / kWave;
-    const int row = blockIdx.x, h = blockIdx.y, g = h / (a.n_q_heads / a.n_kv_heads), lane = threadIdx.x;
-    int b = 0, q_begin = 0, q_end = 0;
-    for (; b < a.batch; ++b) {                        // the sequence that holds the row
-        q_begin = min(max(a.cu_q[b], 0), a.total_q);
-        q_end = min(max(a.cu_q[b + 1], 0), a.total_q);
-        if (row >= q_begin && row < q_end) break;
-    }
-    if (b == a.batch) return;
-    const int k_begin = min(max(a.cu_k[b], 0), a.total_k), k_end = min(max(a.cu_k[b + 1], 0), a.total_k);
-    const int n = q_end - q_begin, keys = max(k_end - k_begin, 0), i = row - q_begin;
-    const int seen = a.causal ? max(min(i + keys - n + 1, keys), 0) : keys;
-    __shared__ float qs[D], ps[kWave];
-    const uint16_t* q = static_cast<const uint16_t*>(a.q) + row * a.q_stride + h * D;
-    const uint16_t* k = static_cast<const uint16_t*>(a.k) + k_begin * a.k_stride + g * D;
-    const uint16_t* v = static_cast<const uint16_t*>(a.v) + k_begin * a.v_stride + g * D;
-    for (int d = lane; d < D; d += kWave) qs[d] = bf16_to_f32(q[d]);
-    float m = -INFINITY, l = 0.f, o[kOwn];
-    for (int x = 0; x < kOwn; ++x) o[x] = 0.f;
-    for (int t0 = 0; t0 < seen; t0 += kWave) {
-        const int t = t0 + lane;
-        __syncthreads();
-        float score = -INFINITY;
-        if (t < seen) {
-            float sum = 0.f;
-            for (int d = 0; d < D; ++d) sum = __builtin_fmaf(qs[d], bf16_to_f32(k[t * a.k_stride + d]), sum);
-            score = sum * a.scale;
+struct PreShape {
+    static constexpr int kRT = 1;                       // 32-row tiles of a wave
+    static constexpr int kRows = kPreWaves * 32 * kRT;  // rows of a workgroup
+    static constexpr int kTK = D == 256 ? 32 : 64;      // keys of a tile
+    static constexpr int kChunks = D / 8;               // 16-byte chunks of a key
+    static constexpr int kBytes = kTK * D * 2;          // of a tile of keys (or values)
+};
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+// 16 bytes per lane from a buffer straight into LDS, lane after lane from
+// `lds` (uniform).  Written out because the compiler, not knowing which tile an
+// LDS read is from, would wait for every such load before it; the kernel waits
+// for all of them itself, before the barrier that hands a tile over.
+__device__ __forceinline__ void load_to_lds(i32x4 rsrc, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 1\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(lds), "v"(off), "s"(rsrc)
+                 : "memory", "m0");
+}
+
+// A buffer over `rows` rows: what lies behind them reads as zeros.
+__device__ __forceinline__ i32x4 rows_rsrc(const uint16_t* base, int rows, uint32_t stride_bytes, int row_bytes) {
+    const uint64_t at = reinterpret_cast<uint64_t>(base);
+    const uint32_t bytes = rows > 0 ? (min(rows, 64) - 1) * stride_bytes + row_bytes : 0;
+    return i32x4{static_cast<int>(at), static_cast<int>(at >> 32) & 0xFFFF, static_cast<int>(bytes), 0x00020000};
+}
+
+// Loads a tile of keys or values (`rows` of them exist) into LDS: 16-byte chunks
+// in the order of LDS, chunk c of row r at c ^ swizzle(r) (so that the operand
+// reads of neighbouring rows fall on different banks).  `off` is the lane's
+// offset (tile_offset); the rows a load starts at move the buffer.
+template <int D>
+__device__ __forceinline__ void load_tile(const uint16_t* base, int rows, int64_t stride, uint32_t off, uint32_t lds, int wave) {
+    using S = PreShape<D>;
+    constexpr int kRowsAtOnce = kPreThreads / S::kChunks;
+    const uint32_t stride_bytes = static_cast<uint32_t>(stride) * 2;
+#pragma unroll
+    for (int n = 0; n < S::kTK / kRowsAtOnce; ++n)
+        load_to_lds(rows_rsrc(base + n * kRowsAtOnce * stride, rows - n * kRowsAtOnce, stride_bytes, D * 2), off,
+                    lds + (n * kPreThreads + wave * kWave) * 16);
+}
+
+template <int D, bool VALUES>
+__device__ __forceinline__ uint32_t tile_offset(int64_t stride, int thread) {
+    const int r = thread / PreShape<D>::kChunks, slot = thread % PreShape<D>::kChunks;
+    return r * static_cast<uint32_t>(stride) * 2 + (slot ^ (VALUES ? (r & 3) << 1 : r & 7)) * 16;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    return __builtin_bit_cast(uint32_t, bf16x2{static_cast<__bf16>(lo), static_cast<__bf16>(hi)});
+}
+
+// x of this lane and of the lane 32 further.
+__device__ __forceinline__ float max_halves(float x) {
+    const u32x2 r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r.x), __uint_as_float(r.y));
+}
+__device__ __forceinline__ float sum_halves(float x) {
+    const u32x2 r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(r.x) + __uint_as_float(r.y);
+}
+
+// Where a flat tile number lies: its sequence and tile, both -1 past the last.
+struct Place {
+    int seq, tile, tiles;
+};
+__device__ __forceinline__ Place find_tile(const Args& a, int group, int rows, int number, int lane) {
+    int before = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += kWave) {
+        int tiles = 0;
+        if (b0 + lane < a.batch) {
+            const int q0 = min(max(a.cu_q[b0 + lane], 0), a.total_q), q1 = min(max(a.cu_q[b0 + lane + 1], 0), a.total_q);
+            tiles = static_cast<int>((static_cast<int64_t>(max(q1 - q0, 0)) * group + rows - 1) / rows);
         }
-        float top = score;
-        for (int x = 1; x < kWave; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
-        const float m_new = fmaxf(m, top), base = m_new == -INFINITY ? 0.f : m_new;
-        const float p = t < seen ? expf(score - base) : 0.f, keep = expf(m - base);
-        float total = p;
-        for (int x = 1; x < kWave; x <<= 1) total += __shfl_xor(total, x);
-        l = l * keep + total;
-        m = m_new;
-        ps[lane] = p;
-        __syncthreads();
-        for (int x = 0; x < kOwn; ++x) o[x] *= keep;
-        for (int j = 0; j < min(kWave, seen - t0); ++j)
-            for (int x = 0; x < kOwn; ++x)
-                o[x] = __builtin_fmaf(ps[j], bf16_to_f32(v[(t0 + j) * a.v_stride + lane + x * kWave]), o[x]);
+        int sum = tiles;
+#pragma unroll
+        for (int k = 1; k < kWave; k <<= 1) {
+            const int x = __shfl_up(sum, k);
+            if (lane >= k) sum += x;
+        }
+        const uint64_t over = __ballot(before + sum > number);
+        if (over != 0) {
+            const int at = __builtin_ctzll(over);
+            const int upto = __shfl(sum, at), mine = __shfl(tiles, at);
+            return Place{b0 + at, number - (before + upto - mine), mine};
+        }
+        before += __shfl(sum, kWave - 1);
     }
-    const int64_t o0 = (static_cast<int64_t>(row) * a.n_q_heads + h) * D;
-    for (int x = 0; x < kOwn; ++x) {
-        const float y = l == 0.f ? 0.f : o[x] / l;
-        if (a.out_dtype == GRINQH_F32)
-            static_cast<float*>(a.out)[o0 + lane + x * kWave] = y;
-        else
-            static_cast<uint16_t*>(a.out)[o0 + lane + x * kWave] = f32_to_bf16(y);
+    return Place{-1, -1, 0};
+}
+
+template <int D>
+__global__ __launch_bounds__(kPreThreads, D == 256 ? 1 : 2) void prefill_attention_kernel(Args a, float c) {
+    using S = PreShape<D>;
+    constexpr int RT = S::kRT, TK = S::kTK, KT = TK / 32, DT = D / 32;
+    __shared__ __attribute__((aligned(1024))) char lds[2][2][S::kBytes];       // [buffer][keys, values]
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int group = a.n_q_heads / a.n_kv_heads;
+    // Heads are the fast index, so that with eight of them each XCD's L2 keeps one head's keys.
+    const int head = blockIdx.x % a.n_kv_heads;
+    const Place at = find_tile(a, group, S::kRows, blockIdx.x / a.n_kv_heads, lane);
+    if (at.seq < 0) return;
+    const int seq = __builtin_amdgcn_readfirstlane(at.seq);
+    // The last tiles of a causal sequence see the most keys and go first.
+    const int tile = __builtin_amdgcn_readfirstlane(a.causal ? at.tiles - 1 - at.tile : at.tile);
+    const int q_begin = min(max(a.cu_q[seq], 0), a.total_q), q_end = min(max(a.cu_q[seq + 1], 0), a.total_q);
+    const int k_begin = min(max(a.cu_k[seq], 0), a.total_k);
+    const int n = q_end - q_begin, m = max(min(max(a.cu_k[seq + 1], 0), a.total_k) - k_begin, 0);
+
+    // Rows: first query and head of the tile, then this lane's.
+    const int64_t row0 = static_cast<int64_t>(tile) * S::kRows;
+    const int i0 = static_cast<int>(row0 / group), rem0 = static_cast<int>(row0 % group);
+    const auto query_of = [&](int local) { return i0 + (rem0 + local) / group; };
+    const auto seen_by = [&](int i) { return a.causal ? min(max(i + m - n + 1, 0), m) : m; };   // keys 0 .. that - 1
+    const int local0 = wave * 32 * RT;
+    const int all_end = seen_by(min(query_of(S::kRows - 1), n - 1));           // keys any row of the workgroup sees
+    const int wave_end = seen_by(min(query_of(local0 + 32 * RT - 1), n - 1));  // any row of the wave
+    const int wave_full = seen_by(query_of(local0));                           // all rows of the wave
+    const bool idle = query_of(local0) >= n;                                   // no row of the wave exists
+
+    bf16x8 qf[RT][D / 16];
+    int seen[RT];
+    int64_t out_row[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        const int local = local0 + 32 * rt + (lane & 31);
+        const int i = query_of(local), h = head * group + (rem0 + local) % group;
+        const bool there = i < n;
+        seen[rt] = there ? seen_by(i) : 0;
+        out_row[rt] = there ? static_cast<int64_t>(q_begin + i) * a.n_q_heads + h : -1;
+        const uint16_t* q = static_cast<const uint16_t*>(a.q) + (q_begin + (there ? i : 0)) * a.q_stride + (there ? h : 0) * D;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            u32x4 x = *reinterpret_cast<const u32x4*>(q + 16 * kk + 8 * (lane >> 5));
+            if (a.scale < 0.f) x ^= 0x80008000u;                               // c is |scale| log2 e
+            if (a.scale == 0.f) x = u32x4{0u, 0u, 0u, 0u};
+            qf[rt][kk] = __builtin_bit_cast(bf16x8, x);
+        }
     }
-    if (a.lse != nullptr && lane == 0) a.lse[static_cast<int64_t>(row) * a.n_q_heads + h] = m + logf(l);
+
+    f32x16 o[RT][DT];
+    float top[RT], l[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        top[rt] = -INFINITY;
+        l[rt] = 0.f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) o[rt][d][r] = 0.f;
+    }
+
+    const uint16_t* keys = static_cast<const uint16_t*>(a.k) + k_begin * a.k_stride + head * D;
+    const uint16_t* values = static_cast<const uint16_t*>(a.v) + k_begin * a.v_stride + head * D;
+    const uint32_t ks = tile_offset<D, false>(a.k_stride, threadIdx.x), vs = tile_offset<D, true>(a.v_stride, threadIdx.x);
+    const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)&lds[0][0][0]));
+    const auto load = [&](int t0, int buf) {
+        load_tile<D>(keys + t0 * a.k_stride, m - t0, a.k_stride, ks, lds0 + buf * 2 * S::kBytes, wave);
+        load_tile<D>(values + t0 * a.v_stride, m - t0, a.v_stride, vs, lds0 + (2 * buf + 1) * S::kBytes, wave);
+    };
+    // Byte offsets of this lane's operand reads (see load_tile): keys by step
+    // modulo 4, values by dimension tile modulo 2.
+    uint32_t k_off[4], v_off[2];
+    {
+        const int r = lane & 31, i = lane & 15;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) k_off[x] = r * D * 2 + (((2 * x + (lane >> 5)) ^ (r & 7)) * 16);
+        const int vr = 4 * (lane >> 5) + (i >> 2);
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            v_off[x] = vr * D * 2 + (((4 * x + 2 * ((lane >> 4) & 1) + ((i & 3) >> 1)) ^ ((vr & 3) << 1)) * 16) + (i & 1) * 8;
+    }
+    const auto key_frag = [&](const char* kb, int tt, int kk) {
+        return *reinterpret_cast<const bf16x8*>(kb + k_off[kk & 3] + tt * 32 * D * 2 + (kk >> 2) * 128);
+    };
+    const auto value_frag = [&](const char* vb, int step, int d) {             // 16 keys from 16 * step, 32 dimensions
+        const char* p = vb + v_off[d & 1] + step * 16 * D * 2 + (d >> 1) * 128;
+        const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p));
+        const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p + 8 * D * 2));
+        return __builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+    };
+
+    const int tiles = (all_end + TK - 1) / TK;
+    if (tiles > 0) load(0, 0);
+    for (int t = 0; t < tiles; ++t) {
+        const int t0 = t * TK;
+        __builtin_amdgcn_s_waitcnt(0);                  // this wave's share of the tile has arrived
+        __syncthreads();                                // everyone's has; and the other buffer is free
+        if (t + 1 < tiles) load(t0 + TK, (t + 1) & 1);
+        if (idle || t0 >= wave_end) continue;
+        const char* kb = lds[t & 1][0];
+        const char* vb = lds[t & 1][1];
+        f32x16 s[RT][KT];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int tt = 0; tt < KT; ++tt)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[rt][tt][r] = 0.f;
+        {
+            bf16x8 kf[3][KT];                           // operands two steps ahead
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int tt = 0; tt < KT; ++tt) kf[kk][tt] = key_frag(kb, tt, kk);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                if (kk + 2 < D / 16)
+#pragma unroll
+                    for (int tt = 0; tt < KT; ++tt) kf[(kk + 2) % 3][tt] = key_frag(kb, tt, kk + 2);
+#pragma unroll
+                for (int tt = 0; tt < KT; ++tt)
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt)
+                        s[rt][tt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[kk % 3][tt], qf[rt][kk], s[rt][tt], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        const bool masked = t0 + TK > wave_full;
+        if (masked) {
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int tt = 0; tt < KT; ++tt)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        s[rt][tt][r] = t0 + 32 * tt + 8 * (r / 4) + 4 * (lane >> 5) + r % 4 < seen[rt] ? s[rt][tt][r] : -INFINITY;
+        }
+        bf16x8 pf[RT][2 * KT];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            float mx = s[rt][0][0];
+#pragma unroll
+            for (int tt = 0; tt < KT; ++tt)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[rt][tt][r]);
+            mx = max_halves(mx);
+            if (__any((mx - top[rt]) * c > kSlack)) {   // -inf - -inf is NaN: no token yet, nothing to do
+                const float m_new = fmaxf(mx, top[rt]), base = m_new == -INFINITY ? 0.f : m_new;
+                const float keep = __builtin_amdgcn_exp2f((top[rt] - base) * c);
+                top[rt] = m_new;
+                l[rt] *= keep;
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) o[rt][d][r] *= keep;
+            }
+            const float mc = top[rt] == -INFINITY ? 0.f : top[rt] * c;
+            float sum = 0.f;
+#pragma unroll
+            for (int tt = 0; tt < KT; ++tt)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    u32x4 w;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[rt][tt][8 * u + 2 * x], c, -mc));
+                        const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[rt][tt][8 * u + 2 * x + 1], c, -mc));
+                        sum += p0 + p1;
+                        w[x] = pack_bf16(p0, p1);
+                    }
+                    pf[rt][2 * tt + u] = __builtin_bit_cast(bf16x8, w);
+                }
+            l[rt] += sum;
+        }
+        bool odd = false;                               // a value that is not finite where some row does not see it
+        if (masked) {
+            uint32_t high = 0;
+#pragma unroll
+            for (int st = 0; st < 2 * KT; ++st)
+#pragma unroll
+                for (int d = 0; d < DT; ++d) {
+                    const u32x4 w = __builtin_bit_cast(u32x4, value_frag(vb, st, d));
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) high |= ((w[x] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            odd = __any(high != 0);
+        }
+        if (!odd) {
+            bf16x8 vf[2][DT];                           // operands a step ahead
+#pragma unroll
+            for (int d = 0; d < DT; ++d) vf[0][d] = value_frag(vb, 0, d);
+#pragma unroll
+            for (int st = 0; st < 2 * KT; ++st) {
+                if (st + 1 < 2 * KT)
+#pragma unroll
+                    for (int d = 0; d < DT; ++d) vf[(st + 1) % 2][d] = value_frag(vb, st + 1, d);
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt)
+                        o[rt][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[st % 2][d], pf[rt][st], o[rt][d], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        } else {
+            // The product would carry 0 * Inf into rows that do not see the
+            // value.  The finite values go the same way; what is not finite
+            // is counted, up and down (NaN both ways), over the seen keys.
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                f32x16 up[RT], down[RT];
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) up[rt][r] = down[rt][r] = 0.f;
+#pragma unroll
+                for (int st = 0; st < 2 * KT; ++st) {
+                    const u32x4 w = __builtin_bit_cast(u32x4, value_frag(vb, st, d));
+                    u32x4 fin, pos, neg;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        fin[x] = pos[x] = neg[x] = 0;
+#pragma unroll
+                        for (int y = 0; y < 32; y += 16) {
+                            const uint32_t v = (w[x] >> y) & 0xFFFFu;
+                            const bool bad = (v & 0x7F80u) == 0x7F80u, nan = bad && (v & 0x7Fu) != 0;
+                            fin[x] |= (bad ? 0u : v) << y;
+                            pos[x] |= (bad && (nan || v < 0x8000u) ? 0x3F80u : 0u) << y;
+                            neg[x] |= (bad && (nan || v >= 0x8000u) ? 0x3F80u : 0u) << y;
+                        }
+                    }
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) {
+                        u32x4 one;
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const int key = t0 + 16 * st + 8 * (x / 2) + 4 * (lane >> 5) + 2 * (x % 2);
+                            one[x] = (key < seen[rt] ? 0x3F80u : 0u) | (key + 1 < seen[rt] ? 0x3F800000u : 0u);
+                        }
+                        o[rt][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, fin), pf[rt][st], o[rt][d], 0, 0, 0);
+                        up[rt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, pos), __builtin_bit_cast(bf16x8, one), up[rt], 0, 0, 0);
+                        down[rt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, neg), __builtin_bit_cast(bf16x8, one), down[rt], 0, 0, 0);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        o[rt][d][r] += (up[rt][r] > 0.f ? INFINITY : 0.f) + (down[rt][r] > 0.f ? -INFINITY : 0.f);
+            }
+        }
+    }
+
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        const float sum = sum_halves(l[rt]);
+        if (out_row[rt] < 0) continue;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int64_t to = out_row[rt] * D + 32 * d + 8 * x + 4 * (lane >> 5);
+                const float y0 = o[rt][d][4 * x] * inv, y1 = o[rt][d][4 * x + 1] * inv, y2 = o[rt][d][4 * x + 2] * inv,
+                            y3 = o[rt][d][4 * x + 3] * inv;
+                if (a.out_dtype == GRINQH_F32)
+                    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + to) = make_float4(y0, y1, y2, y3);
+                else
+                    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + to) = u32x2{pack_bf16(y0, y1), pack_bf16(y2, y3)};
+            }
+        if (a.lse != nullptr && lane < 32)
+            a.lse[out_row[rt]] = sum == 0.f ? -INFINITY : kLn2 * (top[rt] * c + __builtin_amdgcn_logf(sum));
+    }
+}
+
+template <int D>
+grinqh_status launch_prefill_attention(const Args& a, hipStream_t stream) {
+    const int64_t group = a.n_q_heads / a.n_kv_heads;
+    const int64_t tiles = a.total_q * group / PreShape<D>::kRows + a.batch;    // at most, whatever the lengths
+    if (tiles * a.n_kv_heads > kMaxPreGroups) return GRINQH_EINVAL;
+    const float c = a.scale == 0.f ? 1.f : fabsf(a.scale) * kLog2e;
+    prefill_attention_kernel<D><<<dim3(static_cast<unsigned>(tiles * a.n_kv_heads)), dim3(kPreThreads), 0, stream>>>(a, c);
+    return map_hip_error(hipGetLastError());
 }
 
 }  // namespace
@@ -109,10 +460,8 @@ extern "C" grinqh_status grinqh_prefill_attention(const grinqh_prefill_attention
     DeviceInfo dev;
     hipError_t e;
     if (!current_device_info(&dev, &e)) return map_hip_error(e);
-    const dim3 grid(static_cast<unsigned>(a.total_q), static_cast<unsigned>(a.n_q_heads));
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    if (a.head_dim == 64) prefill_attention_kernel<64><<<grid, dim3(kWave), 0, s>>>(a);
-    else if (a.head_dim == 128) prefill_attention_kernel<128><<<grid, dim3(kWave), 0, s>>>(a);
-    else prefill_attention_kernel<256><<<grid, dim3(kWave), 0, s>>>(a);
-    return map_hip_error(hipGetLastError());
+    if (a.head_dim == 64) return launch_prefill_attention<64>(a, s);
+    if (a.head_dim == 128) return launch_prefill_attention<128>(a, s);
+    return launch_prefill_attention<256>(a, s);
 }

@@ -34,7 +34,7 @@ __host__ __device__ __forceinline__ int64_t kv_row(const KvDims& d, int64_t slot
 
 // Largest sizes the calls accept.
 constexpr int kMaxKvHeads = 1024, kMaxQHeads = 1024;
-constexpr int64_t kMaxStride = int64_t{1} << 32;   // elements between tokens
+constexpr int64_t kMaxStride = int64_t{1} << 24;   // elements between tokens
 constexpr int kMaxBatch = 1 << 20, kMaxCacheLen = 1 << 28, kMaxPacked = 1 << 24;
 
 inline bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
