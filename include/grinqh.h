@@ -413,6 +413,12 @@ grinqh_status grinqh_decode_attention(const grinqh_kv_layout* L, const grinqh_kv
  *   out        [total_q][n_q_heads][head_dim] of out_dtype, contiguous, 16-byte
  *              aligned; rows behind the last sequence are left as they are.
  *   lse        fp32 [total_q][n_q_heads] or NULL.
+ *   workspace  NULL, or >= grinqh_prefill_attention_workspace_bytes(args) bytes,
+ *              256-byte aligned, any contents: with it the keys of few queries
+ *              are worked on in parts and joined by a second kernel.  The size
+ *              follows from the sizes in args and causal alone (0: it would not
+ *              be used, or a size is invalid).
+ * total_q * n_q_heads / 128 + batch * n_kv_heads is at most 2^23.
  * The weights p_t are rounded to bf16 for the product with the values. */
 typedef struct {
     const void* q;
@@ -428,7 +434,10 @@ typedef struct {
     void* out;
     grinqh_dtype out_dtype;
     float* lse;
+    void* workspace;
+    size_t workspace_bytes;
 } grinqh_prefill_attention_args;
+size_t grinqh_prefill_attention_workspace_bytes(const grinqh_prefill_attention_args* args);
 grinqh_status grinqh_prefill_attention(const grinqh_prefill_attention_args* args, void* stream);
 
 #ifdef __cplusplus

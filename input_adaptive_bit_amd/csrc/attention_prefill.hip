@@ -21,9 +21,12 @@
 // contraction as they are (the contraction's order is free), rounded to bf16
 // in place; V^T comes from LDS with transposing reads (ds_read_b64_tr_b16).
 //
-// The maximum follows only when a row's scores exceed it by 2^8: weights up to
-// 2^8 lose nothing in fp32 and bf16, and the sums are rarely rescaled.
+// The maximum is the first tile's until a score exceeds it by 30 (as powers of
+// two): weights up to 2^30 lose nothing in fp32 and bf16, and the sums are
+// hardly ever rescaled.
 #include <math.h>
+
+#include <algorithm>
 
 #include "internal.h"
 #include "kv_common.hpp"
@@ -43,7 +46,7 @@ constexpr int kPreWaves = 4;
 constexpr int kPreThreads = kPreWaves * kWave;
 constexpr int64_t kMaxPreGroups = 1 << 23;              // workgroups of a launch
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
-constexpr float kSlack = 8.f;                           // log2 by which scores may exceed the maximum in use
+constexpr float kSlack = 30.f;                          // log2 by which scores may exceed the maximum in use
 
 template <int D>
 struct PreShape {
@@ -99,6 +102,23 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, bf16x2{static_cast<__bf16>(lo), static_cast<__bf16>(hi)});
 }
 
+__device__ __forceinline__ void store_four(const Args& a, int64_t at, float y0, float y1, float y2, float y3) {
+    if (a.out_dtype == GRINQH_F32)
+        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(y0, y1, y2, y3);
+    else
+        *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + at) = u32x2{pack_bf16(y0, y1), pack_bf16(y2, y3)};
+}
+
+__device__ __forceinline__ float lse_of(float top, float sum, float c) {
+    return sum == 0.f ? -INFINITY : kLn2 * (top * c + __builtin_amdgcn_logf(sum));
+}
+
+// Where the workspace holds a part: its rows' sums, then their (maximum, weight).
+template <int D>
+__device__ __forceinline__ int64_t part_at(int number, int head, int part, int heads, int most_parts) {
+    return ((static_cast<int64_t>(number) * heads + head) * most_parts + part) * PreShape<D>::kRows * (D + 2);
+}
+
 // x of this lane and of the lane 32 further.
 __device__ __forceinline__ float max_halves(float x) {
     const u32x2 r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -109,17 +129,30 @@ __device__ __forceinline__ float sum_halves(float x) {
     return __uint_as_float(r.x) + __uint_as_float(r.y);
 }
 
-// Where a flat tile number lies: its sequence and tile, both -1 past the last.
+// Where a flat tile number lies: its sequence, the tile in it, and how many
+// tiles the sequence has; seq -1 past the last.  Up to 64 sequences are taken
+// from the longest to the shortest, so that the launch ends on short ones.
 struct Place {
     int seq, tile, tiles;
 };
 __device__ __forceinline__ Place find_tile(const Args& a, int group, int rows, int number, int lane) {
     int before = 0;
     for (int b0 = 0; b0 < a.batch; b0 += kWave) {
-        int tiles = 0;
-        if (b0 + lane < a.batch) {
-            const int q0 = min(max(a.cu_q[b0 + lane], 0), a.total_q), q1 = min(max(a.cu_q[b0 + lane + 1], 0), a.total_q);
+        int tiles = 0, seq = b0 + lane;
+        if (seq < a.batch) {
+            const int q0 = min(max(a.cu_q[seq], 0), a.total_q), q1 = min(max(a.cu_q[seq + 1], 0), a.total_q);
             tiles = static_cast<int>((static_cast<int64_t>(max(q1 - q0, 0)) * group + rows - 1) / rows);
+        }
+        if (a.batch > 1 && a.batch <= kWave) {
+            int rank = 0;
+            for (int b = 0; b < a.batch; ++b) {
+                const int other = __builtin_amdgcn_readlane(tiles, b);
+                rank += other > tiles || (other == tiles && b < lane);
+            }
+            // lane -> lane of its rank (lanes past the last sequence keep their place)
+            const int to = 4 * (lane < a.batch ? rank : lane);
+            tiles = __builtin_amdgcn_ds_permute(to, tiles);
+            seq = __builtin_amdgcn_ds_permute(to, seq);
         }
         int sum = tiles;
 #pragma unroll
@@ -131,15 +164,26 @@ __device__ __forceinline__ Place find_tile(const Args& a, int group, int rows, i
         if (over != 0) {
             const int at = __builtin_ctzll(over);
             const int upto = __shfl(sum, at), mine = __shfl(tiles, at);
-            return Place{b0 + at, number - (before + upto - mine), mine};
+            return Place{__shfl(seq, at), number - (before + upto - mine), mine};
         }
         before += __shfl(sum, kWave - 1);
     }
     return Place{-1, -1, 0};
 }
 
+// How a call is cut up (host arithmetic on its sizes alone).
+struct PrePlan {
+    int64_t tiles;          // row tiles of a key-value head, at most
+    int parts;              // parts of a tile's keys, at most
+    size_t ws_bytes;
+};
+
+// Parts of a tile that sees `keys` keys: whole tiles of at least kMinPart keys.
+constexpr int kMinPart = 256, kMaxParts = 32, kCus = 256;
+__device__ __forceinline__ int parts_of(int keys, int most) { return max(1, min(most, keys / kMinPart)); }
+
 template <int D>
-__global__ __launch_bounds__(kPreThreads, D == 256 ? 1 : 2) void prefill_attention_kernel(Args a, float c) {
+__global__ __launch_bounds__(kPreThreads, D == 256 ? 1 : 2) void prefill_attention_kernel(Args a, float c, int most_parts) {
     using S = PreShape<D>;
     constexpr int RT = S::kRT, TK = S::kTK, KT = TK / 32, DT = D / 32;
     __shared__ __attribute__((aligned(1024))) char lds[2][2][S::kBytes];       // [buffer][keys, values]
@@ -147,7 +191,9 @@ __global__ __launch_bounds__(kPreThreads, D == 256 ? 1 : 2) void prefill_attenti
     const int group = a.n_q_heads / a.n_kv_heads;
     // Heads are the fast index, so that with eight of them each XCD's L2 keeps one head's keys.
     const int head = blockIdx.x % a.n_kv_heads;
-    const Place at = find_tile(a, group, S::kRows, blockIdx.x / a.n_kv_heads, lane);
+    const int flat = blockIdx.x / a.n_kv_heads;             // and parts within a tile the next
+    const int number = flat / most_parts, part = flat % most_parts;
+    const Place at = find_tile(a, group, S::kRows, number, lane);
     if (at.seq < 0) return;
     const int seq = __builtin_amdgcn_readfirstlane(at.seq);
     // The last tiles of a causal sequence see the most keys and go first.
@@ -166,6 +212,12 @@ __global__ __launch_bounds__(kPreThreads, D == 256 ? 1 : 2) void prefill_attenti
     const int wave_end = seen_by(min(query_of(local0 + 32 * RT - 1), n - 1));  // any row of the wave
     const int wave_full = seen_by(query_of(local0));                           // all rows of the wave
     const bool idle = query_of(local0) >= n;                                   // no row of the wave exists
+
+    // This workgroup's part of the tile's keys, in whole tiles of keys.
+    const int parts = parts_of(all_end, most_parts);
+    if (part >= parts) return;
+    const int all_tiles = (all_end + TK - 1) / TK;
+    const int first = part * all_tiles / parts, tiles = (part + 1) * all_tiles / parts;
 
     bf16x8 qf[RT][D / 16];
     int seen[RT];
@@ -229,13 +281,22 @@ __global__ __launch_bounds__(kPreThreads, D == 256 ? 1 : 2) void prefill_attenti
         return __builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
     };
 
-    const int tiles = (all_end + TK - 1) / TK;
-    if (tiles > 0) load(0, 0);
-    for (int t = 0; t < tiles; ++t) {
+    if (first < tiles) load(first * TK, first & 1);
+    // A row whose scores pass its maximum by too much leaves the inner loop, so
+    // that the loop itself never touches the output sums but to add to them,
+    // and comes back to the same tile with the new maximum.
+    float mx[RT];
+    bool again = false;
+    for (int t = first;; again = true) {
+      bool passed = false;
+      for (; t < tiles; ++t) {
         const int t0 = t * TK;
-        __builtin_amdgcn_s_waitcnt(0);                  // this wave's share of the tile has arrived
-        __syncthreads();                                // everyone's has; and the other buffer is free
-        if (t + 1 < tiles) load(t0 + TK, (t + 1) & 1);
+        if (!again) {
+            __builtin_amdgcn_s_waitcnt(0);              // this wave's share of the tile has arrived
+            __syncthreads();                            // everyone's has; and the other buffer is free
+            if (t + 1 < tiles) load(t0 + TK, (t + 1) & 1);
+        }
+        again = false;
         if (idle || t0 >= wave_end) continue;
         const char* kb = lds[t & 1][0];
         const char* vb = lds[t & 1][1];
@@ -275,25 +336,22 @@ __global__ __launch_bounds__(kPreThreads, D == 256 ? 1 : 2) void prefill_attenti
                     for (int r = 0; r < 16; ++r)
                         s[rt][tt][r] = t0 + 32 * tt + 8 * (r / 4) + 4 * (lane >> 5) + r % 4 < seen[rt] ? s[rt][tt][r] : -INFINITY;
         }
-        bf16x8 pf[RT][2 * KT];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-            float mx = s[rt][0][0];
+            mx[rt] = s[rt][0][0];
 #pragma unroll
             for (int tt = 0; tt < KT; ++tt)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[rt][tt][r]);
-            mx = max_halves(mx);
-            if (__any((mx - top[rt]) * c > kSlack)) {   // -inf - -inf is NaN: no token yet, nothing to do
-                const float m_new = fmaxf(mx, top[rt]), base = m_new == -INFINITY ? 0.f : m_new;
-                const float keep = __builtin_amdgcn_exp2f((top[rt] - base) * c);
-                top[rt] = m_new;
-                l[rt] *= keep;
+                for (int r = 0; r < 16; ++r) mx[rt] = fmaxf(mx[rt], s[rt][tt][r]);
+            mx[rt] = max_halves(mx[rt]);
+            top[rt] = top[rt] == -INFINITY ? mx[rt] : top[rt];                 // nothing summed yet
+            passed |= (mx[rt] - top[rt]) * c > kSlack;                         // (no if both are infinite: NaN)
+        }
+        passed = __any(passed);
+        if (passed) break;
+        bf16x8 pf[RT][2 * KT];
 #pragma unroll
-                for (int d = 0; d < DT; ++d)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) o[rt][d][r] *= keep;
-            }
+        for (int rt = 0; rt < RT; ++rt) {
             const float mc = top[rt] == -INFINITY ? 0.f : top[rt] * c;
             float sum = 0.f;
 #pragma unroll
@@ -390,8 +448,37 @@ __global__ __launch_bounds__(kPreThreads, D == 256 ? 1 : 2) void prefill_attenti
                         o[rt][d][r] += (up[rt][r] > 0.f ? INFINITY : 0.f) + (down[rt][r] > 0.f ? -INFINITY : 0.f);
             }
         }
+      }
+      if (!passed) break;
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+          const float m_new = (mx[rt] - top[rt]) * c > kSlack ? mx[rt] : top[rt];
+          const float keep = m_new == top[rt] ? 1.f : __builtin_amdgcn_exp2f((top[rt] - m_new) * c);
+          top[rt] = m_new;
+          l[rt] *= keep;
+#pragma unroll
+          for (int d = 0; d < DT; ++d)
+#pragma unroll
+              for (int r = 0; r < 16; ++r) o[rt][d][r] *= keep;
+      }
     }
 
+    if (parts > 1) {        // sums, maximum and weight for join_kernel
+        float* to = static_cast<float*>(a.workspace) + part_at<D>(number, head, part, a.n_kv_heads, most_parts);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            const int local = local0 + 32 * rt + (lane & 31);
+            const float sum = sum_halves(l[rt]);
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    *reinterpret_cast<float4*>(to + local * D + 32 * d + 8 * x + 4 * (lane >> 5)) =
+                        make_float4(o[rt][d][4 * x], o[rt][d][4 * x + 1], o[rt][d][4 * x + 2], o[rt][d][4 * x + 3]);
+            if (lane < 32) *reinterpret_cast<float2*>(to + S::kRows * D + 2 * local) = make_float2(top[rt], sum);
+        }
+        return;
+    }
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
         const float sum = sum_halves(l[rt]);
@@ -400,27 +487,105 @@ __global__ __launch_bounds__(kPreThreads, D == 256 ? 1 : 2) void prefill_attenti
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int64_t to = out_row[rt] * D + 32 * d + 8 * x + 4 * (lane >> 5);
-                const float y0 = o[rt][d][4 * x] * inv, y1 = o[rt][d][4 * x + 1] * inv, y2 = o[rt][d][4 * x + 2] * inv,
-                            y3 = o[rt][d][4 * x + 3] * inv;
-                if (a.out_dtype == GRINQH_F32)
-                    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + to) = make_float4(y0, y1, y2, y3);
-                else
-                    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + to) = u32x2{pack_bf16(y0, y1), pack_bf16(y2, y3)};
-            }
-        if (a.lse != nullptr && lane < 32)
-            a.lse[out_row[rt]] = sum == 0.f ? -INFINITY : kLn2 * (top[rt] * c + __builtin_amdgcn_logf(sum));
+            for (int x = 0; x < 4; ++x)
+                store_four(a, out_row[rt] * D + 32 * d + 8 * x + 4 * (lane >> 5), o[rt][d][4 * x] * inv,
+                           o[rt][d][4 * x + 1] * inv, o[rt][d][4 * x + 2] * inv, o[rt][d][4 * x + 3] * inv);
+        if (a.lse != nullptr && lane < 32) a.lse[out_row[rt]] = lse_of(top[rt], sum, c);
+    }
+}
+
+// Joins the parts of every tile that has several.  A workgroup takes
+// kJoinRows rows of a tile; D / 4 lanes hold a row, four values each.
+constexpr int kJoinRows = 32;
+
+template <int D>
+__global__ __launch_bounds__(kPreThreads) void join_kernel(Args a, float c, int most_parts) {
+    using S = PreShape<D>;
+    const int lane = threadIdx.x & 63, group = a.n_q_heads / a.n_kv_heads;
+    const int head = blockIdx.x % a.n_kv_heads, number = blockIdx.x / a.n_kv_heads;
+    const Place at = find_tile(a, group, S::kRows, number, lane);
+    if (at.seq < 0) return;
+    const int seq = at.seq, tile = a.causal ? at.tiles - 1 - at.tile : at.tile;
+    const int q_begin = min(max(a.cu_q[seq], 0), a.total_q), q_end = min(max(a.cu_q[seq + 1], 0), a.total_q);
+    const int k_begin = min(max(a.cu_k[seq], 0), a.total_k);
+    const int n = q_end - q_begin, m = max(min(max(a.cu_k[seq + 1], 0), a.total_k) - k_begin, 0);
+    const int64_t row0 = static_cast<int64_t>(tile) * S::kRows;
+    const int i0 = static_cast<int>(row0 / group), rem0 = static_cast<int>(row0 % group);
+    const int last = min(i0 + (rem0 + S::kRows - 1) / group, n - 1);
+    const int parts = parts_of(a.causal ? min(max(last + m - n + 1, 0), m) : m, most_parts);
+    if (parts == 1) return;
+    const float* from = static_cast<const float*>(a.workspace) + part_at<D>(number, head, 0, a.n_kv_heads, most_parts);
+    const int64_t step = part_at<D>(0, 0, 1, a.n_kv_heads, most_parts);
+    constexpr int kPerRow = D / 4;
+    for (int u = threadIdx.x; u < kJoinRows * kPerRow; u += kPreThreads) {
+        const int local = blockIdx.y * kJoinRows + u / kPerRow, x = u % kPerRow * 4;
+        const int i = i0 + (rem0 + local) / group, h = head * group + (rem0 + local) % group;
+        if (i >= n) continue;
+        float top = -INFINITY;
+        for (int p = 0; p < parts; ++p) top = fmaxf(top, from[p * step + S::kRows * D + 2 * local]);
+        const float base = top == -INFINITY ? 0.f : top;
+        float l = 0.f;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int p = 0; p < parts; ++p) {
+            const float2 ml = *reinterpret_cast<const float2*>(from + p * step + S::kRows * D + 2 * local);
+            const float4 v = *reinterpret_cast<const float4*>(from + p * step + local * D + x);
+            const float f = __builtin_amdgcn_exp2f((ml.x - base) * c);
+            l = __builtin_fmaf(f, ml.y, l);
+            y = make_float4(__builtin_fmaf(f, v.x, y.x), __builtin_fmaf(f, v.y, y.y), __builtin_fmaf(f, v.z, y.z),
+                            __builtin_fmaf(f, v.w, y.w));
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int64_t row = static_cast<int64_t>(q_begin + i) * a.n_q_heads + h;
+        store_four(a, row * D + x, y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+        if (a.lse != nullptr && x == 0) a.lse[row] = lse_of(top, l, c);
     }
 }
 
 template <int D>
-grinqh_status launch_prefill_attention(const Args& a, hipStream_t stream) {
+PrePlan plan_prefill(const Args& a) {
+    PrePlan p;
     const int64_t group = a.n_q_heads / a.n_kv_heads;
-    const int64_t tiles = a.total_q * group / PreShape<D>::kRows + a.batch;    // at most, whatever the lengths
-    if (tiles * a.n_kv_heads > kMaxPreGroups) return GRINQH_EINVAL;
+    p.tiles = a.total_q * group / PreShape<D>::kRows + a.batch;                // at most, whatever the lengths
+    // Parts where they make the call shorter, by what was measured: a tile of keys
+    // takes a workgroup alone on its CU t us, two on one CU 1.6 times that (at
+    // head_dim 256 there is room for one), and the parts cost a second launch and
+    // their way through memory.  Two prompts of 257 and 512 queries after 6000
+    // keys, 28 heads of 64, in 1 to 5 parts: 113, 85, 97, 79, 80 us; 512 after 7680,
+    // 32 heads of 128, in 1, 3, 4, 5: 189, 108, 96, 117; 1024 queries of a prompt: 35
+    // whole, 43 in two.
+    const int64_t rows = PreShape<D>::kRows, groups = (a.total_q * group + rows - 1) / rows * a.n_kv_heads;
+    const double keys = (a.total_k - (a.causal ? 0.5 * a.total_q : 0.0)) / std::max(1, a.batch);
+    const double t = (D == 64 ? 1.1 : D == 128 ? 1.5 : 1.9) * keys / PreShape<D>::kTK;
+    const auto cost = [&](int64_t parts) {
+        const int64_t deep = (groups * parts + kCus - 1) / kCus;               // workgroups on the fullest CU
+        const double rounds = D == 256 ? deep : deep / 2 * 1.6 + deep % 2;
+        const double bytes = 2.0 * groups * parts * rows * (D + 2) * sizeof(float);
+        return t * rounds / parts + (parts > 1 ? 5.0 + bytes / 5e6 : 0.0);
+    };
+    p.parts = 1;
+    if (groups < 3 * kCus)
+        for (int parts = 2; parts <= std::min(kMaxParts, a.total_k / kMinPart); ++parts)
+            if (cost(parts) < cost(p.parts)) p.parts = parts;
+    p.ws_bytes = p.parts > 1 ? static_cast<size_t>(p.tiles) * a.n_kv_heads * p.parts * PreShape<D>::kRows * (D + 2) * sizeof(float) : 0;
+    return p;
+}
+
+template <int D>
+size_t prefill_workspace(const Args& a) {
+    return plan_prefill<D>(a).ws_bytes;
+}
+
+template <int D>
+grinqh_status launch_prefill_attention(const Args& a, hipStream_t stream) {
+    PrePlan p = plan_prefill<D>(a);
+    if (p.tiles * a.n_kv_heads > kMaxPreGroups) return GRINQH_EINVAL;
+    if (a.workspace == nullptr) p.parts = 1;
+    else if (a.workspace_bytes < p.ws_bytes) return GRINQH_ENOSPACE;
     const float c = a.scale == 0.f ? 1.f : fabsf(a.scale) * kLog2e;
-    prefill_attention_kernel<D><<<dim3(static_cast<unsigned>(tiles * a.n_kv_heads)), dim3(kPreThreads), 0, stream>>>(a, c);
+    const unsigned n = static_cast<unsigned>(p.tiles * a.n_kv_heads);
+    prefill_attention_kernel<D><<<dim3(n * p.parts), dim3(kPreThreads), 0, stream>>>(a, c, p.parts);
+    if (p.parts > 1)
+        join_kernel<D><<<dim3(n, PreShape<D>::kRows / kJoinRows), dim3(kPreThreads), 0, stream>>>(a, c, p.parts);
     return map_hip_error(hipGetLastError());
 }
 
@@ -429,9 +594,10 @@ grinqh_status launch_prefill_attention(const Args& a, hipStream_t stream) {
 
 using namespace grinqh;
 
-extern "C" grinqh_status grinqh_prefill_attention(const grinqh_prefill_attention_args* args, void* stream) {
-    if (args == nullptr) return GRINQH_EINVAL;
-    const Args& a = *args;
+namespace {
+
+// Sizes and types: what the workspace depends on.
+grinqh_status check_sizes(const Args& a) {
     if (a.batch < 0 || a.batch > kMaxBatch || a.total_q < 0 || a.total_q > kMaxPacked || a.total_k < 0 ||
         a.total_k > kMaxPacked)
         return GRINQH_EINVAL;
@@ -440,6 +606,23 @@ extern "C" grinqh_status grinqh_prefill_attention(const grinqh_prefill_attention
         a.n_q_heads % a.n_kv_heads != 0 || !isfinite(a.scale))
         return GRINQH_EINVAL;
     if (a.out_dtype != GRINQH_BF16 && a.out_dtype != GRINQH_F32) return GRINQH_EINVAL;
+    return GRINQH_OK;
+}
+
+}  // namespace
+
+extern "C" size_t grinqh_prefill_attention_workspace_bytes(const grinqh_prefill_attention_args* args) {
+    if (args == nullptr || check_sizes(*args) != GRINQH_OK) return 0;
+    if (args->head_dim == 64) return prefill_workspace<64>(*args);
+    if (args->head_dim == 128) return prefill_workspace<128>(*args);
+    return prefill_workspace<256>(*args);
+}
+
+extern "C" grinqh_status grinqh_prefill_attention(const grinqh_prefill_attention_args* args, void* stream) {
+    if (args == nullptr) return GRINQH_EINVAL;
+    const Args& a = *args;
+    const grinqh_status st = check_sizes(a);
+    if (st != GRINQH_OK) return st;
     if (a.batch == 0 || a.total_q == 0) return GRINQH_OK;
     if (a.q == nullptr || a.cu_q == nullptr || a.cu_k == nullptr || a.out == nullptr) return GRINQH_EINVAL;
     if (a.total_k > 0 && (a.k == nullptr || a.v == nullptr)) return GRINQH_EINVAL;
@@ -449,7 +632,7 @@ extern "C" grinqh_status grinqh_prefill_attention(const grinqh_prefill_attention
         return GRINQH_EINVAL;
     if (!aligned_to(a.q, 16) || !aligned_to(a.k, 16) || !aligned_to(a.v, 16) || a.q_stride % 8 != 0 ||
         a.k_stride % 8 != 0 || a.v_stride % 8 != 0 || !aligned_to(a.cu_q, 4) || !aligned_to(a.cu_k, 4) ||
-        !aligned_to(a.out, 16) || !aligned_to(a.lse, 4))
+        !aligned_to(a.out, 16) || !aligned_to(a.lse, 4) || !aligned_to(a.workspace, 256))
         return GRINQH_EALIGN;
     const size_t out_bytes = static_cast<size_t>(a.total_q) * qw * (a.out_dtype == GRINQH_BF16 ? 2 : 4);
     if (overlaps(a.q, static_cast<size_t>((a.total_q - 1) * a.q_stride + qw) * 2, a.out, out_bytes)) return GRINQH_EINVAL;

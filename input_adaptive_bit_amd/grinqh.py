@@ -63,7 +63,8 @@ class PrefillAttentionArgs(ctypes.Structure):
                 ("batch", ctypes.c_int32), ("total_q", ctypes.c_int32), ("total_k", ctypes.c_int32),
                 ("n_q_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("causal", ctypes.c_int32), ("scale", ctypes.c_float), ("out", ctypes.c_void_p),
-                ("out_dtype", ctypes.c_int), ("lse", ctypes.c_void_p)]
+                ("out_dtype", ctypes.c_int), ("lse", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t)]
 
 
 MAX_GROUP = 8
@@ -76,7 +77,7 @@ EXPORTS = ("grinqh_version", "grinqh_status_string", "grinqh_layout_init", "grin
            "grinqh_prefill_workspace_bytes", "grinqh_prefill_gemm",
            "grinqh_kv_layout_init", "grinqh_kv_code_bytes", "grinqh_kv_grid_bytes", "grinqh_kv_write",
            "grinqh_kv_read", "grinqh_debug_kv_row", "grinqh_attention_workspace_bytes",
-           "grinqh_decode_attention", "grinqh_prefill_attention")
+           "grinqh_decode_attention", "grinqh_prefill_attention", "grinqh_prefill_attention_workspace_bytes")
 
 _lib = None
 
@@ -157,6 +158,8 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.grinqh_decode_attention.restype = ctypes.c_int
     lib.grinqh_prefill_attention.argtypes = [ctypes.POINTER(PrefillAttentionArgs), vp]
     lib.grinqh_prefill_attention.restype = ctypes.c_int
+    lib.grinqh_prefill_attention_workspace_bytes.argtypes = [ctypes.POINTER(PrefillAttentionArgs)]
+    lib.grinqh_prefill_attention_workspace_bytes.restype = sz
     if path is None:
         _lib = lib
     return lib

@@ -296,6 +296,37 @@ def test_prefill_with_other_numbers_of_keys_than_queries(dev, causal, dim, lens_
     _prefill(*_packed(rng, 4, 2, dim, lens_q, lens_k), dev, causal, "f32")
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dim,n_kv,group,lens_q,lens_k", [
+    (128, 2, 4, [40], [5000]),
+    (64, 1, 7, [9, 60, 3], [2100, 60, 1023]),             # parts for some, one for others
+    (256, 1, 2, [20, 1], [1100, 2500]),
+    (128, 1, 1, [1], [4111]),
+    (64, 2, 3, [600, 30], [580, 3000]),                   # rows that see nothing beside split ones
+])
+def test_few_queries_over_many_keys_in_parts(dev, causal, dim, n_kv, group, lens_q, lens_k):
+    import input_adaptive_bit_amd as G
+    import torch
+    say(f"prefill parts dim={dim} q={lens_q} k={lens_k} causal={causal}")
+    rng = np.random.default_rng(sum(lens_k) + dim)
+    q, k, v, cu_q, cu_k = _packed(rng, n_kv * group, n_kv, dim, lens_q, lens_k)
+    o, bound, l, l_bound = prefill_reference(q, k, v, cu_q, cu_k, dim ** -0.5, causal, "f32")
+    t = [to_bf16(x, dev) for x in (q, k, v)] + [torch.from_numpy(x).to(dev) for x in (cu_q, cu_k)]
+    out, lse = G.prefill_attention(*t, causal, out_dtype=torch.float32, return_lse=True)
+    n = G.grinqh_prefill_attention_workspace_bytes(*t, out, causal)
+    assert n > 0, "the case is one whose keys are split"
+    inside(_np(out), o, bound, "split")
+    inside(_np(lse), l, l_bound, "split lse")
+    again = torch.empty_like(out)
+    ws = torch.full((n,), 0xFF, dtype=torch.uint8, device=dev)                    # any contents
+    G.grinqh_prefill_attention(*t, again, causal, workspace=ws)
+    assert torch.equal(out, again)
+    G.grinqh_prefill_attention(*t, again, causal)
+    inside(_np(again), o, bound, "without a workspace")
+    with pytest.raises(G.GrinqhError):
+        G.grinqh_prefill_attention(*t, again, causal, workspace=ws[:256])
+
+
 def test_rows_behind_the_last_sequence_and_batches_of_many(dev):
     rng = np.random.default_rng(3)
     _prefill(*_packed(rng, 2, 1, 64, [3, 50], [3, 50], extra=150), dev)
