@@ -50,9 +50,8 @@ constexpr float kSlack = 30.f;                          // log2 by which scores 
 
 template <int D>
 struct PreShape {
-    static constexpr int kRT = 1;                       // 32-row tiles of a wave
-    static constexpr int kRows = kPreWaves * 32 * kRT;  // rows of a workgroup
-    static constexpr int kTK = D == 256 ? 32 : 64;      // keys of a tile
+    static constexpr int kRows = kPreWaves * 32;        // rows of a workgroup
+    static constexpr int kTK = 64;                      // keys of a tile
     static constexpr int kChunks = D / 8;               // 16-byte chunks of a key
     static constexpr int kBytes = kTK * D * 2;          // of a tile of keys (or values)
 };
@@ -77,26 +76,44 @@ __device__ __forceinline__ i32x4 rows_rsrc(const uint16_t* base, int rows, uint3
     return i32x4{static_cast<int>(at), static_cast<int>(at >> 32) & 0xFFFF, static_cast<int>(bytes), 0x00020000};
 }
 
-// Loads a tile of keys or values (`rows` of them exist) into LDS: 16-byte chunks
-// in the order of LDS, chunk c of row r at c ^ swizzle(r) (so that the operand
-// reads of neighbouring rows fall on different banks).  `off` is the lane's
-// offset (tile_offset); the rows a load starts at move the buffer.
-template <int D>
-__device__ __forceinline__ void load_tile(const uint16_t* base, int rows, int64_t stride, uint32_t off, uint32_t lds, int wave) {
-    using S = PreShape<D>;
-    constexpr int kRowsAtOnce = kPreThreads / S::kChunks;
-    const uint32_t stride_bytes = static_cast<uint32_t>(stride) * 2;
-#pragma unroll
-    for (int n = 0; n < S::kTK / kRowsAtOnce; ++n)
-        load_to_lds(rows_rsrc(base + n * kRowsAtOnce * stride, rows - n * kRowsAtOnce, stride_bytes, D * 2), off,
-                    lds + (n * kPreThreads + wave * kWave) * 16);
+// A tile lies in LDS as rows of 2 D bytes, chunk c (16 bytes) of row r at
+// c ^ swizzle(r): the 16 rows that one step of a key operand's read touches fall
+// on different banks, and so do the 4 rows x 4 chunks of a value operand's.
+template <int D, bool VALUES>
+__device__ __forceinline__ constexpr int swizzle(int r) {
+    if (VALUES) return D == 64 ? (r & 2) << 1 : (r & 3) << 2;
+    return D == 64 ? (r & 7) ^ (r >> 3 & 1) : r & 15;
 }
 
+// Loads a tile (`rows` of it exist) into LDS in the order of LDS.  The lane's
+// chunk changes from one load to the next where they are 8 rows apart (keys of
+// head_dim 256).
 template <int D, bool VALUES>
-__device__ __forceinline__ uint32_t tile_offset(int64_t stride, int thread) {
-    const int r = thread / PreShape<D>::kChunks, slot = thread % PreShape<D>::kChunks;
-    return r * static_cast<uint32_t>(stride) * 2 + (slot ^ (VALUES ? (r & 3) << 1 : r & 7)) * 16;
-}
+struct TileLoad {
+    static constexpr int kRowsAtOnce = kPreThreads / PreShape<D>::kChunks, kOffsets = kRowsAtOnce < 16 && !VALUES ? 2 : 1;
+    uint32_t off[kOffsets];
+    __device__ __forceinline__ TileLoad(int64_t stride) {
+        const int r = threadIdx.x / PreShape<D>::kChunks, slot = threadIdx.x % PreShape<D>::kChunks;
+#pragma unroll
+        for (int x = 0; x < kOffsets; ++x)
+            off[x] = r * static_cast<uint32_t>(stride) * 2 + (slot ^ swizzle<D, VALUES>(r + x * kRowsAtOnce)) * 16;
+    }
+    __device__ __forceinline__ void operator()(const uint16_t* base, int rows, int64_t stride, uint32_t lds, int wave) const {
+        const uint32_t stride_bytes = static_cast<uint32_t>(stride) * 2;
+        const i32x4 rs = rows_rsrc(base, rows, stride_bytes, D * 2);
+        uint32_t at[kOffsets];
+#pragma unroll
+        for (int x = 0; x < kOffsets; ++x) {
+            at[x] = off[x] + x * kRowsAtOnce * stride_bytes;
+            asm volatile("" : "+v"(at[x]));             // one register each, not one for every load of the loop
+        }
+#pragma unroll
+        for (int n = 0; n < PreShape<D>::kTK / kRowsAtOnce; ++n) {
+            load_to_lds(rs, at[n % kOffsets], lds + (n * kPreThreads + wave * kWave) * 16);
+            at[n % kOffsets] += kOffsets * kRowsAtOnce * stride_bytes;
+        }
+    }
+};
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, bf16x2{static_cast<__bf16>(lo), static_cast<__bf16>(hi)});
@@ -183,9 +200,9 @@ constexpr int kMinPart = 256, kMaxParts = 32, kCus = 256;
 __device__ __forceinline__ int parts_of(int keys, int most) { return max(1, min(most, keys / kMinPart)); }
 
 template <int D>
-__global__ __launch_bounds__(kPreThreads, D == 256 ? 1 : 2) void prefill_attention_kernel(Args a, float c, int most_parts) {
+__global__ __launch_bounds__(kPreThreads, D == 256 ? 1 : D == 64 ? 3 : 2) void prefill_attention_kernel(Args a, float c, int most_parts) {
     using S = PreShape<D>;
-    constexpr int RT = S::kRT, TK = S::kTK, KT = TK / 32, DT = D / 32;
+    constexpr int TK = S::kTK, KK = D / 16, DT = D / 32;
     __shared__ __attribute__((aligned(1024))) char lds[2][2][S::kBytes];       // [buffer][keys, values]
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int group = a.n_q_heads / a.n_kv_heads;
@@ -207,9 +224,9 @@ __global__ __launch_bounds__(kPreThreads, D == 256 ? 1 : 2) void prefill_attenti
     const int i0 = static_cast<int>(row0 / group), rem0 = static_cast<int>(row0 % group);
     const auto query_of = [&](int local) { return i0 + (rem0 + local) / group; };
     const auto seen_by = [&](int i) { return a.causal ? min(max(i + m - n + 1, 0), m) : m; };   // keys 0 .. that - 1
-    const int local0 = wave * 32 * RT;
+    const int local0 = wave * 32;
     const int all_end = seen_by(min(query_of(S::kRows - 1), n - 1));           // keys any row of the workgroup sees
-    const int wave_end = seen_by(min(query_of(local0 + 32 * RT - 1), n - 1));  // any row of the wave
+    const int wave_end = seen_by(min(query_of(local0 + 31), n - 1));  // any row of the wave
     const int wave_full = seen_by(query_of(local0));                           // all rows of the wave
     const bool idle = query_of(local0) >= n;                                   // no row of the wave exists
 
@@ -219,76 +236,94 @@ __global__ __launch_bounds__(kPreThreads, D == 256 ? 1 : 2) void prefill_attenti
     const int all_tiles = (all_end + TK - 1) / TK;
     const int first = part * all_tiles / parts, tiles = (part + 1) * all_tiles / parts;
 
-    bf16x8 qf[RT][D / 16];
-    int seen[RT];
-    int64_t out_row[RT];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        const int local = local0 + 32 * rt + (lane & 31);
-        const int i = query_of(local), h = head * group + (rem0 + local) % group;
-        const bool there = i < n;
-        seen[rt] = there ? seen_by(i) : 0;
-        out_row[rt] = there ? static_cast<int64_t>(q_begin + i) * a.n_q_heads + h : -1;
+    // This lane's row.
+    const int local = local0 + (lane & 31), i = query_of(local), h = head * group + (rem0 + local) % group;
+    const bool there = i < n;
+    const int seen = there ? seen_by(i) : 0;
+    const int64_t out_row = there ? static_cast<int64_t>(q_begin + i) * a.n_q_heads + h : -1;
+    bf16x8 qf[KK];
+    {
         const uint16_t* q = static_cast<const uint16_t*>(a.q) + (q_begin + (there ? i : 0)) * a.q_stride + (there ? h : 0) * D;
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
+        for (int kk = 0; kk < KK; ++kk) {
             u32x4 x = *reinterpret_cast<const u32x4*>(q + 16 * kk + 8 * (lane >> 5));
             if (a.scale < 0.f) x ^= 0x80008000u;                               // c is |scale| log2 e
             if (a.scale == 0.f) x = u32x4{0u, 0u, 0u, 0u};
-            qf[rt][kk] = __builtin_bit_cast(bf16x8, x);
+            qf[kk] = __builtin_bit_cast(bf16x8, x);
         }
     }
 
-    f32x16 o[RT][DT];
-    float top[RT], l[RT];
+    f32x16 o[DT];
+    float top = -INFINITY, l = 0.f;
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        top[rt] = -INFINITY;
-        l[rt] = 0.f;
+    for (int d = 0; d < DT; ++d)
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) o[rt][d][r] = 0.f;
-    }
+        for (int r = 0; r < 16; ++r) o[d][r] = 0.f;
 
     const uint16_t* keys = static_cast<const uint16_t*>(a.k) + k_begin * a.k_stride + head * D;
     const uint16_t* values = static_cast<const uint16_t*>(a.v) + k_begin * a.v_stride + head * D;
-    const uint32_t ks = tile_offset<D, false>(a.k_stride, threadIdx.x), vs = tile_offset<D, true>(a.v_stride, threadIdx.x);
+    const TileLoad<D, false> load_keys(a.k_stride);
+    const TileLoad<D, true> load_values(a.v_stride);
     const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)&lds[0][0][0]));
     const auto load = [&](int t0, int buf) {
-        load_tile<D>(keys + t0 * a.k_stride, m - t0, a.k_stride, ks, lds0 + buf * 2 * S::kBytes, wave);
-        load_tile<D>(values + t0 * a.v_stride, m - t0, a.v_stride, vs, lds0 + (2 * buf + 1) * S::kBytes, wave);
+        load_keys(keys + t0 * a.k_stride, m - t0, a.k_stride, lds0 + buf * 2 * S::kBytes, wave);
+        load_values(values + t0 * a.v_stride, m - t0, a.v_stride, lds0 + (2 * buf + 1) * S::kBytes, wave);
     };
-    // Byte offsets of this lane's operand reads (see load_tile): keys by step
-    // modulo 4, values by dimension tile modulo 2.
-    uint32_t k_off[4], v_off[2];
+    // Operand reads: this lane's place in a tile; steps and dimension tiles only
+    // flip bits of the chunk.
+    const uint32_t k_at = (lane & 31) * D * 2 + (((lane >> 5) ^ swizzle<D, false>(lane & 31)) * 16);
+    uint32_t v_at;
     {
-        const int r = lane & 31, i = lane & 15;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) k_off[x] = r * D * 2 + (((2 * x + (lane >> 5)) ^ (r & 7)) * 16);
-        const int vr = 4 * (lane >> 5) + (i >> 2);
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-            v_off[x] = vr * D * 2 + (((4 * x + 2 * ((lane >> 4) & 1) + ((i & 3) >> 1)) ^ ((vr & 3) << 1)) * 16) + (i & 1) * 8;
+        const int x = lane & 15, r = 4 * (lane >> 5) + (x >> 2);
+        v_at = r * D * 2 + (((2 * ((lane >> 4) & 1) + ((x & 3) >> 1)) ^ swizzle<D, true>(r)) * 16) + (x & 1) * 8;
     }
-    const auto key_frag = [&](const char* kb, int tt, int kk) {
-        return *reinterpret_cast<const bf16x8*>(kb + k_off[kk & 3] + tt * 32 * D * 2 + (kk >> 2) * 128);
+    const auto key_frag = [&](uint32_t kb, int half, int kk) {                 // 32 keys of a half, 16 dimensions
+        return *reinterpret_cast<const bf16x8 __attribute__((address_space(3)))*>((kb ^ (kk * 32)) + half * 32 * D * 2);
     };
-    const auto value_frag = [&](const char* vb, int step, int d) {             // 16 keys from 16 * step, 32 dimensions
-        const char* p = vb + v_off[d & 1] + step * 16 * D * 2 + (d >> 1) * 128;
-        const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p));
-        const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p + 8 * D * 2));
+    const auto value_frag = [&](uint32_t vb, int step, int d) {                // 16 keys from 16 step, 32 dimensions
+        const uint32_t at = (vb ^ (d * 64)) + step * 16 * D * 2;
+        const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(at));
+        const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(at + 8 * D * 2));
         return __builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+    };
+    const auto mma = [](bf16x8 x, bf16x8 y, f32x16 z) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, y, z, 0, 0, 0); };
+    const auto zero = [] {
+        f32x16 z;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) z[r] = 0.f;
+        return z;
+    };
+    const auto top_of = [](const f32x16& s) {
+        float x = s[0];
+#pragma unroll
+        for (int r = 1; r < 16; ++r) x = fmaxf(x, s[r]);
+        return max_halves(x);
+    };
+    const auto mask = [&](f32x16& s, int key0) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[r] = key0 + 8 * (r / 4) + 4 * (lane >> 5) + r % 4 < seen ? s[r] : -INFINITY;
+    };
+    // Weights of the score pair e (0 .. 7) of a half, into its operands.
+    const auto weigh = [&](const f32x16& s, int e, float mc, u32x4 (&p)[2], float& sum) {
+        const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * e], c, -mc));
+        const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * e + 1], c, -mc));
+        sum += p0;
+        sum += p1;
+        uint32_t w = pack_bf16(p0, p1);
+        asm volatile("" : "+v"(w));                     // here, between the products, not where it is used
+        p[e / 4][e % 4] = w;
     };
 
     if (first < tiles) load(first * TK, first & 1);
-    // A row whose scores pass its maximum by too much leaves the inner loop, so
-    // that the loop itself never touches the output sums but to add to them,
-    // and comes back to the same tile with the new maximum.
-    float mx[RT];
+    __builtin_amdgcn_s_waitcnt(0);                      // the queries too: nothing but tiles is waited for below
+    // The inner loop never touches the output sums but to add to them.  A row whose
+    // scores pass its maximum by too much leaves it and comes back to the same
+    // tile with the new maximum; a tile with values that are not finite where some
+    // row does not see them is used outside.
+    float mx = 0.f;
     bool again = false;
-    for (int t = first;; again = true) {
-      bool passed = false;
+    for (int t = first;;) {
+      bool passed = false, odd = false;
       for (; t < tiles; ++t) {
         const int t0 = t * TK;
         if (!again) {
@@ -297,84 +332,46 @@ __global__ __launch_bounds__(kPreThreads, D == 256 ? 1 : 2) void prefill_attenti
             if (t + 1 < tiles) load(t0 + TK, (t + 1) & 1);
         }
         again = false;
-        if (idle || t0 >= wave_end) continue;
-        const char* kb = lds[t & 1][0];
-        const char* vb = lds[t & 1][1];
-        f32x16 s[RT][KT];
+        const uint32_t kb = lds0 + (t & 1) * 2 * S::kBytes + k_at, vb = lds0 + (2 * (t & 1) + 1) * S::kBytes + v_at;
+        if (idle || t0 >= wave_end) continue;           // no row here sees any of it
+        // The second half's scores are formed between the first's weights, the
+        // first's values added between the second's.
+        const bool masked = t0 + TK > wave_full;        // some row sees a part of the tile
+        f32x16 s0 = zero(), s1 = zero();
+        u32x4 p0[2], p1[2];
+        float sum = 0.f;
+        bf16x8 kf[3], vf[2][DT];
+        kf[0] = key_frag(kb, 0, 0);
+        kf[1] = key_frag(kb, 0, 1);
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-            for (int tt = 0; tt < KT; ++tt)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) s[rt][tt][r] = 0.f;
-        {
-            bf16x8 kf[3][KT];                           // operands two steps ahead
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-                for (int tt = 0; tt < KT; ++tt) kf[kk][tt] = key_frag(kb, tt, kk);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                if (kk + 2 < D / 16)
-#pragma unroll
-                    for (int tt = 0; tt < KT; ++tt) kf[(kk + 2) % 3][tt] = key_frag(kb, tt, kk + 2);
-#pragma unroll
-                for (int tt = 0; tt < KT; ++tt)
-#pragma unroll
-                    for (int rt = 0; rt < RT; ++rt)
-                        s[rt][tt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[kk % 3][tt], qf[rt][kk], s[rt][tt], 0, 0, 0);
-                __builtin_amdgcn_sched_barrier(0);
-            }
+        for (int kk = 0; kk < KK; ++kk) {
+            kf[(kk + 2) % 3] = kk + 2 < KK ? key_frag(kb, 0, kk + 2) : key_frag(kb, 1, kk + 2 - KK);
+            s0 = mma(kf[kk % 3], qf[kk], s0);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        const bool masked = t0 + TK > wave_full;
-        if (masked) {
+        if (masked) mask(s0, t0);
+        mx = top_of(s0);
+        top = top == -INFINITY ? mx : top;              // nothing summed yet
+        const float mc0 = top == -INFINITY ? 0.f : top * c;
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
+        for (int kk = 0; kk < KK; ++kk) {
+            if (kk + 2 < KK) kf[(KK + kk + 2) % 3] = key_frag(kb, 1, kk + 2);
+            if (kk >= KK - DT) vf[0][kk - (KK - DT)] = value_frag(vb, 0, kk - (KK - DT));
+            s1 = mma(kf[(KK + kk) % 3], qf[kk], s1);
 #pragma unroll
-                for (int tt = 0; tt < KT; ++tt)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        s[rt][tt][r] = t0 + 32 * tt + 8 * (r / 4) + 4 * (lane >> 5) + r % 4 < seen[rt] ? s[rt][tt][r] : -INFINITY;
+            for (int e = 8 * kk / KK; e < 8 * (kk + 1) / KK; ++e) weigh(s0, e, mc0, p0, sum);
+            __builtin_amdgcn_sched_barrier(0);
         }
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            mx[rt] = s[rt][0][0];
-#pragma unroll
-            for (int tt = 0; tt < KT; ++tt)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) mx[rt] = fmaxf(mx[rt], s[rt][tt][r]);
-            mx[rt] = max_halves(mx[rt]);
-            top[rt] = top[rt] == -INFINITY ? mx[rt] : top[rt];                 // nothing summed yet
-            passed |= (mx[rt] - top[rt]) * c > kSlack;                         // (no if both are infinite: NaN)
-        }
-        passed = __any(passed);
-        if (passed) break;
-        bf16x8 pf[RT][2 * KT];
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            const float mc = top[rt] == -INFINITY ? 0.f : top[rt] * c;
-            float sum = 0.f;
-#pragma unroll
-            for (int tt = 0; tt < KT; ++tt)
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    u32x4 w;
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[rt][tt][8 * u + 2 * x], c, -mc));
-                        const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[rt][tt][8 * u + 2 * x + 1], c, -mc));
-                        sum += p0 + p1;
-                        w[x] = pack_bf16(p0, p1);
-                    }
-                    pf[rt][2 * tt + u] = __builtin_bit_cast(bf16x8, w);
-                }
-            l[rt] += sum;
-        }
-        bool odd = false;                               // a value that is not finite where some row does not see it
-        if (masked) {
+        if (masked) mask(s1, t0 + 32);
+        const float mx1 = top_of(s1);
+        top = top == -INFINITY ? mx1 : top;
+        const float mc1 = top == -INFINITY ? 0.f : top * c;
+        mx = fmaxf(mx, mx1);
+        passed = __any((mx - top) * c > kSlack);        // (no if both are infinite: NaN)
+        if (masked) {                                   // a value that is not finite where some row does not see it
             uint32_t high = 0;
 #pragma unroll
-            for (int st = 0; st < 2 * KT; ++st)
+            for (int st = 0; st < 4; ++st)
 #pragma unroll
                 for (int d = 0; d < DT; ++d) {
                     const u32x4 w = __builtin_bit_cast(u32x4, value_frag(vb, st, d));
@@ -384,114 +381,118 @@ __global__ __launch_bounds__(kPreThreads, D == 256 ? 1 : 2) void prefill_attenti
                 }
             odd = __any(high != 0);
         }
-        if (!odd) {
-            bf16x8 vf[2][DT];                           // operands a step ahead
+        if (passed || odd) break;
 #pragma unroll
-            for (int d = 0; d < DT; ++d) vf[0][d] = value_frag(vb, 0, d);
-#pragma unroll
-            for (int st = 0; st < 2 * KT; ++st) {
-                if (st + 1 < 2 * KT)
-#pragma unroll
-                    for (int d = 0; d < DT; ++d) vf[(st + 1) % 2][d] = value_frag(vb, st + 1, d);
-#pragma unroll
-                for (int d = 0; d < DT; ++d)
-#pragma unroll
-                    for (int rt = 0; rt < RT; ++rt)
-                        o[rt][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[st % 2][d], pf[rt][st], o[rt][d], 0, 0, 0);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-        } else {
-            // The product would carry 0 * Inf into rows that do not see the
-            // value.  The finite values go the same way; what is not finite
-            // is counted, up and down (NaN both ways), over the seen keys.
+        for (int st = 0; st < 2; ++st)
 #pragma unroll
             for (int d = 0; d < DT; ++d) {
-                f32x16 up[RT], down[RT];
+                vf[(st + 1) & 1][d] = value_frag(vb, st + 1, d);
+                o[d] = mma(vf[st & 1][d], __builtin_bit_cast(bf16x8, p0[st]), o[d]);
+                const int x = st * DT + d;
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) up[rt][r] = down[rt][r] = 0.f;
-#pragma unroll
-                for (int st = 0; st < 2 * KT; ++st) {
-                    const u32x4 w = __builtin_bit_cast(u32x4, value_frag(vb, st, d));
-                    u32x4 fin, pos, neg;
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        fin[x] = pos[x] = neg[x] = 0;
-#pragma unroll
-                        for (int y = 0; y < 32; y += 16) {
-                            const uint32_t v = (w[x] >> y) & 0xFFFFu;
-                            const bool bad = (v & 0x7F80u) == 0x7F80u, nan = bad && (v & 0x7Fu) != 0;
-                            fin[x] |= (bad ? 0u : v) << y;
-                            pos[x] |= (bad && (nan || v < 0x8000u) ? 0x3F80u : 0u) << y;
-                            neg[x] |= (bad && (nan || v >= 0x8000u) ? 0x3F80u : 0u) << y;
-                        }
-                    }
-#pragma unroll
-                    for (int rt = 0; rt < RT; ++rt) {
-                        u32x4 one;
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const int key = t0 + 16 * st + 8 * (x / 2) + 4 * (lane >> 5) + 2 * (x % 2);
-                            one[x] = (key < seen[rt] ? 0x3F80u : 0u) | (key + 1 < seen[rt] ? 0x3F800000u : 0u);
-                        }
-                        o[rt][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, fin), pf[rt][st], o[rt][d], 0, 0, 0);
-                        up[rt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, pos), __builtin_bit_cast(bf16x8, one), up[rt], 0, 0, 0);
-                        down[rt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, neg), __builtin_bit_cast(bf16x8, one), down[rt], 0, 0, 0);
-                    }
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        o[rt][d][r] += (up[rt][r] > 0.f ? INFINITY : 0.f) + (down[rt][r] > 0.f ? -INFINITY : 0.f);
+                for (int e = 4 * x / DT; e < 4 * (x + 1) / DT; ++e) weigh(s1, e, mc1, p1, sum);
+                __builtin_amdgcn_sched_barrier(0);
             }
-        }
-      }
-      if (!passed) break;
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-          const float m_new = (mx[rt] - top[rt]) * c > kSlack ? mx[rt] : top[rt];
-          const float keep = m_new == top[rt] ? 1.f : __builtin_amdgcn_exp2f((top[rt] - m_new) * c);
-          top[rt] = m_new;
-          l[rt] *= keep;
+        for (int st = 2; st < 4; ++st)
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                if (st == 2) vf[1][d] = value_frag(vb, 3, d);
+                o[d] = mma(vf[st & 1][d], __builtin_bit_cast(bf16x8, p1[st - 2]), o[d]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        l += sum;
+      }
+      if (!passed && !odd) break;
+      if (passed) {
+          const float m_new = (mx - top) * c > kSlack ? mx : top;
+          const float keep = m_new == top ? 1.f : __builtin_amdgcn_exp2f((top - m_new) * c);
+          top = m_new;
+          l *= keep;
 #pragma unroll
           for (int d = 0; d < DT; ++d)
 #pragma unroll
-              for (int r = 0; r < 16; ++r) o[rt][d][r] *= keep;
+              for (int r = 0; r < 16; ++r) o[d][r] *= keep;
+          again = true;
+      } else {
+          const int t0 = t * TK;
+          const uint32_t kb = lds0 + (t & 1) * 2 * S::kBytes + k_at, vb = lds0 + (2 * (t & 1) + 1) * S::kBytes + v_at;
+          f32x16 s0 = zero(), s1 = zero();
+          u32x4 p0[2], p1[2];
+          float sum = 0.f;
+#pragma unroll
+          for (int kk = 0; kk < KK; ++kk) {
+              s0 = mma(key_frag(kb, 0, kk), qf[kk], s0);
+              s1 = mma(key_frag(kb, 1, kk), qf[kk], s1);
+              __builtin_amdgcn_sched_barrier(0);
+          }
+          mask(s0, t0);
+          mask(s1, t0 + 32);
+          const float mc = top == -INFINITY ? 0.f : top * c;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) weigh(s0, e, mc, p0, sum);
+          // The product would carry 0 * Inf into rows that do not see the
+          // value.  The finite values go the same way; what is not finite is
+          // counted, up and down (NaN both ways), over the seen keys.
+#pragma unroll
+          for (int e = 0; e < 8; ++e) weigh(s1, e, mc, p1, sum);
+          const u32x4 p[4] = {p0[0], p0[1], p1[0], p1[1]};
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+              f32x16 up = zero(), down = zero();
+#pragma unroll
+              for (int st = 0; st < 4; ++st) {
+                  const u32x4 w = __builtin_bit_cast(u32x4, value_frag(vb, st, d));
+                  u32x4 fin, pos, neg, one;
+#pragma unroll
+                  for (int x = 0; x < 4; ++x) {
+                      fin[x] = pos[x] = neg[x] = 0;
+#pragma unroll
+                      for (int y = 0; y < 32; y += 16) {
+                          const uint32_t v = (w[x] >> y) & 0xFFFFu;
+                          const bool bad = (v & 0x7F80u) == 0x7F80u, nan = bad && (v & 0x7Fu) != 0;
+                          fin[x] |= (bad ? 0u : v) << y;
+                          pos[x] |= (bad && (nan || v < 0x8000u) ? 0x3F80u : 0u) << y;
+                          neg[x] |= (bad && (nan || v >= 0x8000u) ? 0x3F80u : 0u) << y;
+                      }
+                      const int key = t0 + 16 * st + 8 * (x / 2) + 4 * (lane >> 5) + 2 * (x % 2);
+                      one[x] = (key < seen ? 0x3F80u : 0u) | (key + 1 < seen ? 0x3F800000u : 0u);
+                  }
+                  o[d] = mma(__builtin_bit_cast(bf16x8, fin), __builtin_bit_cast(bf16x8, p[st]), o[d]);
+                  up = mma(__builtin_bit_cast(bf16x8, pos), __builtin_bit_cast(bf16x8, one), up);
+                  down = mma(__builtin_bit_cast(bf16x8, neg), __builtin_bit_cast(bf16x8, one), down);
+                  __builtin_amdgcn_sched_barrier(0);
+              }
+#pragma unroll
+              for (int r = 0; r < 16; ++r) o[d][r] += (up[r] > 0.f ? INFINITY : 0.f) + (down[r] > 0.f ? -INFINITY : 0.f);
+          }
+          l += sum;
+          ++t;
+          again = false;
       }
     }
 
+    const float sum = sum_halves(l);
     if (parts > 1) {        // sums, maximum and weight for join_kernel
         float* to = static_cast<float*>(a.workspace) + part_at<D>(number, head, part, a.n_kv_heads, most_parts);
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            const int local = local0 + 32 * rt + (lane & 31);
-            const float sum = sum_halves(l[rt]);
-#pragma unroll
-            for (int d = 0; d < DT; ++d)
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    *reinterpret_cast<float4*>(to + local * D + 32 * d + 8 * x + 4 * (lane >> 5)) =
-                        make_float4(o[rt][d][4 * x], o[rt][d][4 * x + 1], o[rt][d][4 * x + 2], o[rt][d][4 * x + 3]);
-            if (lane < 32) *reinterpret_cast<float2*>(to + S::kRows * D + 2 * local) = make_float2(top[rt], sum);
-        }
-        return;
-    }
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        const float sum = sum_halves(l[rt]);
-        if (out_row[rt] < 0) continue;
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-                store_four(a, out_row[rt] * D + 32 * d + 8 * x + 4 * (lane >> 5), o[rt][d][4 * x] * inv,
-                           o[rt][d][4 * x + 1] * inv, o[rt][d][4 * x + 2] * inv, o[rt][d][4 * x + 3] * inv);
-        if (a.lse != nullptr && lane < 32) a.lse[out_row[rt]] = lse_of(top[rt], sum, c);
+                *reinterpret_cast<float4*>(to + local * D + 32 * d + 8 * x + 4 * (lane >> 5)) =
+                    make_float4(o[d][4 * x], o[d][4 * x + 1], o[d][4 * x + 2], o[d][4 * x + 3]);
+        if (lane < 32) *reinterpret_cast<float2*>(to + S::kRows * D + 2 * local) = make_float2(top, sum);
+        return;
     }
+    if (out_row < 0) return;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            store_four(a, out_row * D + 32 * d + 8 * x + 4 * (lane >> 5), o[d][4 * x] * inv, o[d][4 * x + 1] * inv,
+                       o[d][4 * x + 2] * inv, o[d][4 * x + 3] * inv);
+    if (a.lse != nullptr && lane < 32) a.lse[out_row] = lse_of(top, sum, c);
 }
 
 // Joins the parts of every tile that has several.  A workgroup takes
