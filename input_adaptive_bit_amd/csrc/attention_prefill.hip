@@ -548,20 +548,22 @@ PrePlan plan_prefill(const Args& a) {
     const int64_t group = a.n_q_heads / a.n_kv_heads;
     p.tiles = a.total_q * group / PreShape<D>::kRows + a.batch;                // at most, whatever the lengths
     // Parts where they make the call shorter, by what was measured: a tile of keys
-    // takes a workgroup alone on its CU t us, two on one CU 1.6 times that (at
-    // head_dim 256 there is room for one), and the parts cost a second launch and
-    // their way through memory.  Two prompts of 257 and 512 queries after 6000
-    // keys, 28 heads of 64, in 1 to 5 parts: 113, 85, 97, 79, 80 us; 512 after 7680,
-    // 32 heads of 128, in 1, 3, 4, 5: 189, 108, 96, 117; 1024 queries of a prompt: 35
-    // whole, 43 in two.
+    // takes a workgroup alone on its CU t us, two on one CU 1.35 and three 1.8
+    // times that (where there is room for them), and the parts cost a second
+    // launch and their way through memory.  512 queries after 7680 keys, 32 heads
+    // of 128, in 1, 2, 4, 5, 8 parts: 158, 101, 92, 106, 107 us; 128 queries: 150, 87,
+    // 58, 53, 49; 1024 queries of a prompt: 31 whole, 38 in two; two prompts of 257
+    // and 512 after 6000 keys, 28 heads of 64, in 1, 2, 4, 5: 97, 81, 66, 72.
+    constexpr int kFit = D == 64 ? 3 : D == 128 ? 2 : 1;
+    constexpr double kTime = D == 64 ? 0.95 : D == 128 ? 1.2 : 2.1, kRate = D == 256 ? 1.7e6 : 2.5e6;   // us, bytes per us
+    constexpr double kTogether[4] = {0.0, 1.0, 1.35, 1.8};
     const int64_t rows = PreShape<D>::kRows, groups = (a.total_q * group + rows - 1) / rows * a.n_kv_heads;
     const double keys = (a.total_k - (a.causal ? 0.5 * a.total_q : 0.0)) / std::max(1, a.batch);
-    const double t = (D == 64 ? 1.1 : D == 128 ? 1.5 : 1.9) * keys / PreShape<D>::kTK;
     const auto cost = [&](int64_t parts) {
         const int64_t deep = (groups * parts + kCus - 1) / kCus;               // workgroups on the fullest CU
-        const double rounds = D == 256 ? deep : deep / 2 * 1.6 + deep % 2;
+        const double rounds = deep / kFit * kTogether[kFit] + kTogether[deep % kFit];
         const double bytes = 2.0 * groups * parts * rows * (D + 2) * sizeof(float);
-        return t * rounds / parts + (parts > 1 ? 5.0 + bytes / 5e6 : 0.0);
+        return kTime * keys / PreShape<D>::kTK * rounds / parts + (parts > 1 ? 5.0 + bytes / kRate : 0.0);
     };
     p.parts = 1;
     if (groups < 3 * kCus)
