@@ -378,8 +378,15 @@ __device__ __forceinline__ void agent_store(float* p, float2 v) {
                        __HIP_MEMORY_SCOPE_AGENT);
 }
 
+// Waves of a workgroup that has a CU to itself, as many as its registers allow.
+__host__ __device__ constexpr int big_waves(int D) { return D == 256 ? 8 : 12; }
+
+__host__ __device__ constexpr int waves_per_simd(int D, int qp, int waves) {
+    return waves > 4 ? waves / 4 : D == 256 || qp == 2 ? 2 : 3;
+}
+
 template <int D, int BITS, int QP, int W>
-__global__ __launch_bounds__(W * kWave, W == 8 || D == 256 || QP == 2 ? 2 : 3) void decode_kernel(DecodeArgs a) {
+__global__ __launch_bounds__(W * kWave, waves_per_simd(D, QP, W)) void decode_kernel(DecodeArgs a) {
     using S = Shape<D, BITS>;
     constexpr int kDecWaves = W, kDecThreads = W * kWave, kUnit = W * kTileTokens;   // tokens of one round
     constexpr int kStride = D + 4;                       // floats of a head's row in LDS
@@ -420,20 +427,19 @@ __global__ __launch_bounds__(W * kWave, W == 8 || D == 256 || QP == 2 ? 2 : 3) v
                                       : *reinterpret_cast<const u32x4*>(static_cast<const float*>(a.q) + at + 4 * x);
         }
     }
-    const int len = min(max(a.seq_lens[b], 0), a.longest);
-    const int parts = max(1, (len + a.chunk - 1) / a.chunk);
-    if (split >= parts) return;
-    const int end = min(len, begin + a.chunk);
-
     // Pages of the two halves of the tile at t0; -1 past the end or absent.
-    const auto check_pages = [&](int t0, int (&page)[2]) {
+    const auto check_pages = [&](int t0, int end, int (&page)[2]) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
             if (t0 + 16 * h >= end || static_cast<unsigned>(page[h]) >= static_cast<unsigned>(a.d.n_pages)) page[h] = -1;
     };
     Tile<D, BITS> T;
     int64_t row[2];
-    check_pages(t, page);
+    const int len = min(max(a.seq_lens[b], 0), a.longest);
+    const int parts = max(1, (len + a.chunk - 1) / a.chunk);
+    if (split >= parts) return;
+    const int end = min(len, begin + a.chunk);
+    check_pages(t, end, page);
     if (t < end) {
         tile_rows(row, a, t, page, head);
         load_keys(T, a, row, lane);
@@ -477,7 +483,7 @@ __global__ __launch_bounds__(W * kWave, W == 8 || D == 256 || QP == 2 ? 2 : 3) v
             float sc[8];
             tile_scores<D, BITS, QP>(sc, T, qf, q_sum, a.scale_log2);
             __builtin_amdgcn_sched_barrier(0);
-            check_pages(t + kUnit, next);
+            check_pages(t + kUnit, end, next);
             if (more) {
                 tile_rows(row, a, t + kUnit, next, head);
                 load_keys(T, a, row, lane);
@@ -620,10 +626,12 @@ __global__ __launch_bounds__(W * kWave, W == 8 || D == 256 || QP == 2 ? 2 : 3) v
 }
 
 // How a call is cut up (host arithmetic on its sizes alone).  Measured in us a
-// call, four and eight waves, 8 bits, 8 heads of 128, groups of 4, one sequence:
-//   500 tokens 8.3 and 10.2; 2000 10.0 and 10.6; 4000 12.8 and 11.8; 32768 24 and 22;
-// 32 sequences of 17 .. 8192 tokens, four waves: one workgroup to a CU 79, twelve
-// 66 (eight waves, one to a CU: 73); 32 of 2048 each: 34 and 37.
+// call, 8 bits, 8 key-value heads of 128, groups of 4:
+//   one sequence, four waves and eight: 500 tokens 8.3, 10.2; 2000 10.0, 10.6; 4000
+//   12.8, 11.8; 32768 24, 22; eight waves and twelve: 8192 15.2, 14.3; 131071 at 4
+//   bits, groups of 8, 46.6, 43.5;
+//   32 sequences of 17 .. 8192 tokens, four waves: one workgroup to a CU 79, twelve
+//   66 (eight waves, one to a CU 73); 32 of 2048 each: 34, 37.
 constexpr int kCus = 256, kFewItems = 48, kOneRound = 128;
 
 struct DecodePlan {
@@ -638,12 +646,12 @@ DecodePlan plan_decode(const grinqh_kv_layout& L, int n_q_heads, int batch, int 
     p.head_tiles = (group + kHeadTile - 1) / kHeadTile;
     p.items = static_cast<int64_t>(batch) * L.n_kv_heads * p.head_tiles;
     // Few sequences and heads: parts for one round of a short cache (four waves,
-    // 128 tokens), else one workgroup of eight waves to a CU.  Many: workgroups
+    // 128 tokens), else one workgroup to a CU.  Many: workgroups
     // of four waves, three to a CU, of 512 tokens and more, enough of them that
     // sequences of different lengths fill the card evenly.
     const bool few = p.items <= kFewItems;
     const auto units_of = [&](int waves) { return (static_cast<int64_t>(max_len) + waves * kTileTokens - 1) / (waves * kTileTokens); };
-    p.waves = few && p.items * units_of(4) > kOneRound ? 8 : 4;
+    p.waves = few && p.items * units_of(4) > kOneRound ? big_waves(L.head_dim) : 4;
     const int64_t units = units_of(p.waves);
     const auto at_most = [&](int64_t groups) {          // units of a part, for that many workgroups in all
         const int64_t parts = std::max<int64_t>(1, groups / std::max<int64_t>(p.items, 1));
@@ -651,6 +659,8 @@ DecodePlan plan_decode(const grinqh_kv_layout& L, int n_q_heads, int batch, int 
     };
     int64_t per = few ? at_most(kCus) : std::max<int64_t>(at_most(12 * kCus), 4);
     if (!few && p.items * ((units + per - 1) / per) < 3 * kCus) per = std::min(per, at_most(3 * kCus));
+    // Joining is one workgroup's work: more than 32 parts only of four rounds each.
+    per = std::max(per, std::min<int64_t>((units + 31) / 32, 4));
     if (p.items > kCounters) per = units;
     p.chunk = static_cast<int>(per * p.waves * kTileTokens);
     p.splits = static_cast<int>((units + per - 1) / per);
@@ -664,9 +674,10 @@ template <int D, int BITS>
 void launch_queries(const DecodeArgs& a, int waves, unsigned n, hipStream_t stream) {
     const int here = a.group < kHeadTile ? a.group : kHeadTile;
     const size_t lds = static_cast<size_t>(waves) * std::max<size_t>(here * (D + 4 + 2) * sizeof(float), kWave * sizeof(f32x4));
-    if (waves == 8) {
-        if (a.q_dtype == GRINQH_BF16) decode_kernel<D, BITS, 1, 8><<<dim3(n), dim3(512), lds, stream>>>(a);
-        else decode_kernel<D, BITS, 2, 8><<<dim3(n), dim3(512), lds, stream>>>(a);
+    if (waves > 4) {
+        constexpr int W = big_waves(D);
+        if (a.q_dtype == GRINQH_BF16) decode_kernel<D, BITS, 1, W><<<dim3(n), dim3(W * kWave), lds, stream>>>(a);
+        else decode_kernel<D, BITS, 2, W><<<dim3(n), dim3(W * kWave), lds, stream>>>(a);
         return;
     }
     if (a.q_dtype == GRINQH_BF16) decode_kernel<D, BITS, 1, 4><<<dim3(n), dim3(256), lds, stream>>>(a);
@@ -725,9 +736,6 @@ grinqh_status grinqh_decode_attention(const grinqh_kv_layout* L, const grinqh_kv
     if (overlaps(q, static_cast<size_t>(((batch - 1) * q_stride + width) * qb), out,
                  static_cast<size_t>(batch * width * ob)))
         return GRINQH_EINVAL;
-    DeviceInfo dev;
-    hipError_t e;
-    if (!current_device_info(&dev, &e)) return map_hip_error(e);
     const int64_t reach = static_cast<int64_t>(max_pages) * L->page_size;
     DecodeArgs a;
     a.d = kv_dims(*L);

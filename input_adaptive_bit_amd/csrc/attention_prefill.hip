@@ -643,9 +643,6 @@ extern "C" grinqh_status grinqh_prefill_attention(const grinqh_prefill_attention
         (overlaps(a.k, static_cast<size_t>((a.total_k - 1) * a.k_stride + kw) * 2, a.out, out_bytes) ||
          overlaps(a.v, static_cast<size_t>((a.total_k - 1) * a.v_stride + kw) * 2, a.out, out_bytes)))
         return GRINQH_EINVAL;
-    DeviceInfo dev;
-    hipError_t e;
-    if (!current_device_info(&dev, &e)) return map_hip_error(e);
     const hipStream_t s = static_cast<hipStream_t>(stream);
     if (a.head_dim == 64) return launch_prefill_attention<64>(a, s);
     if (a.head_dim == 128) return launch_prefill_attention<128>(a, s);

@@ -296,9 +296,6 @@ grinqh_status grinqh_kv_write(const grinqh_kv_layout* L, const grinqh_kv_pools* 
             overlaps(src[i], n, pools->k_grid, grid_bytes) || overlaps(src[i], n, pools->v_grid, grid_bytes))
             return GRINQH_EINVAL;
     }
-    DeviceInfo dev;
-    hipError_t e;
-    if (!current_device_info(&dev, &e)) return map_hip_error(e);
     const KvWriteArgs a{kv_dims(*L), {k, v}, {pools->k_codes, pools->v_codes}, {pools->k_grid, pools->v_grid},
                         slots, {k_stride, v_stride}, n_tokens};
     dispatch<WriteLaunch>(*L, dtype, row_grid(*L, n_tokens), static_cast<hipStream_t>(stream), a);
@@ -320,9 +317,6 @@ grinqh_status grinqh_kv_read(const grinqh_kv_layout* L, const grinqh_kv_pools* p
         if (overlaps(dst, n, pools->k_codes, code_bytes) || overlaps(dst, n, pools->v_codes, code_bytes) ||
             overlaps(dst, n, pools->k_grid, grid_bytes) || overlaps(dst, n, pools->v_grid, grid_bytes))
             return GRINQH_EINVAL;
-    DeviceInfo dev;
-    hipError_t e;
-    if (!current_device_info(&dev, &e)) return map_hip_error(e);
     const KvReadArgs a{kv_dims(*L), {pools->k_codes, pools->v_codes}, {pools->k_grid, pools->v_grid}, {k, v},
                        slots, n_tokens};
     dispatch<ReadLaunch>(*L, dtype, row_grid(*L, n_tokens), static_cast<hipStream_t>(stream), a);
