@@ -326,7 +326,7 @@ size_t grinqh_kv_grid_bytes(const grinqh_kv_layout* L);
 /* Write the keys and values of n_tokens tokens into their slots.
  *   k, v       [n_tokens][n_kv_heads][head_dim] of dtype, 16-byte aligned; the
  *              tokens lie k_stride and v_stride elements apart (multiples of
- *              16 bytes, at least n_kv_heads * head_dim), so both can be
+ *              16 bytes, from n_kv_heads * head_dim to 2^24 elements), so both can be
  *              slices of a fused projection's output.
  *   n_tokens   0 .. 2^24 (0: nothing is launched).
  *   slots      int64 [n_tokens]; a token whose slot is negative or not below
@@ -366,7 +366,7 @@ int64_t grinqh_debug_kv_row(const grinqh_kv_layout* L, int64_t slot, int32_t hea
  * tokens (the new one among them, if it was written first).
  *   q           [batch][n_q_heads][head_dim] of q_dtype, 16-byte aligned; the
  *               sequences' tokens lie q_stride elements apart (a multiple of
- *               16 bytes, at least n_q_heads * head_dim).
+ *               16 bytes, from n_q_heads * head_dim to 2^24 elements).
  *   n_q_heads   a multiple of L->n_kv_heads, up to 1024.
  *   page_table  int32 [batch][max_pages], rows table_stride entries apart: the
  *               pages of a sequence in order.  A page outside 0 .. n_pages - 1
@@ -375,7 +375,7 @@ int64_t grinqh_debug_kv_row(const grinqh_kv_layout* L, int64_t slot, int32_t hea
  *               negative and as min(max_len, max_pages * page_size) if above.
  *   batch       0 .. 2^20 (0: nothing is launched); max_len 1 .. 2^28, the
  *               host's bound on the lengths.
- *   scale       finite.
+ *   scale       -1e30 .. 1e30.
  *   out         [batch][n_q_heads][head_dim] of out_dtype, contiguous, 16-byte
  *               aligned.
  *   lse         fp32 [batch][n_q_heads] or NULL.
@@ -403,13 +403,13 @@ grinqh_status grinqh_decode_attention(const grinqh_kv_layout* L, const grinqh_kv
  * beginning, and with fewer the first queries see nothing).
  *   q          bf16 [total_q][n_q_heads][head_dim], token rows q_stride elements
  *              apart; k, v bf16 [total_k][n_kv_heads][head_dim], k_stride and
- *              v_stride apart (multiples of 8; rows may be slices of a fused
- *              projection's output); all 16-byte aligned.
+ *              v_stride apart (multiples of 8, up to 2^24; rows may be slices of
+ *              a fused projection's output); all 16-byte aligned.
  *   cu_q, cu_k int32 [batch + 1], ascending from 0; entries are clamped to
  *              0 .. total_q (total_k).
  *   total_q, total_k  0 .. 2^24 rows (total_q 0: nothing is launched).
  *   n_q_heads  a multiple of n_kv_heads, up to 1024; head_dim 64, 128 or 256.
- *   scale      finite.
+ *   scale      -1e30 .. 1e30.
  *   out        [total_q][n_q_heads][head_dim] of out_dtype, contiguous, 16-byte
  *              aligned; rows behind the last sequence are left as they are.
  *   lse        fp32 [total_q][n_q_heads] or NULL.

@@ -61,8 +61,8 @@ def _tensor(t, name, device=None):
 
 def _plain(t, name, dtype, device, numel):
     """The address of a contiguous tensor of one type with at least numel elements."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device and t.is_contiguous()
-            and t.numel() >= numel and t.is_cuda):
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.get_device() == device.index
+            and t.is_contiguous() and t.numel() >= numel):
         return t.data_ptr()
     _tensor(t, name, device)                     # the reason why not
     if t.dtype != dtype:
@@ -72,6 +72,12 @@ def _plain(t, name, dtype, device, numel):
     if t.numel() < numel:
         raise ValueError(f"{name} is too small ({t.numel()} < {numel} elements)")
     return t.data_ptr()
+
+
+def _floats(t, name, device, numel):
+    """The same for a tensor of a type that _float_code takes."""
+    _float_code(t.dtype if isinstance(t, torch.Tensor) else None, name)
+    return _plain(t, name, t.dtype, device, numel)
 
 
 def _float_code(dtype, name) -> int:
@@ -85,7 +91,7 @@ def _float_code(dtype, name) -> int:
 def _rows(t, name, heads, dim, device):
     """Token stride in elements of [tokens][heads][dim] whose token rows are
     each contiguous (the tokens may lie further apart)."""
-    if not isinstance(t, torch.Tensor) or t.device != device or not t.is_cuda:
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() == device.index):
         _tensor(t, name, device)                 # the reason why not
     shape, stride = t.shape, t.stride()
     if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
@@ -206,10 +212,9 @@ def grinqh_kv_read(cache: KVCache, slots, k, v, stream=None) -> None:
     """k, v: bf16 or fp32 [tokens][n_kv_heads][head_dim], contiguous, overwritten."""
     device = cache.device
     n = slots.numel()
-    _tensor(k, "k", device)
     width = n * cache.n_kv_heads * cache.head_dim
     _run("grinqh_kv_read", device, stream, *cache._refs, _plain(slots, "slots", torch.int64, device, n), n,
-         _plain(k, "k", k.dtype, device, width), _plain(v, "v", k.dtype, device, width), _float_code(k.dtype, "k"))
+         _floats(k, "k", device, width), _plain(v, "v", k.dtype, device, width), _float_code(k.dtype, "k"))
 
 
 def kv_write(cache: KVCache, k, v, slots, stream=None) -> None:
@@ -238,26 +243,25 @@ def grinqh_decode_attention(cache: KVCache, q, page_table, seq_lens, max_len: in
     fp32, contiguous; lse: fp32 [batch][n_q_heads] or None; scale: default
     head_dim ** -0.5."""
     device, dim = cache.device, cache.head_dim
-    _tensor(page_table, "page_table", device)
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a [batch][n_q_heads][head_dim] tensor")
     batch, heads, _ = q.shape
     q_stride = _rows(q, "q", heads, dim, device)
-    shape, stride = page_table.shape, page_table.stride()
-    if page_table.dtype != torch.int32 or len(shape) != 2 or shape[0] != batch:
+    _tensor(page_table, "page_table", device)
+    rows, max_pages = page_table.shape if page_table.dim() == 2 else (-1, -1)
+    if page_table.dtype is not torch.int32 or rows != batch:
         raise ValueError("page_table must be int32 [batch][max_pages]")
-    if shape[1] > 1 and stride[1] != 1:
+    if max_pages > 1 and page_table.stride(1) != 1:
         raise ValueError("the rows of page_table must be contiguous")
-    _tensor(out, "out", device)
     _tensor(workspace, "workspace", device)
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    width = batch * heads
     _run("grinqh_decode_attention", device, stream, *cache._refs, q.data_ptr(), _float_code(q.dtype, "q"), q_stride,
-         heads, page_table.data_ptr(), stride[0] if batch > 1 else shape[1], shape[1],
+         heads, page_table.data_ptr(), page_table.stride(0) if batch > 1 else max_pages, max_pages,
          _plain(seq_lens, "seq_lens", torch.int32, device, batch), batch, max_len,
-         dim ** -0.5 if scale is None else scale, _plain(out, "out", out.dtype, device, width * dim),
-         _float_code(out.dtype, "out"), None if lse is None else _plain(lse, "lse", torch.float32, device, width),
+         dim ** -0.5 if scale is None else scale, _floats(out, "out", device, batch * heads * dim),
+         _float_code(out.dtype, "out"),
+         None if lse is None else _plain(lse, "lse", torch.float32, device, batch * heads),
          workspace.data_ptr(), workspace.nbytes)
 
 
@@ -272,7 +276,7 @@ def decode_attention(cache: KVCache, q, page_table, seq_lens, max_len=None, scal
         raise ValueError("q must be a [batch][n_q_heads][head_dim] tensor")
     batch, heads, _ = q.shape
     if max_len is None:
-        max_len = max(1, page_table.shape[1] * cache.layout.page_size)
+        max_len = min(max(1, page_table.shape[1] * cache.layout.page_size), 1 << 28)
     out = _empty((batch, heads, cache.head_dim), out_dtype or torch.bfloat16, device, stream)
     lse = _empty((batch, heads), torch.float32, device, stream) if return_lse else None
     if workspace is None:
@@ -284,8 +288,7 @@ def decode_attention(cache: KVCache, q, page_table, seq_lens, max_len=None, scal
 def _prefill_args(q, k, v, cu_q, cu_k, out, causal, scale, lse):
     """The checked arguments of a prefill attention, without a workspace."""
     device = _tensor(q, "q")
-    _tensor(k, "k", device)
-    if q.dim() != 3 or k.dim() != 3:
+    if q.dim() != 3 or not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("q and k must be [tokens][heads][head_dim]")
     total_q, heads, dim = q.shape
     total_k, kv_heads, _ = k.shape
@@ -297,7 +300,6 @@ def _prefill_args(q, k, v, cu_q, cu_k, out, causal, scale, lse):
     bf16 = torch.bfloat16
     if q.dtype != bf16 or k.dtype != bf16 or v.dtype != bf16:
         raise TypeError(f"q, k and v must be bfloat16, not {q.dtype}, {k.dtype}, {v.dtype}")
-    _tensor(out, "out", device)
     batch = cu_q.numel() - 1
     if batch < 0 or cu_k.numel() != batch + 1:
         raise ValueError("cu_q and cu_k must both be [batch + 1]")
@@ -305,7 +307,7 @@ def _prefill_args(q, k, v, cu_q, cu_k, out, causal, scale, lse):
         q.data_ptr(), k.data_ptr(), v.data_ptr(), q_stride, k_stride, v_stride,
         _plain(cu_q, "cu_q", torch.int32, device, 1), _plain(cu_k, "cu_k", torch.int32, device, 1), batch, total_q,
         total_k, heads, kv_heads, dim, bool(causal), dim ** -0.5 if scale is None else scale,
-        _plain(out, "out", out.dtype, device, total_q * heads * dim), _float_code(out.dtype, "out"),
+        _floats(out, "out", device, total_q * heads * dim), _float_code(out.dtype, "out"),
         None if lse is None else _plain(lse, "lse", torch.float32, device, total_q * heads))
 
 

@@ -390,7 +390,7 @@ __global__ __launch_bounds__(W * kWave, waves_per_simd(D, QP, W)) void decode_ke
     using S = Shape<D, BITS>;
     constexpr int kDecWaves = W, kDecThreads = W * kWave, kUnit = W * kTileTokens;   // tokens of one round
     constexpr int kStride = D + 4;                       // floats of a head's row in LDS
-    extern __shared__ float lds[];                       // [wave][head][kStride], then m and l [wave][head]
+    extern __shared__ __attribute__((aligned(16))) float lds[];                       // [wave][head][kStride], then m and l [wave][head]
     __shared__ int is_last;
     // Parts are the slow index: workgroups go to the 8 XCDs in turn, and with
     // the items as the fast one every XCD gets early and late parts alike (late
@@ -716,7 +716,7 @@ grinqh_status grinqh_decode_attention(const grinqh_kv_layout* L, const grinqh_kv
                                       size_t workspace_bytes, void* stream) {
     const grinqh_status st = check_kv_pools(L, pools);
     if (st != GRINQH_OK) return st;
-    if (!valid_heads(L, n_q_heads, batch, max_len) || !isfinite(scale)) return GRINQH_EINVAL;
+    if (!valid_heads(L, n_q_heads, batch, max_len) || !(fabsf(scale) <= kMaxScale)) return GRINQH_EINVAL;
     if ((q_dtype != GRINQH_BF16 && q_dtype != GRINQH_F32) || (out_dtype != GRINQH_BF16 && out_dtype != GRINQH_F32))
         return GRINQH_EINVAL;
     if (batch == 0) return GRINQH_OK;

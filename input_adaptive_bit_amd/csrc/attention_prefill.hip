@@ -148,44 +148,56 @@ __device__ __forceinline__ float sum_halves(float x) {
 
 // Where a flat tile number lies: its sequence, the tile in it, and how many
 // tiles the sequence has; seq -1 past the last.  Up to 64 sequences are taken
-// from the longest to the shortest, so that the launch ends on short ones.
+// from the longest to the shortest, so that the launch ends on short ones; more
+// are narrowed down by 64 runs of sequences at a time.
 struct Place {
     int seq, tile, tiles;
 };
-__device__ __forceinline__ Place find_tile(const Args& a, int group, int rows, int number, int lane) {
-    int before = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += kWave) {
-        int tiles = 0, seq = b0 + lane;
-        if (seq < a.batch) {
-            const int q0 = min(max(a.cu_q[seq], 0), a.total_q), q1 = min(max(a.cu_q[seq + 1], 0), a.total_q);
-            tiles = static_cast<int>((static_cast<int64_t>(max(q1 - q0, 0)) * group + rows - 1) / rows);
-        }
-        if (a.batch > 1 && a.batch <= kWave) {
-            int rank = 0;
-            for (int b = 0; b < a.batch; ++b) {
-                const int other = __builtin_amdgcn_readlane(tiles, b);
-                rank += other > tiles || (other == tiles && b < lane);
-            }
-            // lane -> lane of its rank (lanes past the last sequence keep their place)
-            const int to = 4 * (lane < a.batch ? rank : lane);
-            tiles = __builtin_amdgcn_ds_permute(to, tiles);
-            seq = __builtin_amdgcn_ds_permute(to, seq);
-        }
-        int sum = tiles;
+__device__ __forceinline__ int tiles_of(const Args& a, int group, int rows, int seq) {
+    const int q0 = min(max(a.cu_q[seq], 0), a.total_q), q1 = min(max(a.cu_q[seq + 1], 0), a.total_q);
+    return static_cast<int>((static_cast<int64_t>(max(q1 - q0, 0)) * group + rows - 1) / rows);
+}
+__device__ __forceinline__ int sum_up_to(int x, int lane) {                    // over lanes 0 .. lane
 #pragma unroll
-        for (int k = 1; k < kWave; k <<= 1) {
-            const int x = __shfl_up(sum, k);
-            if (lane >= k) sum += x;
-        }
-        const uint64_t over = __ballot(before + sum > number);
-        if (over != 0) {
-            const int at = __builtin_ctzll(over);
-            const int upto = __shfl(sum, at), mine = __shfl(tiles, at);
-            return Place{__shfl(seq, at), number - (before + upto - mine), mine};
-        }
-        before += __shfl(sum, kWave - 1);
+    for (int k = 1; k < kWave; k <<= 1) {
+        const int y = __shfl_up(x, k);
+        if (lane >= k) x += y;
     }
-    return Place{-1, -1, 0};
+    return x;
+}
+__device__ __forceinline__ Place find_tile(const Args& a, int group, int rows, int number, int lane) {
+    int first = 0, count = a.batch, before = 0;
+    while (count > kWave) {
+        const int run = (count + kWave - 1) / kWave;
+        const int r0 = min(first + lane * run, first + count), r1 = min(r0 + run, first + count);
+        int tiles = 0;
+        for (int seq = r0; seq < r1; ++seq) tiles += tiles_of(a, group, rows, seq);
+        const int sum = sum_up_to(tiles, lane);
+        const uint64_t over = __ballot(before + sum > number);
+        if (over == 0) return Place{-1, -1, 0};
+        const int at = __builtin_ctzll(over);
+        before += __shfl(sum, at) - __shfl(tiles, at);
+        count = __shfl(r1 - r0, at);
+        first = __shfl(r0, at);
+    }
+    int seq = first + lane, tiles = lane < count ? tiles_of(a, group, rows, seq) : 0;
+    if (a.batch > 1 && a.batch <= kWave) {
+        int rank = 0;
+        for (int b = 0; b < a.batch; ++b) {
+            const int other = __builtin_amdgcn_readlane(tiles, b);
+            rank += other > tiles || (other == tiles && b < lane);
+        }
+        // lane -> lane of its rank (lanes past the last sequence keep their place)
+        const int to = 4 * (lane < a.batch ? rank : lane);
+        tiles = __builtin_amdgcn_ds_permute(to, tiles);
+        seq = __builtin_amdgcn_ds_permute(to, seq);
+    }
+    const int sum = sum_up_to(tiles, lane);
+    const uint64_t over = __ballot(before + sum > number);
+    if (over == 0) return Place{-1, -1, 0};
+    const int at = __builtin_ctzll(over);
+    const int upto = __shfl(sum, at), mine = __shfl(tiles, at);
+    return Place{__shfl(seq, at), number - (before + upto - mine), mine};
 }
 
 // How a call is cut up (host arithmetic on its sizes alone).
@@ -606,7 +618,7 @@ grinqh_status check_sizes(const Args& a) {
         return GRINQH_EINVAL;
     if (a.head_dim != 64 && a.head_dim != 128 && a.head_dim != 256) return GRINQH_EINVAL;
     if (a.n_kv_heads < 1 || a.n_kv_heads > kMaxKvHeads || a.n_q_heads < 1 || a.n_q_heads > kMaxQHeads ||
-        a.n_q_heads % a.n_kv_heads != 0 || !isfinite(a.scale))
+        a.n_q_heads % a.n_kv_heads != 0 || !(fabsf(a.scale) <= kMaxScale))
         return GRINQH_EINVAL;
     if (a.out_dtype != GRINQH_BF16 && a.out_dtype != GRINQH_F32) return GRINQH_EINVAL;
     return GRINQH_OK;

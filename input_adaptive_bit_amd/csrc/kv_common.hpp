@@ -37,6 +37,8 @@ constexpr int kMaxKvHeads = 1024, kMaxQHeads = 1024;
 constexpr int64_t kMaxStride = int64_t{1} << 24;   // elements between tokens
 constexpr int kMaxBatch = 1 << 20, kMaxCacheLen = 1 << 28, kMaxPacked = 1 << 24;
 
+constexpr float kMaxScale = 1e30f;                 // times log2(e) it stays finite
+
 inline bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 inline bool overlaps(const void* a, size_t na, const void* b, size_t nb) {

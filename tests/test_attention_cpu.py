@@ -152,7 +152,7 @@ def test_cache_calls_check_their_arguments_before_any_device_call():
     for key in ("ks", "vs"):
         assert write(**{key: 127}) == B.GRINQH_EINVAL                             # tokens would overlap
         assert write(**{key: 132}) == B.GRINQH_EALIGN
-        assert write(**{key: (1 << 32) + 8}) == B.GRINQH_EINVAL
+        assert write(**{key: (1 << 24) + 8}) == B.GRINQH_EINVAL
         assert write(dt=1, **{key: 130}) == B.GRINQH_EALIGN
     assert read(v=K + 512) == B.GRINQH_EINVAL                                     # outputs overlap
 
@@ -172,7 +172,7 @@ def test_decode_attention_checks_its_arguments_before_any_device_call():
         assert call(**{key: None}) == B.GRINQH_EINVAL, key
     for key, value in (("qd", 3), ("od", -1), ("nq", 7), ("nq", 0), ("nq", 1026), ("mp", 0), ("ts", 3), ("b", -1),
                        ("b", (1 << 20) + 1), ("ml", 0), ("ml", (1 << 28) + 1), ("sc", float("nan")),
-                       ("sc", float("inf")), ("qs", 8 * 64 - 8), ("qs", (1 << 32) + 8), ("o", Q + 64)):
+                       ("sc", float("inf")), ("sc", -2e30), ("qs", 8 * 64 - 8), ("qs", (1 << 24) + 8), ("o", Q + 64)):
         assert call(**{key: value}) == B.GRINQH_EINVAL, (key, value)
     for key, value in (("q", Q + 8), ("qs", 8 * 64 + 4), ("t", T + 2), ("n", N + 1), ("o", OUT + 8), ("lse", LSE + 2),
                        ("ws", WS + 64)):
@@ -199,10 +199,19 @@ def test_prefill_attention_checks_its_arguments_before_any_device_call():
         assert call(**{key: None}) == B.GRINQH_EINVAL, key
     for key, value in (("batch", -1), ("batch", (1 << 20) + 1), ("total_q", -1), ("total_q", (1 << 24) + 1),
                        ("total_k", -1), ("total_k", (1 << 24) + 1), ("n_q_heads", 7), ("n_q_heads", 1026),
-                       ("n_kv_heads", 0), ("head_dim", 96), ("scale", float("nan")), ("out_dtype", 2),
-                       ("q_stride", 504), ("k_stride", 120), ("v_stride", 64), ("q_stride", (1 << 32) + 8),
+                       ("n_kv_heads", 0), ("head_dim", 96), ("scale", float("nan")), ("scale", 2e30), ("out_dtype", 2),
+                       ("q_stride", 504), ("k_stride", 120), ("v_stride", 64), ("q_stride", (1 << 24) + 8),
                        ("out", Q + 64), ("out", K + 64), ("out", V + 64)):
         assert call(**{key: value}) == B.GRINQH_EINVAL, (key, value)
+    assert call(workspace=64) == B.GRINQH_EALIGN
+    few = dict(q_stride=512, total_q=20, total_k=9000, batch=1)
+    need = lib.grinqh_prefill_attention_workspace_bytes(ctypes.byref(B.PrefillAttentionArgs(**dict(good, **few))))
+    assert need > 0 and need % 4 == 0
+    assert call(**few, workspace=K64 * 16 * 9, workspace_bytes=need - 1) == B.GRINQH_ENOSPACE
+    assert lib.grinqh_prefill_attention_workspace_bytes(None) == 0
+    for key, value in (("head_dim", 96), ("batch", -1), ("n_q_heads", 7), ("total_q", 5000)):     # the last: filled already
+        a = B.PrefillAttentionArgs(**dict(good, **dict(few, **{key: value})))
+        assert (lib.grinqh_prefill_attention_workspace_bytes(ctypes.byref(a)) == 0) == (key != "total_q"), key
     for key, value in (("q", Q + 8), ("k", K + 2), ("v", V + 4), ("cu_q", CQ + 2), ("cu_k", CK + 1), ("out", OUT + 8),
                        ("lse", LSE + 1), ("q_stride", 516), ("k_stride", 132), ("v_stride", 129)):
         assert call(**{key: value}) == B.GRINQH_EALIGN, (key, value)

@@ -67,7 +67,8 @@ def test_decode_matches_the_oracle(dev, bits, heads, group, dim, page, lens):
         _decode(c, _queries(rng, len(lens), heads * group, dim, q_dtype), q_dtype, out_dtype, dev)
 
 
-@pytest.mark.parametrize("bits,heads,group,dim,page,n", [(8, 2, 4, 128, 64, 20011), (4, 1, 8, 128, 128, 30001),
+@pytest.mark.parametrize("bits,heads,group,dim,page,n", [(8, 1, 16, 256, 64, 9001), (4, 1, 16, 128, 16, 12345),
+                                                         (16, 1, 24, 64, 128, 8000), (8, 2, 4, 128, 64, 20011), (4, 1, 8, 128, 128, 30001),
                                                          (16, 1, 2, 64, 16, 9000), (8, 1, 3, 256, 32, 5003)])
 def test_decode_over_a_long_cache(dev, bits, heads, group, dim, page, n):
     """One sequence, many parts, joined."""
@@ -362,6 +363,49 @@ def test_keys_that_are_not_seen_may_be_anything(dev, dim):
         assert torch.equal(out[:150], base[:150]) and torch.equal(out[200:290], base[200:290])
         if bad is np.nan:
             assert torch.isnan(out[150:200]).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_infinities_in_seen_values_go_where_the_formula_says(dev, dim):
+    """Into the queries that see them and the dimension they are in: up, down,
+    and NaN where both or a NaN is seen; in tiles seen whole and in part."""
+    import input_adaptive_bit_amd as G
+    import torch
+    rng = np.random.default_rng(9)
+    q, k, v, cu_q, cu_k = _packed(rng, 2, 1, dim, [300], [300])
+    t = [to_bf16(x, dev) for x in (q, k)] + [torch.from_numpy(x).to(dev) for x in (cu_q, cu_k)]
+    base = G.prefill_attention(t[0], t[1], to_bf16(v, dev), *t[2:], scale=0.01, out_dtype=torch.float32)
+    want = base.clone()
+    bad = v.copy()
+    for key, d, x in ((20, 3, np.inf), (100, 40, -np.inf), (150, 3, np.inf), (200, 40, np.inf), (250, 9, np.nan)):
+        bad[key, 0, d] = x
+        want[key:, :, d] += float(x)
+    out = G.prefill_attention(t[0], t[1], to_bf16(bad, dev), *t[2:], scale=0.01, out_dtype=torch.float32)
+    assert torch.equal(out.isnan(), want.isnan())
+    assert torch.equal(out.isposinf(), want.isposinf()) and torch.equal(out.isneginf(), want.isneginf())
+    assert torch.equal(out[want.isfinite()], want[want.isfinite()])
+
+
+def test_prefill_of_very_many_sequences(dev):
+    """More than 64 x 64, empty ones among them, against one call for each run."""
+    import input_adaptive_bit_amd as G
+    import torch
+    rng = np.random.default_rng(10)
+    lens = rng.integers(0, 5, 5000)
+    lens[[17, 4999]] = [200, 90]
+    q, k, v, cu, _ = _packed(rng, 2, 1, 64, lens, lens)
+    t = [to_bf16(x, dev) for x in (q, k, v)]
+    out = G.prefill_attention(*t, torch.from_numpy(cu).to(dev), out_dtype=torch.float32)
+    for a, b in ((0, 40), (1000, 1050), (4960, 5000)):
+        r = slice(cu[a], cu[b])
+        o, bound, _, _ = prefill_reference(q[r], k[r], v[r], cu[a:b + 1] - cu[a], cu[a:b + 1] - cu[a], 0.125, True, "f32")
+        inside(_np(out[r]), o, bound, f"{a}..{b}")
+    for a in range(0, 5000, 50):
+        r = slice(cu[a], cu[a + 50])
+        if cu[a] < cu[a + 50]:
+            few = G.prefill_attention(*(x[r] for x in t), torch.from_numpy(cu[a:a + 51] - cu[a]).to(dev),
+                                      out_dtype=torch.float32)
+            assert torch.equal(out[r], few), a
 
 
 def test_prefill_takes_slices_of_a_fused_projection(dev):
