@@ -351,6 +351,12 @@ grinqh_status grinqh_kv_read(const grinqh_kv_layout* L, const grinqh_kv_pools* p
  * pool, a head outside 0 .. n_kv_heads - 1 or an invalid layout. */
 int64_t grinqh_debug_kv_row(const grinqh_kv_layout* L, int64_t slot, int32_t head);
 
+/* Test call, host only: the row index that the decode attention reads for
+ * token t of a sequence and head from a page table's entry; for an entry that
+ * names no page of the pool, -1 minus the row that is read in its stead and not
+ * used.  -1 for a negative t, a head outside the layout or an invalid layout. */
+int64_t grinqh_debug_page_row(const grinqh_kv_layout* L, int32_t page, int32_t head, int32_t t);
+
 /* ---- Attention -----------------------------------------------------------
  *
  * For every query head h of a query token, with key-value head

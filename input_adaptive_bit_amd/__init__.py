@@ -18,7 +18,7 @@ from .grinqh import (  # noqa: F401
 )
 from .attention import (  # noqa: F401
     KVLayout, KVCache, grinqh_kv_layout_init, grinqh_kv_code_bytes, grinqh_kv_grid_bytes, grinqh_kv_write,
-    grinqh_kv_read, grinqh_debug_kv_row, grinqh_attention_workspace_bytes, grinqh_decode_attention,
+    grinqh_kv_read, grinqh_debug_kv_row, grinqh_debug_page_row, grinqh_attention_workspace_bytes, grinqh_decode_attention,
     grinqh_prefill_attention, grinqh_prefill_attention_workspace_bytes, new_kv_cache, new_attention_workspace, kv_write, kv_read, decode_attention,
     prefill_attention,
 )

@@ -43,6 +43,10 @@ def grinqh_debug_kv_row(L: KVLayout, slot: int, head: int) -> int:
     return int(load().grinqh_debug_kv_row(ctypes.byref(L), int(slot), int(head)))
 
 
+def grinqh_debug_page_row(L: KVLayout, page: int, head: int, t: int) -> int:
+    return int(load().grinqh_debug_page_row(ctypes.byref(L), int(page), int(head), int(t)))
+
+
 def grinqh_attention_workspace_bytes(L: KVLayout, n_q_heads: int, batch: int, max_len: int) -> int:
     return int(load().grinqh_attention_workspace_bytes(ctypes.byref(L), int(n_q_heads), int(batch), int(max_len)))
 

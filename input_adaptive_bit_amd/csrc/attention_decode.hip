@@ -120,9 +120,7 @@ struct Tile {
 // there read page 0, and nothing of it is used).
 __device__ __forceinline__ void tile_rows(int64_t (&row)[2], const DecodeArgs& a, int t0, const int (&page)[2], int head) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-        row[h] = ((static_cast<int64_t>(max(page[h], 0)) * a.d.heads + head) << a.d.page_shift) +
-                 ((t0 + 16 * h) & ((1 << a.d.page_shift) - 1));
+    for (int h = 0; h < 2; ++h) row[h] = page_row(a.d, page[h], head, t0 + 16 * h);
 }
 
 template <int D, int BITS>
@@ -431,7 +429,7 @@ __global__ __launch_bounds__(W * kWave, waves_per_simd(D, QP, W)) void decode_ke
     const auto check_pages = [&](int t0, int end, int (&page)[2]) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-            if (t0 + 16 * h >= end || static_cast<unsigned>(page[h]) >= static_cast<unsigned>(a.d.n_pages)) page[h] = -1;
+            page[h] = t0 + 16 * h < end ? page_or_absent(page[h], a.d.n_pages) : -1;
     };
     Tile<D, BITS> T;
     int64_t row[2];

@@ -176,9 +176,9 @@ __device__ __forceinline__ Place find_tile(const Args& a, int group, int rows, i
         const uint64_t over = __ballot(before + sum > number);
         if (over == 0) return Place{-1, -1, 0};
         const int at = __builtin_ctzll(over);
-        before += __shfl(sum, at) - __shfl(tiles, at);
-        count = __shfl(r1 - r0, at);
-        first = __shfl(r0, at);
+        before += __builtin_amdgcn_readlane(sum, at) - __builtin_amdgcn_readlane(tiles, at);
+        count = __builtin_amdgcn_readlane(r1 - r0, at);
+        first = __builtin_amdgcn_readlane(r0, at);
     }
     int seq = first + lane, tiles = lane < count ? tiles_of(a, group, rows, seq) : 0;
     if (a.batch > 1 && a.batch <= kWave) {

@@ -274,6 +274,13 @@ int64_t grinqh_debug_kv_row(const grinqh_kv_layout* L, int64_t slot, int32_t hea
     return kv_row(kv_dims(*L), slot, head);
 }
 
+int64_t grinqh_debug_page_row(const grinqh_kv_layout* L, int32_t page, int32_t head, int32_t t) {
+    if (!valid_kv_layout(L) || head < 0 || head >= L->n_kv_heads || t < 0) return -1;
+    const KvDims d = kv_dims(*L);
+    const int there = page_or_absent(page, d.n_pages);
+    return there < 0 ? -1 - page_row(d, there, head, t) : page_row(d, there, head, t);
+}
+
 grinqh_status grinqh_kv_write(const grinqh_kv_layout* L, const grinqh_kv_pools* pools, const void* k,
                               const void* v, grinqh_dtype dtype, int64_t k_stride, int64_t v_stride,
                               int32_t n_tokens, const int64_t* slots, void* stream) {

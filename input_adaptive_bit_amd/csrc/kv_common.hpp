@@ -32,6 +32,18 @@ __host__ __device__ __forceinline__ int64_t kv_row(const KvDims& d, int64_t slot
     return ((page * d.heads + head) << d.page_shift) + t;
 }
 
+// A page table's entry, or -1 where it names no page of the pool.
+__host__ __device__ __forceinline__ int page_or_absent(int page, int n_pages) {
+    return static_cast<unsigned>(page) < static_cast<unsigned>(n_pages) ? page : -1;
+}
+
+// Row of token t of a sequence in the page that holds it.  An absent page gives a
+// row of page 0: the pool may be read there, and nothing of it is used.
+__host__ __device__ __forceinline__ int64_t page_row(const KvDims& d, int page, int head, int t) {
+    const int64_t at = page < 0 ? 0 : page;
+    return ((at * d.heads + head) << d.page_shift) + (t & ((1 << d.page_shift) - 1));
+}
+
 // Largest sizes the calls accept.
 constexpr int kMaxKvHeads = 1024, kMaxQHeads = 1024;
 constexpr int64_t kMaxStride = int64_t{1} << 24;   // elements between tokens

@@ -76,7 +76,7 @@ EXPORTS = ("grinqh_version", "grinqh_status_string", "grinqh_layout_init", "grin
            "grinqh_calibrate_workspace_bytes", "grinqh_calibrate_thresholds", "grinqh_quantize_rtn",
            "grinqh_prefill_workspace_bytes", "grinqh_prefill_gemm",
            "grinqh_kv_layout_init", "grinqh_kv_code_bytes", "grinqh_kv_grid_bytes", "grinqh_kv_write",
-           "grinqh_kv_read", "grinqh_debug_kv_row", "grinqh_attention_workspace_bytes",
+           "grinqh_kv_read", "grinqh_debug_kv_row", "grinqh_debug_page_row", "grinqh_attention_workspace_bytes",
            "grinqh_decode_attention", "grinqh_prefill_attention", "grinqh_prefill_attention_workspace_bytes")
 
 _lib = None
@@ -151,6 +151,8 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.grinqh_kv_read.restype = ctypes.c_int
     lib.grinqh_debug_kv_row.argtypes = [KP, i64, i32]
     lib.grinqh_debug_kv_row.restype = i64
+    lib.grinqh_debug_page_row.argtypes = [KP, i32, i32, i32]
+    lib.grinqh_debug_page_row.restype = i64
     lib.grinqh_attention_workspace_bytes.argtypes = [KP, i32, i32, i32]
     lib.grinqh_attention_workspace_bytes.restype = sz
     lib.grinqh_decode_attention.argtypes = [KP, PP, vp, ctypes.c_int, i64, i32, vp, i64, i32, vp, i32, i32,

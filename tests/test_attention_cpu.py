@@ -93,6 +93,22 @@ def test_rows_of_slots(heads, page, n_pages):
     assert len(set(rows)) == len(rows)
 
 
+@pytest.mark.parametrize("heads,page,n_pages", [(1, 16, 1), (8, 64, 1000), (5, 256, 1 << 24)])
+def test_rows_of_page_table_entries(heads, page, n_pages):
+    """An entry of the pool gives its token's row; any other entry a row that
+    lies in the pool, marked as not to be used."""
+    L = G.grinqh_kv_layout_init(heads, 128, page, n_pages, 8)
+    for entry in (0, 1, n_pages - 1, n_pages, n_pages + 7, -1, -2 ** 31, 2 ** 31 - 1):
+        for head in {0, heads - 1}:
+            for t in (0, 15, page - 1, page, 5 * page + 3, 2 ** 28 - 1):
+                got = G.grinqh_debug_page_row(L, entry, head, t)
+                if 0 <= entry < n_pages:
+                    assert got == A.row_index(entry * page + t % page, head, heads, page, n_pages)
+                else:
+                    assert 0 <= -1 - got < heads * page * n_pages
+    assert G.grinqh_debug_page_row(L, 0, heads, 0) == -1 and G.grinqh_debug_page_row(L, 0, 0, -1) == -1
+
+
 def test_layout_sizes():
     L = G.grinqh_kv_layout_init(8, 128, 64, 10, 4)
     assert (L.row_bytes, G.grinqh_kv_code_bytes(L), G.grinqh_kv_grid_bytes(L)) == (64, 10 * 8 * 64 * 64, 10 * 8 * 64 * 4)
