@@ -22,6 +22,11 @@ from .grinqh import (GRINQH_BF16, GRINQH_EINVAL, GRINQH_F32, GrinqhError, KVLayo
                      _check, load)
 
 
+if torch is not None:
+    _CODES = {torch.bfloat16: GRINQH_BF16, torch.float32: GRINQH_F32}
+    _BF16, _I32, _I64 = torch.bfloat16, torch.int32, torch.int64
+
+
 # ------------------------------------------------------------------ host ----
 
 def grinqh_kv_layout_init(n_kv_heads: int, head_dim: int, page_size: int, n_pages: int, bits: int) -> KVLayout:
@@ -52,6 +57,10 @@ def grinqh_attention_workspace_bytes(L: KVLayout, n_q_heads: int, batch: int, ma
 
 
 # ---------------------------------------------------------------- checks ----
+#
+# Each call tests all its conditions in one expression, which costs a program
+# 2 us a call, and only if one fails goes through them one by one to say which.
+
 
 def _tensor(t, name, device=None):
     if not isinstance(t, torch.Tensor):
@@ -85,11 +94,10 @@ def _floats(t, name, device, numel):
 
 
 def _float_code(dtype, name) -> int:
-    if dtype is torch.bfloat16:
-        return GRINQH_BF16
-    if dtype is torch.float32:
-        return GRINQH_F32
-    raise TypeError(f"{name} must be bfloat16 or float32, not {dtype}")
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"{name} must be bfloat16 or float32, not {dtype}")
+    return code
 
 
 def _rows(t, name, heads, dim, device):
@@ -123,7 +131,7 @@ def _run(name, device, stream, *args) -> None:
     """Calls an entry point whose last argument is the stream, with the tensors'
     device current."""
     call, raw = getattr(load(), name), _raw_stream(device, stream)
-    if torch.cuda.current_device() == device.index:
+    if torch._C._cuda_getDevice() == device.index:
         status = call(*args, raw)
     else:
         with torch.cuda.device(device):
@@ -140,6 +148,13 @@ def _empty(shape, dtype, device, stream):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _empty_as(t, dtype, device, stream):
+    """An output of t's shape."""
+    if stream is None and t.dtype is dtype and t.device == device:       # the shorter way there
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
+    return _empty(t.shape, dtype, device, stream)
 
 
 def _zeros(n, device, stream):
@@ -199,17 +214,30 @@ def new_attention_workspace(L: KVLayout, n_q_heads: int, batch: int, max_len: in
 def grinqh_kv_write(cache: KVCache, k, v, slots, stream=None) -> None:
     """k, v: bf16 or fp32 [tokens][n_kv_heads][head_dim], token rows contiguous;
     slots: int64 [tokens]."""
-    device = cache.device
-    k_stride = _rows(k, "k", cache.n_kv_heads, cache.head_dim, device)
-    v_stride = _rows(v, "v", cache.n_kv_heads, cache.head_dim, device)
-    n = k.shape[0]
-    at = _plain(slots, "slots", torch.int64, device, n)
-    if v.shape[0] != n or slots.numel() != n:
-        raise ValueError("k, v and slots must name the same number of tokens")
-    if v.dtype != k.dtype:
-        raise TypeError("k and v must have one dtype")
-    _run("grinqh_kv_write", device, stream, *cache._refs, k.data_ptr(), v.data_ptr(), _float_code(k.dtype, "k"),
-         k_stride, v_stride, n, at)
+    device, heads, dim = cache.device, cache.n_kv_heads, cache.head_dim
+    index, width = device.index, heads * dim
+    try:
+        n, kh, kd = k.shape
+        (ks, k1, k2), (vs, v1, v2) = k.stride(), v.stride()
+        fits = (kh == heads and kd == dim and k2 == v2 == 1 and (k1 == v1 == dim or heads == 1)
+                and (n < 2 or (ks >= width and vs >= width)) and v.shape == k.shape and v.dtype is k.dtype
+                and k.dtype in _CODES and slots.dtype is _I64 and slots.is_contiguous() and slots.numel() == n
+                and k.get_device() == v.get_device() == slots.get_device() == index)
+    except (AttributeError, TypeError, ValueError):
+        fits = False
+    if not fits:
+        _rows(k, "k", heads, dim, device)
+        _rows(v, "v", heads, dim, device)
+        _plain(slots, "slots", _I64, device, k.shape[0])
+        if v.shape[0] != k.shape[0] or slots.numel() != k.shape[0]:
+            raise ValueError("k, v and slots must name the same number of tokens")
+        if v.dtype != k.dtype:
+            raise TypeError("k and v must have one dtype")
+        _float_code(k.dtype, "k")
+    if n < 2:
+        ks = vs = width                          # one token: its distance to the next is never used
+    _run("grinqh_kv_write", device, stream, *cache._refs, k.data_ptr(), v.data_ptr(), _CODES[k.dtype], ks, vs, n,
+         slots.data_ptr())
 
 
 def grinqh_kv_read(cache: KVCache, slots, k, v, stream=None) -> None:
@@ -217,7 +245,7 @@ def grinqh_kv_read(cache: KVCache, slots, k, v, stream=None) -> None:
     device = cache.device
     n = slots.numel()
     width = n * cache.n_kv_heads * cache.head_dim
-    _run("grinqh_kv_read", device, stream, *cache._refs, _plain(slots, "slots", torch.int64, device, n), n,
+    _run("grinqh_kv_read", device, stream, *cache._refs, _plain(slots, "slots", _I64, device, n), n,
          _floats(k, "k", device, width), _plain(v, "v", k.dtype, device, width), _float_code(k.dtype, "k"))
 
 
@@ -228,14 +256,14 @@ def kv_write(cache: KVCache, k, v, slots, stream=None) -> None:
 
 def kv_read(cache: KVCache, slots, out_dtype=None, stream=None):
     """(k, v) of the slots, [tokens][n_kv_heads][head_dim] (allocates them)."""
-    device, n = cache.device, slots.numel()
-    at = _plain(slots, "slots", torch.int64, device, n)
-    dtype = out_dtype or torch.bfloat16
+    device = cache.device
+    at = _plain(slots, "slots", _I64, device, 0)
+    n, dtype = slots.numel(), out_dtype or _BF16
     code = _float_code(dtype, "out_dtype")
     both = _empty((2, n, cache.n_kv_heads, cache.head_dim), dtype, device, stream)
-    k, v = both.unbind(0)
-    _run("grinqh_kv_read", device, stream, *cache._refs, at, n, k.data_ptr(), v.data_ptr(), code)
-    return k, v
+    k = both.data_ptr()
+    _run("grinqh_kv_read", device, stream, *cache._refs, at, n, k, k + both.nbytes // 2, code)
+    return both.unbind(0)
 
 
 # -------------------------------------------------------------- attention ---
@@ -247,26 +275,40 @@ def grinqh_decode_attention(cache: KVCache, q, page_table, seq_lens, max_len: in
     fp32, contiguous; lse: fp32 [batch][n_q_heads] or None; scale: default
     head_dim ** -0.5."""
     device, dim = cache.device, cache.head_dim
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise ValueError("q must be a [batch][n_q_heads][head_dim] tensor")
-    batch, heads, _ = q.shape
-    q_stride = _rows(q, "q", heads, dim, device)
-    _tensor(page_table, "page_table", device)
-    rows, max_pages = page_table.shape if page_table.dim() == 2 else (-1, -1)
-    if page_table.dtype is not torch.int32 or rows != batch:
-        raise ValueError("page_table must be int32 [batch][max_pages]")
-    if max_pages > 1 and page_table.stride(1) != 1:
-        raise ValueError("the rows of page_table must be contiguous")
-    _tensor(workspace, "workspace", device)
-    if not workspace.is_contiguous():
+    index = device.index
+    try:
+        batch, heads, last = q.shape
+        (q_stride, s1, s2), (rows, max_pages), (table_stride, t1) = q.stride(), page_table.shape, page_table.stride()
+        width = heads * dim
+        fits = (last == dim and s2 == 1 and (s1 == dim or heads == 1) and rows == batch and (t1 == 1 or max_pages < 2)
+                and (batch < 2 or q_stride >= width) and q.dtype in _CODES and out.dtype in _CODES
+                and page_table.dtype is _I32 and seq_lens.dtype is _I32 and seq_lens.is_contiguous()
+                and seq_lens.numel() >= batch and out.is_contiguous() and out.numel() >= batch * width
+                and workspace.is_contiguous() and q.get_device() == page_table.get_device() == seq_lens.get_device()
+                == out.get_device() == workspace.get_device() == index)
+    except (AttributeError, TypeError, ValueError):
+        fits = False
+    if not fits:
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise ValueError("q must be a [batch][n_q_heads][head_dim] tensor")
+        _rows(q, "q", q.shape[1], dim, device)
+        _float_code(q.dtype, "q")
+        _tensor(page_table, "page_table", device)
+        if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != q.shape[0]:
+            raise ValueError("page_table must be int32 [batch][max_pages]")
+        if page_table.shape[1] > 1 and page_table.stride(1) != 1:
+            raise ValueError("the rows of page_table must be contiguous")
+        _plain(seq_lens, "seq_lens", _I32, device, q.shape[0])
+        _floats(out, "out", device, q.numel())
+        _tensor(workspace, "workspace", device)
         raise ValueError("workspace must be contiguous")
-    _run("grinqh_decode_attention", device, stream, *cache._refs, q.data_ptr(), _float_code(q.dtype, "q"), q_stride,
-         heads, page_table.data_ptr(), page_table.stride(0) if batch > 1 else max_pages, max_pages,
-         _plain(seq_lens, "seq_lens", torch.int32, device, batch), batch, max_len,
-         dim ** -0.5 if scale is None else scale, _floats(out, "out", device, batch * heads * dim),
-         _float_code(out.dtype, "out"),
-         None if lse is None else _plain(lse, "lse", torch.float32, device, batch * heads),
-         workspace.data_ptr(), workspace.nbytes)
+    if batch < 2:
+        q_stride, table_stride = width, max_pages
+    _run("grinqh_decode_attention", device, stream, *cache._refs, q.data_ptr(), _CODES[q.dtype], q_stride, heads,
+         page_table.data_ptr(), table_stride, max_pages, seq_lens.data_ptr(), batch, max_len,
+         dim ** -0.5 if scale is None else scale, out.data_ptr(), _CODES[out.dtype],
+         None if lse is None else _plain(lse, "lse", torch.float32, device, batch * heads), workspace.data_ptr(),
+         workspace.nbytes)
 
 
 def decode_attention(cache: KVCache, q, page_table, seq_lens, max_len=None, scale=None, out_dtype=None,
@@ -278,10 +320,12 @@ def decode_attention(cache: KVCache, q, page_table, seq_lens, max_len=None, scal
     device = cache.device
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a [batch][n_q_heads][head_dim] tensor")
-    batch, heads, _ = q.shape
+    batch, heads, dim = q.shape
+    if dim != cache.head_dim:
+        raise ValueError(f"q must be [batch][n_q_heads][{cache.head_dim}], not {list(q.shape)}")
     if max_len is None:
         max_len = min(max(1, page_table.shape[1] * cache.layout.page_size), 1 << 28)
-    out = _empty((batch, heads, cache.head_dim), out_dtype or torch.bfloat16, device, stream)
+    out = _empty_as(q, out_dtype or torch.bfloat16, device, stream)
     lse = _empty((batch, heads), torch.float32, device, stream) if return_lse else None
     if workspace is None:
         workspace = _zeros(grinqh_attention_workspace_bytes(cache.layout, heads, batch, max_len), device, stream)
@@ -292,26 +336,38 @@ def decode_attention(cache: KVCache, q, page_table, seq_lens, max_len=None, scal
 def _prefill_args(q, k, v, cu_q, cu_k, out, causal, scale, lse):
     """The checked arguments of a prefill attention, without a workspace."""
     device = _tensor(q, "q")
-    if q.dim() != 3 or not isinstance(k, torch.Tensor) or k.dim() != 3:
-        raise ValueError("q and k must be [tokens][heads][head_dim]")
-    total_q, heads, dim = q.shape
-    total_k, kv_heads, _ = k.shape
-    q_stride = _rows(q, "q", heads, dim, device)
-    k_stride = _rows(k, "k", kv_heads, dim, device)
-    v_stride = _rows(v, "v", kv_heads, dim, device)
-    if v.shape[0] != total_k:
-        raise ValueError("k and v must hold the same tokens")
-    bf16 = torch.bfloat16
-    if q.dtype != bf16 or k.dtype != bf16 or v.dtype != bf16:
-        raise TypeError(f"q, k and v must be bfloat16, not {q.dtype}, {k.dtype}, {v.dtype}")
-    batch = cu_q.numel() - 1
-    if batch < 0 or cu_k.numel() != batch + 1:
-        raise ValueError("cu_q and cu_k must both be [batch + 1]")
+    index = device.index
+    try:
+        (total_q, heads, dim), (total_k, kv_heads, kd) = q.shape, k.shape
+        (qs, q1, q2), (ks, k1, k2), (vs, v1, v2) = q.stride(), k.stride(), v.stride()
+        q_width, width, ends = heads * dim, kv_heads * dim, cu_q.numel()
+        fits = (kd == dim and q2 == k2 == v2 == 1 and (q1 == dim or heads == 1) and (k1 == v1 == dim or kv_heads == 1)
+                and (total_q < 2 or qs >= q_width) and (total_k < 2 or (ks >= width and vs >= width))
+                and v.shape == k.shape and q.dtype is k.dtype is v.dtype is _BF16 and cu_q.dtype is cu_k.dtype is _I32
+                and cu_q.is_contiguous() and cu_k.is_contiguous() and cu_k.numel() == ends > 0 and out.dtype in _CODES
+                and out.is_contiguous() and out.numel() >= total_q * q_width and k.get_device() == v.get_device()
+                == cu_q.get_device() == cu_k.get_device() == out.get_device() == index)
+    except (AttributeError, TypeError, ValueError):
+        fits = False
+    if not fits:
+        if q.dim() != 3 or not isinstance(k, torch.Tensor) or k.dim() != 3:
+            raise ValueError("q and k must be [tokens][heads][head_dim]")
+        _rows(q, "q", q.shape[1], q.shape[2], device)
+        _rows(k, "k", k.shape[1], q.shape[2], device)
+        _rows(v, "v", k.shape[1], q.shape[2], device)
+        if v.shape[0] != k.shape[0]:
+            raise ValueError("k and v must hold the same tokens")
+        if q.dtype != _BF16 or k.dtype != _BF16 or v.dtype != _BF16:
+            raise TypeError(f"q, k and v must be bfloat16, not {q.dtype}, {k.dtype}, {v.dtype}")
+        _plain(cu_q, "cu_q", _I32, device, 1)
+        _plain(cu_k, "cu_k", _I32, device, 1)
+        if cu_k.numel() != cu_q.numel():
+            raise ValueError("cu_q and cu_k must both be [batch + 1]")
+        _floats(out, "out", device, q.numel())
     return PrefillAttentionArgs(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), q_stride, k_stride, v_stride,
-        _plain(cu_q, "cu_q", torch.int32, device, 1), _plain(cu_k, "cu_k", torch.int32, device, 1), batch, total_q,
-        total_k, heads, kv_heads, dim, bool(causal), dim ** -0.5 if scale is None else scale,
-        _floats(out, "out", device, total_q * heads * dim), _float_code(out.dtype, "out"),
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), qs if total_q > 1 else q_width, ks if total_k > 1 else width,
+        vs if total_k > 1 else width, cu_q.data_ptr(), cu_k.data_ptr(), ends - 1, total_q, total_k, heads, kv_heads, dim,
+        bool(causal), dim ** -0.5 if scale is None else scale, out.data_ptr(), _CODES[out.dtype],
         None if lse is None else _plain(lse, "lse", torch.float32, device, total_q * heads))
 
 
@@ -346,7 +402,7 @@ def prefill_attention(q, k, v, cu_q, cu_k=None, causal: bool = True, scale=None,
     device = _tensor(q, "q")
     if q.dim() != 3:
         raise ValueError("q must be [tokens][heads][head_dim]")
-    out = _empty(q.shape, out_dtype or torch.bfloat16, device, stream)
+    out = _empty_as(q, out_dtype or torch.bfloat16, device, stream)
     lse = _empty(q.shape[:2], torch.float32, device, stream) if return_lse else None
     a = _prefill_args(q, k, v, cu_q, cu_q if cu_k is None else cu_k, out, causal, scale, lse)
     n = load().grinqh_prefill_attention_workspace_bytes(ctypes.byref(a))

@@ -252,6 +252,86 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         G.new_attention_workspace(L, 3, 1, 10)
 
 
+def test_binding_says_what_does_not_fit():
+    """Every condition of the calls' joint test has its own message."""
+    import torch
+    from input_adaptive_bit_amd import attention as N
+
+    class Fake:
+        """Stands for a tensor on a GPU."""
+        def __init__(self, *shape, dtype=torch.bfloat16, stride=None, device=torch.device("cuda", 0)):
+            self.shape, self.dtype, self.device, self.is_cuda = torch.Size(shape), dtype, device, device.type == "cuda"
+            c = [1]
+            for n in reversed(shape[1:]):
+                c.insert(0, c[0] * n)
+            self._stride = tuple(stride or c)
+
+        def stride(self, i=None):
+            return self._stride if i is None else self._stride[i]
+
+        def dim(self):
+            return len(self.shape)
+
+        def numel(self):
+            return self.shape.numel()
+
+        def get_device(self):
+            return self.device.index if self.is_cuda else -1
+
+        def is_contiguous(self):
+            return all(n < 2 or s == c for n, s, c in zip(self.shape, self._stride, Fake(*self.shape)._stride))
+
+        def data_ptr(self):
+            return 4096
+
+        nbytes = 1 << 20
+
+    sent = []
+    orig = N._run, torch.Tensor
+    N._run = lambda name, *a: sent.append(name)
+    torch.Tensor = Fake
+    try:
+        cache = type("C", (), dict(device=torch.device("cuda", 0), n_kv_heads=2, head_dim=64, _refs=()))()
+        cpu, i32, i64, f16 = torch.device("cpu"), torch.int32, torch.int64, torch.float16
+        rows = lambda n=3, **kw: Fake(n, 2, 64, **kw)                                                  # noqa: E731
+
+        def refuse(call, *good, **bad):
+            call(*good)
+            assert sent.pop()
+            for at, others in bad.items():
+                for other in others:
+                    a = list(good)
+                    a[int(at[1:])] = other
+                    with pytest.raises((TypeError, ValueError)):
+                        call(*a)
+                    assert not sent, (call, at)
+
+        shapes = [rows(4), Fake(3, 2, 32), Fake(3, 1, 64), Fake(3, 128), rows(stride=(64, 64, 1)), rows(stride=(128, 1, 2)),
+                  rows(dtype=f16), rows(dtype=torch.float32), rows(device=cpu), rows(device=torch.device("cuda", 1)), None]
+        slots = [Fake(4, dtype=i64), Fake(3, dtype=i32), Fake(3, dtype=i64, stride=(2,)), Fake(3, dtype=i64, device=cpu), 7]
+        refuse(lambda *a: N.grinqh_kv_write(cache, *a), rows(), rows(), Fake(3, dtype=i64), _0=shapes, _1=shapes, _2=slots)
+
+        ints = [Fake(2, dtype=i32), Fake(3, dtype=i64), Fake(3, dtype=i32, stride=(2,)), Fake(3, dtype=i32, device=cpu), None]
+        q, out = Fake(3, 8, 64), Fake(3, 8, 64)
+        refuse(lambda q, t, n, o, w: N.grinqh_decode_attention(cache, q, t, n, 10, o, w),
+               q, Fake(3, 5, dtype=i32), Fake(3, dtype=i32), out, Fake(64),
+               _0=[Fake(3, 8, 32), Fake(3, 512), Fake(3, 8, 64, stride=(64, 64, 1)), Fake(3, 8, 64, dtype=f16),
+                   Fake(3, 8, 64, device=cpu), Fake(4, 8, 64), 1],
+               _1=[Fake(2, 5, dtype=i32), Fake(3, 5, dtype=i64), Fake(3, 5, dtype=i32, stride=(10, 2)), Fake(15, dtype=i32),
+                   Fake(3, 5, dtype=i32, device=cpu)],
+               _2=ints, _3=[Fake(3, 7, 64), Fake(3, 8, 64, dtype=f16), Fake(3, 8, 64, stride=(1024, 64, 1)), None],
+               _4=[Fake(64, device=cpu), Fake(64, stride=(2,))])
+
+        wide = [Fake(4, 2, 32), Fake(4, 128), Fake(4, 2, 64, stride=(64, 64, 1)), Fake(4, 2, 64, dtype=torch.float32),
+                Fake(4, 2, 64, device=cpu), None]
+        refuse(lambda *a: N.grinqh_prefill_attention(*a), q, Fake(4, 2, 64), Fake(4, 2, 64), Fake(3, dtype=i32),
+               Fake(3, dtype=i32), out, _0=[Fake(3, 8, 64, dtype=torch.float32), Fake(3, 8, 64, device=cpu), Fake(24, 64)],
+               _1=wide, _2=wide + [Fake(5, 2, 64)], _3=ints, _4=ints,
+               _5=[Fake(3, 7, 64), Fake(3, 8, 64, dtype=f16), Fake(3, 8, 64, device=cpu)])
+    finally:
+        N._run, torch.Tensor = orig
+
+
 def test_binding_takes_the_stride_of_a_token_and_refuses_other_views():
     import torch
     from input_adaptive_bit_amd import attention as N
