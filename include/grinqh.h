@@ -364,9 +364,10 @@ int64_t grinqh_debug_page_row(const grinqh_kv_layout* L, int32_t page, int32_t h
  *   o_h = sum_t p_t v_gt,  p_t = exp(a_t) / sum_u exp(a_u),  a_t = scale * q_h . k_gt,
  * over the tokens t that the query sees.  A query that sees none gets zeros.
  * lse_h = log(sum_t exp(a_t)) (-Inf where no token is seen).  Scores, softmax
- * statistics and sums are fp32.  Infinities and NaN in a token that is seen go
- * into the outputs of its heads as the formula says; in tokens that are not seen
- * they have no effect.
+ * statistics and sums are fp32.  Infinities and NaN in tokens that are seen go
+ * through the formula (where an infinite value makes it infinite, an output may
+ * be NaN; a query whose seen scores are all -Inf gets zeros); in tokens that are
+ * not seen they have no effect.
  *
  * Decode stage: one new token of every sequence attends to its cached
  * tokens (the new one among them, if it was written first).
@@ -379,8 +380,9 @@ int64_t grinqh_debug_page_row(const grinqh_kv_layout* L, int32_t page, int32_t h
  *               is absent: its tokens are not seen.
  *   seq_lens    int32 [batch]: cached tokens of each sequence, taken as 0 if
  *               negative and as min(max_len, max_pages * page_size) if above.
- *   batch       0 .. 2^20 (0: nothing is launched); max_len 1 .. 2^28, the
- *               host's bound on the lengths.
+ *   batch       0 .. 2^20 (0: nothing is launched), and batch * n_kv_heads *
+ *               ceil(n_q_heads / n_kv_heads / 16) at most 2^23; max_len 1 ..
+ *               2^28, the host's bound on the lengths.
  *   scale       -1e30 .. 1e30.
  *   out         [batch][n_q_heads][head_dim] of out_dtype, contiguous, 16-byte
  *               aligned.

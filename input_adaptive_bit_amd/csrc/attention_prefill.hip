@@ -24,6 +24,15 @@
 // The maximum is the first tile's until a score exceeds it by 30 (as powers of
 // two): weights up to 2^30 lose nothing in fp32 and bf16, and the sums are
 // hardly ever rescaled.
+//
+// What bounds it.  Matrix and vector instructions together: at 8192 tokens, 32
+// heads of 128 (530 - 580 us, 950 - 1040 TFLOP/s), the matrix cores are busy for 50%
+// of the cycles and the vector units for 50%, 41% of the matrix cycles with
+// vector work beside them, at 1.9 GHz; LDS reads take 25% and have no bank
+// conflicts.  A wave's own overlap (the halves of a tile) took it from 594 us; 64
+// rows to a wave would halve the LDS reads but leave one wave per SIMD.  Heads of
+// 64 have half the matrix work for the same exponentials: 720 TFLOP/s at 4096
+// tokens.
 #include <math.h>
 
 #include <algorithm>
@@ -223,7 +232,7 @@ __global__ __launch_bounds__(kPreThreads, D == 256 ? 1 : D == 64 ? 3 : 2) void p
     const int flat = blockIdx.x / a.n_kv_heads;             // and parts within a tile the next
     const int number = flat / most_parts, part = flat % most_parts;
     const Place at = find_tile(a, group, S::kRows, number, lane);
-    if (at.seq < 0) return;
+    if (at.seq < 0 || at.tile < 0 || at.tile >= at.tiles) return;   // (a tile outside: ends that do not ascend)
     const int seq = __builtin_amdgcn_readfirstlane(at.seq);
     // The last tiles of a causal sequence see the most keys and go first.
     const int tile = __builtin_amdgcn_readfirstlane(a.causal ? at.tiles - 1 - at.tile : at.tile);
@@ -499,17 +508,36 @@ __global__ __launch_bounds__(kPreThreads, D == 256 ? 1 : D == 64 ? 3 : 2) void p
     if (out_row < 0) return;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-    for (int d = 0; d < DT; ++d)
+    for (int d = 0; d < DT; ++d) {
+        const auto y = [&](int r) { return o[d][r] * inv; };
+        if (a.out_dtype == GRINQH_F32) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-            store_four(a, out_row * D + 32 * d + 8 * x + 4 * (lane >> 5), o[d][4 * x] * inv, o[d][4 * x + 1] * inv,
-                       o[d][4 * x + 2] * inv, o[d][4 * x + 3] * inv);
+            for (int x = 0; x < 4; ++x)
+                *reinterpret_cast<float4*>(static_cast<float*>(a.out) + out_row * D + 32 * d + 8 * x + 4 * (lane >> 5)) =
+                    make_float4(y(4 * x), y(4 * x + 1), y(4 * x + 2), y(4 * x + 3));
+            continue;
+        }
+        // Two lanes hold a row: they swap quads, so that each has 8 neighbours of it
+        // and 16 bytes to store (six prompts of 33 .. 1200 tokens: 50 us with 8, 46 so).
+#pragma unroll
+        for (int x = 0; x < 4; x += 2) {
+            u32x4 w;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const u32x2 z = __builtin_amdgcn_permlane32_swap(pack_bf16(y(4 * x + 2 * e), y(4 * x + 2 * e + 1)),
+                                                                 pack_bf16(y(4 * x + 4 + 2 * e), y(4 * x + 5 + 2 * e)), false, false);
+                w[e] = z.x;
+                w[2 + e] = z.y;
+            }
+            *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.out) + out_row * D + 32 * d + 8 * x + 8 * (lane >> 5)) = w;
+        }
+    }
     if (a.lse != nullptr && lane < 32) a.lse[out_row] = lse_of(top, sum, c);
 }
 
 // Joins the parts of every tile that has several.  A workgroup takes
 // kJoinRows rows of a tile; D / 4 lanes hold a row, four values each.
-constexpr int kJoinRows = 32;
+constexpr int kJoinRows = 32, kJoinBatch = 4;           // rows of a workgroup; parts asked for at a time
 
 template <int D>
 __global__ __launch_bounds__(kPreThreads) void join_kernel(Args a, float c, int most_parts) {
@@ -517,7 +545,7 @@ __global__ __launch_bounds__(kPreThreads) void join_kernel(Args a, float c, int 
     const int lane = threadIdx.x & 63, group = a.n_q_heads / a.n_kv_heads;
     const int head = blockIdx.x % a.n_kv_heads, number = blockIdx.x / a.n_kv_heads;
     const Place at = find_tile(a, group, S::kRows, number, lane);
-    if (at.seq < 0) return;
+    if (at.seq < 0 || at.tile < 0 || at.tile >= at.tiles) return;
     const int seq = at.seq, tile = a.causal ? at.tiles - 1 - at.tile : at.tile;
     const int q_begin = min(max(a.cu_q[seq], 0), a.total_q), q_end = min(max(a.cu_q[seq + 1], 0), a.total_q);
     const int k_begin = min(max(a.cu_k[seq], 0), a.total_k);
@@ -534,18 +562,36 @@ __global__ __launch_bounds__(kPreThreads) void join_kernel(Args a, float c, int 
         const int local = blockIdx.y * kJoinRows + u / kPerRow, x = u % kPerRow * 4;
         const int i = i0 + (rem0 + local) / group, h = head * group + (rem0 + local) % group;
         if (i >= n) continue;
-        float top = -INFINITY;
-        for (int p = 0; p < parts; ++p) top = fmaxf(top, from[p * step + S::kRows * D + 2 * local]);
-        const float base = top == -INFINITY ? 0.f : top;
-        float l = 0.f;
+        // A batch of parts is asked for at once (1.5 us less at four parts).
+        float top = -INFINITY, l = 0.f;
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int p = 0; p < parts; ++p) {
-            const float2 ml = *reinterpret_cast<const float2*>(from + p * step + S::kRows * D + 2 * local);
-            const float4 v = *reinterpret_cast<const float4*>(from + p * step + local * D + x);
-            const float f = __builtin_amdgcn_exp2f((ml.x - base) * c);
-            l = __builtin_fmaf(f, ml.y, l);
-            y = make_float4(__builtin_fmaf(f, v.x, y.x), __builtin_fmaf(f, v.y, y.y), __builtin_fmaf(f, v.z, y.z),
-                            __builtin_fmaf(f, v.w, y.w));
+        for (int p0 = 0; p0 < parts; p0 += kJoinBatch) {
+            float2 ml[kJoinBatch];
+            float4 v[kJoinBatch];
+#pragma unroll
+            for (int p = 0; p < kJoinBatch; ++p) {
+                const bool is = p0 + p < parts;
+                const float* part = from + (is ? p0 + p : p0) * step;
+                ml[p] = *reinterpret_cast<const float2*>(part + S::kRows * D + 2 * local);
+                v[p] = *reinterpret_cast<const float4*>(part + local * D + x);
+                if (!is) ml[p] = make_float2(-INFINITY, 0.f);
+            }
+            float next = top;
+#pragma unroll
+            for (int p = 0; p < kJoinBatch; ++p) next = fmaxf(next, ml[p].x);
+            const float base = next == -INFINITY ? 0.f : next;
+            const float keep = top == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((top - base) * c);
+            top = next;
+            l *= keep;
+            y = make_float4(y.x * keep, y.y * keep, y.z * keep, y.w * keep);
+#pragma unroll
+            for (int p = 0; p < kJoinBatch; ++p) {
+                if (p0 + p >= parts) continue;
+                const float f = __builtin_amdgcn_exp2f((ml[p].x - base) * c);
+                l = __builtin_fmaf(f, ml[p].y, l);
+                y = make_float4(__builtin_fmaf(f, v[p].x, y.x), __builtin_fmaf(f, v[p].y, y.y), __builtin_fmaf(f, v[p].z, y.z),
+                                __builtin_fmaf(f, v[p].w, y.w));
+            }
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const int64_t row = static_cast<int64_t>(q_begin + i) * a.n_q_heads + h;
