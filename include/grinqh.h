@@ -426,7 +426,7 @@ grinqh_status grinqh_decode_attention(const grinqh_kv_layout* L, const grinqh_kv
  *              are worked on in parts and joined by a second kernel.  The size
  *              follows from the sizes in args and causal alone (0: it would not
  *              be used, or a size is invalid).
- * total_q * n_q_heads / 128 + batch * n_kv_heads is at most 2^23.
+ * total_q * n_q_heads / 128 + min(batch, total_q) * n_kv_heads is at most 2^23.
  * The weights p_t are rounded to bf16 for the product with the values. */
 typedef struct {
     const void* q;

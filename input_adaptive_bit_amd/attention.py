@@ -398,7 +398,8 @@ def prefill_attention(q, k, v, cu_q, cu_k=None, causal: bool = True, scale=None,
                       return_lse: bool = False, stream=None):
     """Attention over packed prompts: out [total_q][n_q_heads][head_dim], and
     lse [total_q][n_q_heads] if asked for (allocates them, and the workspace).
-    cu_k defaults to cu_q (every prompt's keys are its own tokens)."""
+    cu_k defaults to cu_q (every prompt's keys are its own tokens). Rows behind
+    the last sequence are left as they are allocated."""
     device = _tensor(q, "q")
     if q.dim() != 3:
         raise ValueError("q must be [tokens][heads][head_dim]")

@@ -606,7 +606,9 @@ template <int D>
 PrePlan plan_prefill(const Args& a) {
     PrePlan p;
     const int64_t group = a.n_q_heads / a.n_kv_heads;
-    p.tiles = a.total_q * group / PreShape<D>::kRows + a.batch;                // at most, whatever the lengths
+    const int64_t rows = PreShape<D>::kRows, dense = (a.total_q * group + rows - 1) / rows;
+    const int64_t some = std::min(a.batch, a.total_q);                         // sequences that have queries, at most
+    p.tiles = a.total_q * group / rows + some;                                 // at most, whatever the lengths
     // Parts where they make the call shorter, by what was measured: a tile of keys
     // takes a workgroup alone on its CU t us, two on one CU 1.35 and three 1.8
     // times that (where there is room for them), and the parts cost a second
@@ -617,8 +619,9 @@ PrePlan plan_prefill(const Args& a) {
     constexpr int kFit = D == 64 ? 3 : D == 128 ? 2 : 1;
     constexpr double kTime = D == 64 ? 0.95 : D == 128 ? 1.2 : 2.1, kRate = D == 256 ? 1.7e6 : 2.5e6;   // us, bytes per us
     constexpr double kTogether[4] = {0.0, 1.0, 1.35, 1.8};
-    const int64_t rows = PreShape<D>::kRows, groups = (a.total_q * group + rows - 1) / rows * a.n_kv_heads;
-    const double keys = (a.total_k - (a.causal ? 0.5 * a.total_q : 0.0)) / std::max(1, a.batch);
+    // Every sequence leaves half a tile, and has one.
+    const int64_t groups = std::max(dense + (some - 1) / 2, some) * a.n_kv_heads;
+    const double keys = (a.total_k - (a.causal ? 0.5 * a.total_q : 0.0)) / std::max<int64_t>(1, some);
     const auto cost = [&](int64_t parts) {
         const int64_t deep = (groups * parts + kCus - 1) / kCus;               // workgroups on the fullest CU
         const double rounds = deep / kFit * kTogether[kFit] + kTogether[deep % kFit];

@@ -252,6 +252,21 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         G.new_attention_workspace(L, 3, 1, 10)
 
 
+def test_prefill_workspace_of_many_empty_sequences():
+    """A sequence without queries has no tile: the workspace and the limit follow
+    from the sequences that can have one, at most a query each."""
+    lib = G.load()
+    sizes = dict(n_q_heads=8, n_kv_heads=2, head_dim=128, causal=1, scale=0.1, q_stride=1024, k_stride=256, v_stride=256)
+
+    def need(**kw):
+        return lib.grinqh_prefill_attention_workspace_bytes(ctypes.byref(B.PrefillAttentionArgs(**dict(sizes, **kw))))
+
+    for queries in (1, 10, 40):
+        tiles, parts = queries * 4 // 128 + queries, 32                    # of a key-value head; of its keys, at most
+        for batch in (1, 2, 100, 5000, 1 << 20):
+            assert need(batch=batch, total_q=queries, total_k=1 << 24) <= tiles * 2 * parts * 128 * 130 * 4, (queries, batch)
+
+
 def test_binding_says_what_does_not_fit():
     """Every condition of the calls' joint test has its own message."""
     import torch

@@ -408,6 +408,30 @@ def test_prefill_of_very_many_sequences(dev):
             assert torch.equal(out[r], few), a
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+def test_few_queries_of_many_sequences_in_parts(dev, dim):
+    """Three of 300 sequences have queries, a fourth keys alone; with a workspace and without."""
+    import ctypes
+    import input_adaptive_bit_amd as G
+    from input_adaptive_bit_amd import grinqh as B
+    import torch
+    rng = np.random.default_rng(dim)
+    lens_q, lens_k = np.zeros(300, int), np.zeros(300, int)
+    lens_q[[0, 130, 299]], lens_k[[0, 7, 130, 299]] = [1, 5, 2], [3000, 500, 2777, 1]
+    q, k, v, cu_q, cu_k = _packed(rng, 8, 2, dim, lens_q, lens_k)
+    o, bound, lse, lse_bound = prefill_reference(q, k, v, cu_q, cu_k, dim ** -0.5, True, "f32")
+    t = [to_bf16(x, dev) for x in (q, k, v)]
+    cu = [torch.from_numpy(x).to(dev) for x in (cu_q, cu_k)]
+    a = B.PrefillAttentionArgs(batch=300, total_q=8, total_k=len(k), n_q_heads=8, n_kv_heads=2, head_dim=dim, causal=1)
+    assert G.load().grinqh_prefill_attention_workspace_bytes(ctypes.byref(a)) > 0
+    out, got = G.prefill_attention(*t, *cu, out_dtype=torch.float32, return_lse=True)
+    inside(_np(out), o, bound, "in parts")
+    inside(_np(got), lse, lse_bound, "lse")
+    whole = torch.empty_like(out)
+    G.grinqh_prefill_attention(*t, *cu, whole)
+    inside(_np(whole), o, bound, "whole")
+
+
 def test_prefill_takes_slices_of_a_fused_projection(dev):
     import input_adaptive_bit_amd as G
     import torch
