@@ -70,21 +70,15 @@ struct PreShape {
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 // 16 bytes per lane from a buffer straight into LDS, lane after lane from
-// `lds` (uniform).  Written out because the compiler, not knowing which tile an
-// LDS read is from, would wait for every such load before it; the kernel waits
+// `lds` + AT (uniform).  Written out because the compiler, not knowing which tile
+// an LDS read is from, would wait for every such load before it; the kernel waits
 // for all of them itself, before the barrier that hands a tile over.
+template <int AT>
 __device__ __forceinline__ void load_to_lds(i32x4 rsrc, uint32_t off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 1\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+    asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 1\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  :
-                 : "s"(lds), "v"(off), "s"(rsrc)
-                 : "memory", "m0");
-}
-
-// A buffer over `rows` rows: what lies behind them reads as zeros.
-__device__ __forceinline__ i32x4 rows_rsrc(const uint16_t* base, int rows, uint32_t stride_bytes, int row_bytes) {
-    const uint64_t at = reinterpret_cast<uint64_t>(base);
-    const uint32_t bytes = rows > 0 ? (min(rows, 64) - 1) * stride_bytes + row_bytes : 0;
-    return i32x4{static_cast<int>(at), static_cast<int>(at >> 32) & 0xFFFF, static_cast<int>(bytes), 0x00020000};
+                 : "s"(lds), "v"(off), "s"(rsrc), "i"(AT)
+                 : "memory", "m0", "scc");
 }
 
 // A tile lies in LDS as rows of 2 D bytes, chunk c (16 bytes) of row r at
@@ -96,7 +90,7 @@ __device__ __forceinline__ constexpr int swizzle(int r) {
     return D == 64 ? (r & 7) ^ (r >> 3 & 1) : r & 15;
 }
 
-// Loads a tile (`rows` of it exist) into LDS in the order of LDS.  The lane's
+// Loads a tile into LDS in the order of LDS.  The lane's
 // chunk changes from one load to the next where they are 8 rows apart (keys of
 // head_dim 256).
 template <int D, bool VALUES>
@@ -109,19 +103,23 @@ struct TileLoad {
         for (int x = 0; x < kOffsets; ++x)
             off[x] = r * static_cast<uint32_t>(stride) * 2 + (slot ^ swizzle<D, VALUES>(r + x * kRowsAtOnce)) * 16;
     }
-    __device__ __forceinline__ void operator()(const uint16_t* base, int rows, int64_t stride, uint32_t lds, int wave) const {
-        const uint32_t stride_bytes = static_cast<uint32_t>(stride) * 2;
-        const i32x4 rs = rows_rsrc(base, rows, stride_bytes, D * 2);
+    // A tile at `from`; what lies `bytes` behind it and further reads as zeros.
+    __device__ __forceinline__ void operator()(uint64_t from, uint32_t bytes, uint32_t stride_bytes, uint32_t lds) const {
+        const i32x4 rs{static_cast<int>(from), static_cast<int>(from >> 32) & 0xFFFF, static_cast<int>(bytes), 0x00020000};
         uint32_t at[kOffsets];
 #pragma unroll
         for (int x = 0; x < kOffsets; ++x) {
             at[x] = off[x] + x * kRowsAtOnce * stride_bytes;
             asm volatile("" : "+v"(at[x]));             // one register each, not one for every load of the loop
         }
-#pragma unroll
-        for (int n = 0; n < PreShape<D>::kTK / kRowsAtOnce; ++n) {
-            load_to_lds(rs, at[n % kOffsets], lds + (n * kPreThreads + wave * kWave) * 16);
-            at[n % kOffsets] += kOffsets * kRowsAtOnce * stride_bytes;
+        load<0>(rs, at, stride_bytes, lds);
+    }
+    template <int N>
+    __device__ __forceinline__ void load(i32x4 rs, uint32_t (&at)[kOffsets], uint32_t stride_bytes, uint32_t lds) const {
+        if constexpr (N < PreShape<D>::kTK / kRowsAtOnce) {
+            load_to_lds<N * kPreThreads * 16>(rs, at[N % kOffsets], lds);
+            at[N % kOffsets] += kOffsets * kRowsAtOnce * stride_bytes;
+            load<N + 1>(rs, at, stride_bytes, lds);
         }
     }
 };
@@ -288,9 +286,19 @@ __global__ __launch_bounds__(kPreThreads, D == 256 ? 1 : D == 64 ? 3 : 2) void p
     const TileLoad<D, false> load_keys(a.k_stride);
     const TileLoad<D, true> load_values(a.v_stride);
     const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)&lds[0][0][0]));
-    const auto load = [&](int t0, int buf) {
-        load_keys(keys + t0 * a.k_stride, m - t0, a.k_stride, lds0 + buf * 2 * S::kBytes, wave);
-        load_values(values + t0 * a.v_stride, m - t0, a.v_stride, lds0 + (2 * buf + 1) * S::kBytes, wave);
+    // The next tile to load: where it is, and the bytes that exist of it.
+    const uint32_t k_bytes = static_cast<uint32_t>(a.k_stride) * 2, v_bytes = static_cast<uint32_t>(a.v_stride) * 2;
+    const int last = (m - 1) / TK, last_rows = (m - 1) % TK;
+    const uint32_t k_last = last_rows * k_bytes + 2 * D, v_last = last_rows * v_bytes + 2 * D;
+    uint64_t k_next = reinterpret_cast<uint64_t>(keys + static_cast<int64_t>(first * TK) * a.k_stride);
+    uint64_t v_next = reinterpret_cast<uint64_t>(values + static_cast<int64_t>(first * TK) * a.v_stride);
+    const uint32_t lds_wave = lds0 + wave * kWave * 16;
+    const auto load = [&](int t) {
+        const uint32_t at = lds_wave + (t & 1) * 2 * S::kBytes;
+        load_keys(k_next, t == last ? k_last : (TK - 1) * k_bytes + 2 * D, k_bytes, at);
+        load_values(v_next, t == last ? v_last : (TK - 1) * v_bytes + 2 * D, v_bytes, at + S::kBytes);
+        k_next += static_cast<uint64_t>(TK) * k_bytes;
+        v_next += static_cast<uint64_t>(TK) * v_bytes;
     };
     // Operand reads: this lane's place in a tile; steps and dimension tiles only
     // flip bits of the chunk.
@@ -337,7 +345,7 @@ __global__ __launch_bounds__(kPreThreads, D == 256 ? 1 : D == 64 ? 3 : 2) void p
         p[e / 4][e % 4] = w;
     };
 
-    if (first < tiles) load(first * TK, first & 1);
+    if (first < tiles) load(first);
     __builtin_amdgcn_s_waitcnt(0);                      // the queries too: nothing but tiles is waited for below
     // The inner loop never touches the output sums but to add to them.  A row whose
     // scores pass its maximum by too much leaves it and comes back to the same
@@ -352,7 +360,7 @@ __global__ __launch_bounds__(kPreThreads, D == 256 ? 1 : D == 64 ? 3 : 2) void p
         if (!again) {
             __builtin_amdgcn_s_waitcnt(0);              // this wave's share of the tile has arrived
             __syncthreads();                            // everyone's has; and the other buffer is free
-            if (t + 1 < tiles) load(t0 + TK, (t + 1) & 1);
+            if (t + 1 < tiles) load(t + 1);
         }
         again = false;
         const uint32_t kb = lds0 + (t & 1) * 2 * S::kBytes + k_at, vb = lds0 + (2 * (t & 1) + 1) * S::kBytes + v_at;
