@@ -256,14 +256,17 @@ def kv_write(cache: KVCache, k, v, slots, stream=None) -> None:
 
 def kv_read(cache: KVCache, slots, out_dtype=None, stream=None):
     """(k, v) of the slots, [tokens][n_kv_heads][head_dim] (allocates them)."""
-    device = cache.device
+    device, heads, dim = cache.device, cache.n_kv_heads, cache.head_dim
     at = _plain(slots, "slots", _I64, device, 0)
     n, dtype = slots.numel(), out_dtype or _BF16
     code = _float_code(dtype, "out_dtype")
-    both = _empty((2, n, cache.n_kv_heads, cache.head_dim), dtype, device, stream)
+    if stream is None:                           # the shorter way to the same tensor
+        both = torch.empty_strided((2, n, heads, dim), (n * heads * dim, heads * dim, dim, 1), dtype=dtype, device=device)
+    else:
+        both = _empty((2, n, heads, dim), dtype, device, stream)
     k = both.data_ptr()
     _run("grinqh_kv_read", device, stream, *cache._refs, at, n, k, k + both.nbytes // 2, code)
-    return both.unbind(0)
+    return torch.unbind(both)
 
 
 # -------------------------------------------------------------- attention ---
