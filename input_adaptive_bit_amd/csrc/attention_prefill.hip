@@ -38,6 +38,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "internal.h"
 #include "kv_common.hpp"
@@ -230,7 +231,11 @@ __global__ __launch_bounds__(kPreThreads, D == 256 ? 1 : D == 64 ? 3 : 2) void p
     // Heads are the fast index, so that with eight of them each XCD's L2 keeps one head's keys.
     const int head = blockIdx.x % a.n_kv_heads;
     const int flat = blockIdx.x / a.n_kv_heads;             // and parts within a tile the next
-    const int number = flat / most_parts, part = flat % most_parts;
+    // Short tiles have few parts.  The first part's place among a tile's moves on
+    // from tile to tile: otherwise, with a power of two of parts, some XCDs or
+    // shader engines would get all first parts and others all that are not there
+    // (1024 tokens, 32 heads of 128 in four parts: 41 us, 34 so).
+    const int number = flat / most_parts, part = (flat + number) % most_parts;
     const Place at = find_tile(a, group, S::kRows, number, lane);
     if (at.seq < 0 || at.tile < 0 || at.tile >= at.tiles) return;   // (a tile outside: ends that do not ascend)
     const int seq = __builtin_amdgcn_readfirstlane(at.seq);
@@ -547,7 +552,7 @@ __global__ __launch_bounds__(kPreThreads, D == 256 ? 1 : D == 64 ? 3 : 2) void p
 
 // Joins the parts of every tile that has several.  A workgroup takes
 // kJoinRows rows of a tile; D / 4 lanes hold a row, four values each.
-constexpr int kJoinRows = 32, kJoinBatch = 4;           // rows of a workgroup; parts asked for at a time
+constexpr int kJoinRows = 32, kJoinBatch = 8;           // rows of a workgroup; parts asked for at a time
 
 template <int D>
 __global__ __launch_bounds__(kPreThreads) void join_kernel(Args a, float c, int most_parts) {
@@ -572,7 +577,7 @@ __global__ __launch_bounds__(kPreThreads) void join_kernel(Args a, float c, int 
         const int local = blockIdx.y * kJoinRows + u / kPerRow, x = u % kPerRow * 4;
         const int i = i0 + (rem0 + local) / group, h = head * group + (rem0 + local) % group;
         if (i >= n) continue;
-        // A batch of parts is asked for at once (1.5 us less at four parts).
+        // A batch of parts is asked for at once: 2 us less than one after the other.
         float top = -INFINITY, l = 0.f;
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int p0 = 0; p0 < parts; p0 += kJoinBatch) {
@@ -580,11 +585,13 @@ __global__ __launch_bounds__(kPreThreads) void join_kernel(Args a, float c, int 
             float4 v[kJoinBatch];
 #pragma unroll
             for (int p = 0; p < kJoinBatch; ++p) {
-                const bool is = p0 + p < parts;
-                const float* part = from + (is ? p0 + p : p0) * step;
-                ml[p] = *reinterpret_cast<const float2*>(part + S::kRows * D + 2 * local);
-                v[p] = *reinterpret_cast<const float4*>(part + local * D + x);
-                if (!is) ml[p] = make_float2(-INFINITY, 0.f);
+                ml[p] = make_float2(-INFINITY, 0.f);
+                v[p] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (p0 + p < parts) {
+                    const float* part = from + (p0 + p) * step;
+                    ml[p] = *reinterpret_cast<const float2*>(part + S::kRows * D + 2 * local);
+                    v[p] = *reinterpret_cast<const float4*>(part + local * D + x);
+                }
             }
             float next = top;
 #pragma unroll
@@ -617,29 +624,51 @@ PrePlan plan_prefill(const Args& a) {
     const int64_t rows = PreShape<D>::kRows, dense = (a.total_q * group + rows - 1) / rows;
     const int64_t some = std::min(a.batch, a.total_q);                         // sequences that have queries, at most
     p.tiles = a.total_q * group / rows + some;                                 // at most, whatever the lengths
-    // Parts where they make the call shorter, by what was measured: a tile of keys
-    // takes a workgroup alone on its CU t us, two on one CU 1.35 and three 1.8
-    // times that (where there is room for them), and the parts cost a second
-    // launch and their way through memory.  512 queries after 7680 keys, 32 heads
-    // of 128, in 1, 2, 4, 5, 8 parts: 158, 101, 92, 106, 107 us; 128 queries: 150, 87,
-    // 58, 53, 49; 1024 queries of a prompt: 31 whole, 38 in two; two prompts of 257
-    // and 512 after 6000 keys, 28 heads of 64, in 1, 2, 4, 5: 97, 81, 66, 72.
+    // Parts where they make the call shorter, by a model of what was measured. A
+    // tile of keys takes a workgroup alone on its CU kTime us, two on one CU 1.35 and
+    // three 1.8 times that (where there is room for them); a call takes as long as
+    // its longest piece or as all pieces together; the parts cost a second launch
+    // and their way through memory. Sequences are taken to be alike, and a tile's
+    // keys to lie evenly between `least` and `most`. In us, the model's pick in
+    // brackets: 512 queries after 7680 keys, 32 heads of 128, in 1, 2, 3, [4], 5, 8
+    // parts: 158, 103, 103, 93, 108, 108; 4096 tokens, 4 heads of 128, 1, 2, [3], 4, 5,
+    // 8: 81, 54, 47, 42, 48, 54; 1024 tokens, 32 heads of 128, [1], 2, 3: 28, 34, 34;
+    // 1300 tokens, 6 heads of 256, 1, 2, 3, [4], 5: 51, 43, 39, 39, 40; 170 queries
+    // after 12806 keys, 6 heads of 64, 1, 4, 8, 16, [25]: 184, 57, 35, 27, 27.
     constexpr int kFit = D == 64 ? 3 : D == 128 ? 2 : 1;
-    constexpr double kTime = D == 64 ? 0.95 : D == 128 ? 1.2 : 2.1, kRate = D == 256 ? 1.7e6 : 2.5e6;   // us, bytes per us
+    constexpr double kTime = D == 64 ? 0.95 : D == 128 ? 1.2 : 2.1;            // us
+    constexpr double kJoin = 4.0, kRate = D == 64 ? 3.5e6 : D == 128 ? 3.0e6 : 1.8e6;   // us, bytes per us
     constexpr double kTogether[4] = {0.0, 1.0, 1.35, 1.8};
     // Every sequence leaves half a tile, and has one.
     const int64_t groups = std::max(dense + (some - 1) / 2, some) * a.n_kv_heads;
-    const double keys = (a.total_k - (a.causal ? 0.5 * a.total_q : 0.0)) / std::max<int64_t>(1, some);
-    const auto cost = [&](int64_t parts) {
-        const int64_t deep = (groups * parts + kCus - 1) / kCus;               // workgroups on the fullest CU
-        const double rounds = deep / kFit * kTogether[kFit] + kTogether[deep % kFit];
-        const double bytes = 2.0 * groups * parts * rows * (D + 2) * sizeof(float);
-        return kTime * keys / PreShape<D>::kTK * rounds / parts + (parts > 1 ? 5.0 + bytes / kRate : 0.0);
+    const double most = static_cast<double>(a.total_k) / std::max<int64_t>(1, some);
+    const double least = a.causal ? std::max(0.0, most - static_cast<double>(a.total_q) / std::max<int64_t>(1, some)) : most;
+    const auto share = [&](double keys) {               // of the tiles, with that many keys or more
+        return keys <= least ? 1.0 : keys > most ? 0.0 : (most - keys) / (most - least);
+    };
+    const auto cost = [&](int parts, double pieces) {   // pieces of a tile on average
+        const double per_cu = groups * pieces / kCus, full = std::min<double>(kFit, std::max(1.0, per_cu));
+        const int64_t deep = static_cast<int64_t>(std::max(1.0, std::ceil(per_cu))), at = static_cast<int64_t>(full);
+        const double all = (least + most) / 2 / pieces * (deep / kFit * kTogether[kFit] + kTogether[deep % kFit]);
+        double longest = most / parts;
+        if (parts > 1 && least < parts * kMinPart)      // a tile with keys for one part less
+            longest = std::max(longest, static_cast<double>(parts * kMinPart) / (parts - 1));
+        longest *= kTogether[at] + (at < kFit ? (full - at) * (kTogether[at + 1] - kTogether[at]) : 0.0);
+        const double bytes = 2.0 * groups * (pieces - 1 + share(2 * kMinPart)) * rows * (D + 2) * sizeof(float);
+        return kTime / PreShape<D>::kTK * std::max(all, longest) + (parts > 1 ? kJoin + bytes / kRate : 0.0);
     };
     p.parts = 1;
-    if (groups < 3 * kCus)
-        for (int parts = 2; parts <= std::min(kMaxParts, a.total_k / kMinPart); ++parts)
-            if (cost(parts) < cost(p.parts)) p.parts = parts;
+    if (groups < 3 * kCus) {
+        double pieces = 1.0, best = cost(1, 1.0);
+        for (int parts = 2; parts <= kMaxParts && parts * kMinPart <= most; ++parts) {
+            pieces += share(parts * kMinPart);
+            const double c = cost(parts, pieces);
+            if (c < 0.97 * best) {
+                best = c;
+                p.parts = parts;
+            }
+        }
+    }
     p.ws_bytes = p.parts > 1 ? static_cast<size_t>(p.tiles) * a.n_kv_heads * p.parts * PreShape<D>::kRows * (D + 2) * sizeof(float) : 0;
     return p;
 }
