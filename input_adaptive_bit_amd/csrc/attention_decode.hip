@@ -679,24 +679,23 @@ DecodePlan plan_decode(const grinqh_kv_layout& L, int n_q_heads, int batch, int 
 }
 
 template <int D, int BITS>
-void launch_queries(const DecodeArgs& a, int waves, unsigned n, hipStream_t stream) {
+grinqh_status launch_queries(const DecodeArgs& a, int waves, unsigned n, hipStream_t stream) {
     const int here = a.group < kHeadTile ? a.group : kHeadTile;
     const size_t lds = static_cast<size_t>(waves) * std::max<size_t>(here * (D + 4 + 2) * sizeof(float), kWave * sizeof(f32x4));
     if (waves > 4) {
         constexpr int W = big_waves(D);
-        if (a.q_dtype == GRINQH_BF16) decode_kernel<D, BITS, 1, W><<<dim3(n), dim3(W * kWave), lds, stream>>>(a);
-        else decode_kernel<D, BITS, 2, W><<<dim3(n), dim3(W * kWave), lds, stream>>>(a);
-        return;
+        const auto kernel = a.q_dtype == GRINQH_BF16 ? decode_kernel<D, BITS, 1, W> : decode_kernel<D, BITS, 2, W>;
+        return launch_kernel(kernel, dim3(n), W * kWave, lds, stream, a);
     }
-    if (a.q_dtype == GRINQH_BF16) decode_kernel<D, BITS, 1, 4><<<dim3(n), dim3(256), lds, stream>>>(a);
-    else decode_kernel<D, BITS, 2, 4><<<dim3(n), dim3(256), lds, stream>>>(a);
+    const auto kernel = a.q_dtype == GRINQH_BF16 ? decode_kernel<D, BITS, 1, 4> : decode_kernel<D, BITS, 2, 4>;
+    return launch_kernel(kernel, dim3(n), 4 * kWave, lds, stream, a);
 }
 
 template <int D>
-void launch_bits(const DecodeArgs& a, int bits, int waves, unsigned n, hipStream_t stream) {
-    if (bits == 4) launch_queries<D, 4>(a, waves, n, stream);
-    else if (bits == 8) launch_queries<D, 8>(a, waves, n, stream);
-    else launch_queries<D, 16>(a, waves, n, stream);
+grinqh_status launch_bits(const DecodeArgs& a, int bits, int waves, unsigned n, hipStream_t stream) {
+    if (bits == 4) return launch_queries<D, 4>(a, waves, n, stream);
+    if (bits == 8) return launch_queries<D, 8>(a, waves, n, stream);
+    return launch_queries<D, 16>(a, waves, n, stream);
 }
 
 bool valid_heads(const grinqh_kv_layout* L, int n_q_heads, int batch, int max_len) {
@@ -773,10 +772,9 @@ grinqh_status grinqh_decode_attention(const grinqh_kv_layout* L, const grinqh_kv
     a.scale_log2 = scale * kLog2e;
     const unsigned n = static_cast<unsigned>(plan.items * plan.splits);
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    if (L->head_dim == 64) launch_bits<64>(a, L->bits, plan.waves, n, s);
-    else if (L->head_dim == 128) launch_bits<128>(a, L->bits, plan.waves, n, s);
-    else launch_bits<256>(a, L->bits, plan.waves, n, s);
-    return map_hip_error(hipGetLastError());
+    if (L->head_dim == 64) return launch_bits<64>(a, L->bits, plan.waves, n, s);
+    if (L->head_dim == 128) return launch_bits<128>(a, L->bits, plan.waves, n, s);
+    return launch_bits<256>(a, L->bits, plan.waves, n, s);
 }
 
 }  // extern "C"

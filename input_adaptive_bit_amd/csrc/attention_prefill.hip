@@ -686,10 +686,9 @@ grinqh_status launch_prefill_attention(const Args& a, hipStream_t stream) {
     else if (a.workspace_bytes < p.ws_bytes) return GRINQH_ENOSPACE;
     const float c = a.scale == 0.f ? 1.f : fabsf(a.scale) * kLog2e;
     const unsigned n = static_cast<unsigned>(p.tiles * a.n_kv_heads);
-    prefill_attention_kernel<D><<<dim3(n * p.parts), dim3(kPreThreads), 0, stream>>>(a, c, p.parts);
-    if (p.parts > 1)
-        join_kernel<D><<<dim3(n, PreShape<D>::kRows / kJoinRows), dim3(kPreThreads), 0, stream>>>(a, c, p.parts);
-    return map_hip_error(hipGetLastError());
+    const grinqh_status st = launch_kernel(prefill_attention_kernel<D>, dim3(n * p.parts), kPreThreads, 0, stream, a, c, p.parts);
+    if (p.parts == 1 || st != GRINQH_OK) return st;
+    return launch_kernel(join_kernel<D>, dim3(n, PreShape<D>::kRows / kJoinRows), kPreThreads, 0, stream, a, c, p.parts);
 }
 
 }  // namespace

@@ -189,36 +189,33 @@ bool aligned16(const void* p) { return aligned_to(p, 16); }
 
 // Picks KERNEL<head_dim, bits, T> for a layout and value type.
 template <template <int, int, typename> class Launch, typename Args>
-void dispatch(const grinqh_kv_layout& L, int dtype, dim3 grid, hipStream_t stream, const Args& a) {
+grinqh_status dispatch(const grinqh_kv_layout& L, int dtype, dim3 grid, hipStream_t stream, const Args& a) {
     const auto by_bits = [&](auto dim) {
         constexpr int D = decltype(dim)::value;
         const auto by_type = [&](auto bits) {
             constexpr int B = decltype(bits)::value;
-            if (dtype == GRINQH_BF16)
-                Launch<D, B, uint16_t>::run(grid, stream, a);
-            else
-                Launch<D, B, float>::run(grid, stream, a);
+            return dtype == GRINQH_BF16 ? Launch<D, B, uint16_t>::run(grid, stream, a) : Launch<D, B, float>::run(grid, stream, a);
         };
-        if (L.bits == 4) by_type(std::integral_constant<int, 4>());
-        else if (L.bits == 8) by_type(std::integral_constant<int, 8>());
-        else by_type(std::integral_constant<int, 16>());
+        if (L.bits == 4) return by_type(std::integral_constant<int, 4>());
+        if (L.bits == 8) return by_type(std::integral_constant<int, 8>());
+        return by_type(std::integral_constant<int, 16>());
     };
-    if (L.head_dim == 64) by_bits(std::integral_constant<int, 64>());
-    else if (L.head_dim == 128) by_bits(std::integral_constant<int, 128>());
-    else by_bits(std::integral_constant<int, 256>());
+    if (L.head_dim == 64) return by_bits(std::integral_constant<int, 64>());
+    if (L.head_dim == 128) return by_bits(std::integral_constant<int, 128>());
+    return by_bits(std::integral_constant<int, 256>());
 }
 
 template <int D, int B, typename T>
 struct WriteLaunch {
-    static void run(dim3 grid, hipStream_t stream, const KvWriteArgs& a) {
-        kv_write_kernel<D, B, T><<<grid, dim3(kKvThreads), 0, stream>>>(a);
+    static grinqh_status run(dim3 grid, hipStream_t stream, const KvWriteArgs& a) {
+        return launch_kernel(kv_write_kernel<D, B, T>, grid, kKvThreads, 0, stream, a);
     }
 };
 
 template <int D, int B, typename T>
 struct ReadLaunch {
-    static void run(dim3 grid, hipStream_t stream, const KvReadArgs& a) {
-        kv_read_kernel<D, B, T><<<grid, dim3(kKvThreads), 0, stream>>>(a);
+    static grinqh_status run(dim3 grid, hipStream_t stream, const KvReadArgs& a) {
+        return launch_kernel(kv_read_kernel<D, B, T>, grid, kKvThreads, 0, stream, a);
     }
 };
 
@@ -309,8 +306,7 @@ grinqh_status grinqh_kv_write(const grinqh_kv_layout* L, const grinqh_kv_pools* 
     }
     const KvWriteArgs a{kv_dims(*L), {k, v}, {pools->k_codes, pools->v_codes}, {pools->k_grid, pools->v_grid},
                         slots, {k_stride, v_stride}, n_tokens};
-    dispatch<WriteLaunch>(*L, dtype, row_grid(*L, n_tokens), static_cast<hipStream_t>(stream), a);
-    return map_hip_error(hipGetLastError());
+    return dispatch<WriteLaunch>(*L, dtype, row_grid(*L, n_tokens), static_cast<hipStream_t>(stream), a);
 }
 
 grinqh_status grinqh_kv_read(const grinqh_kv_layout* L, const grinqh_kv_pools* pools, const int64_t* slots,
@@ -330,8 +326,7 @@ grinqh_status grinqh_kv_read(const grinqh_kv_layout* L, const grinqh_kv_pools* p
             return GRINQH_EINVAL;
     const KvReadArgs a{kv_dims(*L), {pools->k_codes, pools->v_codes}, {pools->k_grid, pools->v_grid}, {k, v},
                        slots, n_tokens};
-    dispatch<ReadLaunch>(*L, dtype, row_grid(*L, n_tokens), static_cast<hipStream_t>(stream), a);
-    return map_hip_error(hipGetLastError());
+    return dispatch<ReadLaunch>(*L, dtype, row_grid(*L, n_tokens), static_cast<hipStream_t>(stream), a);
 }
 
 }  // extern "C"
