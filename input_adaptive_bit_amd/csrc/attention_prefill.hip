@@ -26,13 +26,13 @@
 // hardly ever rescaled.
 //
 // What bounds it.  Matrix and vector instructions together: at 8192 tokens, 32
-// heads of 128 (530 - 590 us, 930 - 1040 TFLOP/s), the matrix cores are busy for 52%
-// of the cycles and the vector units for 52%, 40% of the matrix cycles with
+// heads of 128 (520 - 570 us, 960 - 1060 TFLOP/s), the matrix cores are busy for 53%
+// of the cycles and the vector units for 53%, 40% of the matrix cycles with
 // vector work beside them, at 1.8 - 1.9 GHz; LDS reads take 26% and have no bank
 // conflicts.  A wave's own overlap (the halves of a tile) took it from 594 us; 64
 // rows to a wave would halve the LDS reads but leave one wave per SIMD.  Heads of
 // 64 have half the matrix work for the same exponentials: 720 TFLOP/s at 4096
-// tokens, the vector units busy for 58% of the cycles, the matrix cores for 31%.
+// tokens, the vector units busy for 60% of the cycles, the matrix cores for 32%.
 // Short prompts: a workgroup takes 2 us to find its rows, 3 to its first tile,
 // 1.2 a tile (two to a CU: 1.6) and 2 for its output.
 #include <math.h>
