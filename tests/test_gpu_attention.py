@@ -432,6 +432,30 @@ def test_few_queries_of_many_sequences_in_parts(dev, dim):
     inside(_np(whole), o, bound, "whole")
 
 
+def test_tokens_that_lie_gigabytes_apart(dev):
+    """The largest strides: rows of one buffer of 6.7 GB, against the same rows close together."""
+    import input_adaptive_bit_amd as G
+    import torch
+    stride, n, dim = 1 << 24, 200, 64
+    far = torch.empty(n * stride, dtype=torch.bfloat16, device=dev).as_strided((n, 4, dim), (stride, dim, 1))
+    near = torch.randn(n, 4, dim, device=dev).to(torch.bfloat16)
+    far.copy_(near)
+    cu = torch.tensor([0, n], dtype=torch.int32, device=dev)
+    slots = torch.arange(n, device=dev)
+    outs = []
+    for x in (far, near):
+        q, k, v = x[:, :2], x[:, 2:3], x[:, 3:]
+        cache = G.new_kv_cache(1, dim, 64, 4, 8, device=dev)
+        G.kv_write(cache, k, v, slots)
+        table = torch.arange(4, dtype=torch.int32, device=dev).expand(n, 4)
+        lens = torch.arange(1, n + 1, dtype=torch.int32, device=dev)
+        outs.append((G.prefill_attention(q, k, v, cu), cache.k_codes, cache.v_grid,
+                     G.decode_attention(cache, q, table.contiguous(), lens)))
+    torch.cuda.synchronize()
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+
+
 def test_prefill_takes_slices_of_a_fused_projection(dev):
     import input_adaptive_bit_amd as G
     import torch
