@@ -117,14 +117,35 @@ struct Shape {
     static constexpr int kVDims = D / 16;
 };
 
+// At 4 bits the heads of groups of up to 8 have two columns of the score tile each
+// (COPIES 2): column i and column i + 8 hold the same scores, and the lanes of the
+// first weigh the tokens of the tile's first half, those of the second the others,
+// as states of their own until the end.  Half the softmax work for each lane:
+// 131071 tokens take 42 us instead of 44 (and 40 with the waves that the registers
+// then allow), 32 sequences of 2048 22 instead of 24.  At 8 bits it gained nothing.
+__device__ __forceinline__ bool second_copy(int lane) { return (lane & 8) != 0; }
+
 // A wave's 32 tokens as loaded: keys of two score tiles, values of this lane's
-// 8 tokens, grids of the same 8 tokens.
-template <int D, int BITS>
+// 8 tokens, grids of the tokens that it weighs.
+template <int D, int BITS, int COPIES>
 struct Tile {
     uint32_t k[2][D * BITS / 128];
     uint32_t v[8][Shape<D, BITS>::kVDwords];
-    u32x4 kg[2], vg[2];
+    u32x4 kg[2 / COPIES], vg[2 / COPIES];
 };
+
+// The grids of a lane's tokens.
+template <int COPIES>
+__device__ __forceinline__ void load_grids(u32x4 (&to)[2 / COPIES], const uint16_t* grid, const int64_t (&row)[2], int lane) {
+    const int g = lane >> 4;
+    if constexpr (COPIES == 2) {
+        const int64_t first = row[0], other = row[1];
+        to[0] = *reinterpret_cast<const u32x4*>(grid + (second_copy(lane) ? other : first) * 2 + 8 * g);
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) to[h] = *reinterpret_cast<const u32x4*>(grid + row[h] * 2 + 8 * g);
+    }
+}
 
 // Row of the first token of each half of the tile at t0 (pages that are not
 // there read page 0, and nothing of it is used).
@@ -133,8 +154,8 @@ __device__ __forceinline__ void tile_rows(int64_t (&row)[2], const DecodeArgs& a
     for (int h = 0; h < 2; ++h) row[h] = page_row(a.d, page[h], head, t0 + 16 * h);
 }
 
-template <int D, int BITS>
-__device__ __forceinline__ void load_keys(Tile<D, BITS>& T, const DecodeArgs& a, const int64_t (&row)[2], int lane) {
+template <int D, int BITS, int COPIES>
+__device__ __forceinline__ void load_keys(Tile<D, BITS, COPIES>& T, const DecodeArgs& a, const int64_t (&row)[2], int lane) {
     using S = Shape<D, BITS>;
     const int i = lane & 15, g = lane >> 4;
 #pragma unroll
@@ -144,12 +165,12 @@ __device__ __forceinline__ void load_keys(Tile<D, BITS>& T, const DecodeArgs& a,
         for (int n = 0; n < S::kPieces; ++n)
             load_bytes<S::kPiece>(k + static_cast<uint32_t>(i * S::kRow + (4 * n + g) * S::kPiece),
                                   &T.k[h][n * S::kPiece / 4]);
-        if constexpr (BITS < 16) T.kg[h] = *reinterpret_cast<const u32x4*>(a.k_grid + row[h] * 2 + 8 * g);
     }
+    if constexpr (BITS < 16) load_grids<COPIES>(T.kg, a.k_grid, row, lane);
 }
 
-template <int D, int BITS>
-__device__ __forceinline__ void load_values(Tile<D, BITS>& T, const DecodeArgs& a, const int64_t (&row)[2], int lane) {
+template <int D, int BITS, int COPIES>
+__device__ __forceinline__ void load_values(Tile<D, BITS, COPIES>& T, const DecodeArgs& a, const int64_t (&row)[2], int lane) {
     using S = Shape<D, BITS>;
     const int i = lane & 15, g = lane >> 4;
 #pragma unroll
@@ -158,8 +179,8 @@ __device__ __forceinline__ void load_values(Tile<D, BITS>& T, const DecodeArgs& 
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             load_bytes<S::kVBytes>(v + static_cast<uint32_t>((4 * g + j) * S::kRow + i * S::kVBytes), T.v[4 * h + j]);
-        if constexpr (BITS < 16) T.vg[h] = *reinterpret_cast<const u32x4*>(a.v_grid + row[h] * 2 + 8 * g);
     }
+    if constexpr (BITS < 16) load_grids<COPIES>(T.vg, a.v_grid, row, lane);
 }
 
 __device__ __forceinline__ uint32_t pack_high(float lo, float hi) {   // bf16 of two floats that have one exactly
@@ -210,8 +231,8 @@ __device__ __forceinline__ constexpr int q_order(int e) {
 
 // Two rows of the transposed operand (dimensions 2 m2 and 2 m2 + 1 of this
 // lane's D / 16): its 8 tokens' values (codes below 16 bits) as bf16.
-template <int D, int BITS>
-__device__ __forceinline__ void value_pair(const Tile<D, BITS>& T, int m2, bf16x8 (&f)[2]) {
+template <int D, int BITS, int COPIES>
+__device__ __forceinline__ void value_pair(const Tile<D, BITS, COPIES>& T, int m2, bf16x8 (&f)[2]) {
     u32x4 r[2];
     if constexpr (BITS == 16) {
 #pragma unroll
@@ -265,10 +286,10 @@ struct State {
     float m, l, konst;
 };
 
-// The scores of a tile (exponents of base 2) of this lane's 8 tokens.
-template <int D, int BITS, int QP>
-__device__ __forceinline__ void tile_scores(float (&a)[8], const Tile<D, BITS>& T, const bf16x8 (&qf)[QP][D / 32],
-                                            float q_sum, float scale_log2) {
+// The scores of a tile (exponents of base 2) of the tokens that this lane weighs.
+template <int D, int BITS, int QP, int COPIES>
+__device__ __forceinline__ void tile_scores(float (&a)[8 / COPIES], const Tile<D, BITS, COPIES>& T,
+                                            const bf16x8 (&qf)[QP][D / 32], float q_sum, float scale_log2, int lane) {
     f32x4 sc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
     for (int s = 0; s < D / 32; ++s)
@@ -280,55 +301,60 @@ __device__ __forceinline__ void tile_scores(float (&a)[8], const Tile<D, BITS>& 
             __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < 8 / COPIES; ++e) {
         const int h = e / 4, r = e % 4;
+        const float x = COPIES == 2 && second_copy(lane) ? sc[1][r] : sc[h][r];
         if constexpr (BITS < 16) {
             const float s = f16_to_f32(static_cast<uint16_t>(T.kg[h][r])), z = f16_to_f32(static_cast<uint16_t>(T.kg[h][r] >> 16));
-            a[e] = scale_log2 * __builtin_fmaf(s, sc[h][r], __builtin_fmaf(0.5f, s, z) * q_sum);
+            a[e] = scale_log2 * __builtin_fmaf(s, x, __builtin_fmaf(0.5f, s, z) * q_sum);
         } else {
-            a[e] = scale_log2 * sc[h][r];
+            a[e] = scale_log2 * x;
         }
     }
 }
 
 // Folds a tile's scores and values into the state.
-template <int D, int BITS>
-__device__ __forceinline__ void use_values(State<D>& st, Tile<D, BITS>& T, float (&a)[8], int t0, int end,
+template <int D, int BITS, int COPIES>
+__device__ __forceinline__ void use_values(State<D>& st, Tile<D, BITS, COPIES>& T, float (&a)[8 / COPIES], int t0, int end,
                                            const int (&page)[2], int lane) {
+    static_assert(COPIES == 1 || BITS < 16, "values of 16 bits are cleared token by token, whoever weighs them");
+    constexpr int E = 8 / COPIES;                        // tokens that a lane weighs
     const int g = lane >> 4;
-    float vs[8], vz[8];
+    const bool second = COPIES == 2 && second_copy(lane);
+    float vs[E], vz[E];
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
+    for (int e = 0; e < E; ++e)
         if constexpr (BITS < 16) {
             vs[e] = f16_to_f32(static_cast<uint16_t>(T.vg[e / 4][e % 4]));
             vz[e] = f16_to_f32(static_cast<uint16_t>(T.vg[e / 4][e % 4] >> 16));
         }
     // A tile with tokens that are not there: no score, no value, whatever the memory holds.
     if (t0 + kTileTokens > end || page[0] < 0 || page[1] < 0) {
+        const auto seen = [&](int half, int r) { return page[half] >= 0 && t0 + 16 * half + 4 * g + r < end; };
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const bool seen = page[e / 4] >= 0 && t0 + 16 * (e / 4) + 4 * g + e % 4 < end;
-            a[e] = seen ? a[e] : -INFINITY;
+        for (int e = 0; e < E; ++e) {
+            const bool is = second ? seen(1, e % 4) : seen(e / 4, e % 4);
+            a[e] = is ? a[e] : -INFINITY;
             if constexpr (BITS < 16) {
-                vs[e] = seen ? vs[e] : 0.f;
-                vz[e] = seen ? vz[e] : 0.f;
+                vs[e] = is ? vs[e] : 0.f;
+                vz[e] = is ? vz[e] : 0.f;
             } else {
 #pragma unroll
-                for (int w = 0; w < Shape<D, BITS>::kVDwords; ++w) T.v[e][w] = seen ? T.v[e][w] : 0u;
+                for (int w = 0; w < Shape<D, BITS>::kVDwords; ++w) T.v[e][w] = is ? T.v[e][w] : 0u;
             }
         }
     }
     float top = a[0];
 #pragma unroll
-    for (int e = 1; e < 8; ++e) top = fmaxf(top, a[e]);
+    for (int e = 1; e < E; ++e) top = fmaxf(top, a[e]);
     const float m_new = fmaxf(st.m, over_groups_max(top));
     const float base = m_new == -INFINITY ? 0.f : m_new;
     const float keep = __builtin_amdgcn_exp2f(st.m - base);
     st.m = m_new;
     constexpr float mid = static_cast<float>(1 << (BITS - 1));
-    float p[8], l = 0.f, konst = 0.f;
+    float p[E], l = 0.f, konst = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < E; ++e) {
         p[e] = __builtin_amdgcn_exp2f(a[e] - base);
         l += p[e];
         if constexpr (BITS < 16) {
@@ -338,13 +364,22 @@ __device__ __forceinline__ void use_values(State<D>& st, Tile<D, BITS>& T, float
     }
     u32x4 hi, lo;
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
+    for (int x = 0; x < E / 2; ++x) {
         hi[x] = pack_bf16(p[2 * x], p[2 * x + 1]);
         const float r0 = __uint_as_float(hi[x] << 16), r1 = __uint_as_float(hi[x] & 0xFFFF0000u);
         lo[x] = pack_bf16(p[2 * x] - r0, p[2 * x + 1] - r1);
         if constexpr (BITS < 16) {
             const float s0 = r0 + __uint_as_float(lo[x] << 16), s1 = r1 + __uint_as_float(lo[x] & 0xFFFF0000u);
             konst = __builtin_fmaf(-mid, s0 + s1, konst);
+        }
+    }
+    if constexpr (COPIES == 2) {                         // the other copy's tokens weigh nothing here
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            hi[2 + x] = second ? hi[x] : 0u;
+            lo[2 + x] = second ? lo[x] : 0u;
+            hi[x] = second ? 0u : hi[x];
+            lo[x] = second ? 0u : lo[x];
         }
     }
     st.l = __builtin_fmaf(st.l, keep, l);
@@ -358,7 +393,7 @@ __device__ __forceinline__ void use_values(State<D>& st, Tile<D, BITS>& T, float
 #pragma unroll
     for (int m2 = 0; m2 < D / 32; ++m2) {
         bf16x8 vf[2];
-        value_pair<D, BITS>(T, m2, vf);
+        value_pair<D, BITS, COPIES>(T, m2, vf);
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
             f32x4& o = st.o[2 * m2 + y];
@@ -386,14 +421,25 @@ __device__ __forceinline__ void agent_store(float* p, float2 v) {
                        __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Waves of a workgroup that has a CU to itself, as many as its registers allow.
-__host__ __device__ constexpr int big_waves(int D) { return D == 256 ? 8 : 12; }
+// Columns of the score tile that a head has.
+__host__ __device__ constexpr int copies_of(int bits, int group) { return bits == 4 && group <= kHeadTile / 2 ? 2 : 1; }
+
+// Waves of a workgroup that has a CU to itself, as many as its registers allow
+// (fp32 queries: twelve at 128 dimensions; the plan does not know the type).
+__host__ __device__ constexpr int big_waves(int D, int copies, int qp = 1) {
+    return D == 256 ? 8 : copies == 2 && (D == 64 || qp == 1) ? 16 : 12;
+}
 
 __host__ __device__ constexpr int waves_per_simd(int D, int qp, int waves) {
     return waves > 4 ? waves / 4 : D == 256 || qp == 2 ? 2 : 3;
 }
 
-template <int D, int BITS, int QP, int W>
+// x of the lane 8 further round the row of 16.
+__device__ __forceinline__ float other_copy(float x) {
+    return __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(x), 0x128, 0xF, 0xF, true));   // row_ror:8
+}
+
+template <int D, int BITS, int QP, int W, int COPIES>
 __global__ __launch_bounds__(W * kWave, waves_per_simd(D, QP, W)) void decode_kernel(DecodeArgs a) {
     using S = Shape<D, BITS>;
     constexpr int kDecWaves = W, kDecThreads = W * kWave, kUnit = W * kTileTokens;   // tokens of one round
@@ -409,6 +455,7 @@ __global__ __launch_bounds__(W * kWave, waves_per_simd(D, QP, W)) void decode_ke
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int i = lane & 15, g = lane >> 4;
     const int here = min(kHeadTile, a.group - tile * kHeadTile);      // query heads of this workgroup
+    const int column = COPIES == 2 ? i & 7 : i;                       // this lane's among them
     const int h0 = head * a.group + tile * kHeadTile;                 // first query head
     const int begin = split * a.chunk;
     int t = begin + wave * kTileTokens;
@@ -424,7 +471,7 @@ __global__ __launch_bounds__(W * kWave, waves_per_simd(D, QP, W)) void decode_ke
     raw_pages(t, page);
     u32x4 raw_q[S::kSteps][QP];
     {
-        const int64_t q0 = b * a.q_stride + static_cast<int64_t>(h0 + (i < here ? i : 0)) * D;
+        const int64_t q0 = b * a.q_stride + static_cast<int64_t>(h0 + (column < here ? column : 0)) * D;
 #pragma unroll
         for (int s = 0; s < S::kSteps; ++s) {
             constexpr int kPer = S::kPerPiece / 8;                    // steps of a piece
@@ -441,7 +488,7 @@ __global__ __launch_bounds__(W * kWave, waves_per_simd(D, QP, W)) void decode_ke
         for (int h = 0; h < 2; ++h)
             page[h] = t0 + 16 * h < end ? page_or_absent(page[h], a.d.n_pages) : -1;
     };
-    Tile<D, BITS> T;
+    Tile<D, BITS, COPIES> T;
     int64_t row[2];
     const int len = min(max(a.seq_lens[b], 0), a.longest);
     const int parts = max(1, (len + a.chunk - 1) / a.chunk);
@@ -466,7 +513,7 @@ __global__ __launch_bounds__(W * kWave, waves_per_simd(D, QP, W)) void decode_ke
                            : __uint_as_float(e % 2 ? raw_q[s][0][e / 2] & 0xFFFF0000u : raw_q[s][0][e / 2] << 16);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float x = i < here ? w[q_order<BITS>(e)] : 0.f;
+            const float x = column < here ? w[q_order<BITS>(e)] : 0.f;
             const __bf16 part = static_cast<__bf16>(x);
             qf[0][s][e] = part;
             q_sum += x;
@@ -488,8 +535,8 @@ __global__ __launch_bounds__(W * kWave, waves_per_simd(D, QP, W)) void decode_ke
             const bool more = t + kUnit < end;
             int next[2];
             raw_pages(t + kUnit, next);
-            float sc[8];
-            tile_scores<D, BITS, QP>(sc, T, qf, q_sum, a.scale_log2);
+            float sc[8 / COPIES];
+            tile_scores<D, BITS, QP, COPIES>(sc, T, qf, q_sum, a.scale_log2, lane);
             __builtin_amdgcn_sched_barrier(0);
             check_pages(t + kUnit, end, next);
             if (more) {
@@ -497,7 +544,7 @@ __global__ __launch_bounds__(W * kWave, waves_per_simd(D, QP, W)) void decode_ke
                 load_keys(T, a, row, lane);
             }
             __builtin_amdgcn_sched_barrier(0);
-            use_values<D, BITS>(st, T, sc, t, end, page, lane);
+            use_values<D, BITS, COPIES>(st, T, sc, t, end, page, lane);
             if (!more) break;
             load_values(T, a, row, lane);
             t += kUnit;
@@ -506,7 +553,21 @@ __global__ __launch_bounds__(W * kWave, waves_per_simd(D, QP, W)) void decode_ke
         }
     }
 
-    // Join the waves.
+    // Join a head's columns, then the waves.
+    if constexpr (COPIES == 2) {
+        const float m = fmaxf(st.m, other_copy(st.m)), f = __builtin_amdgcn_exp2f(st.m - (m == -INFINITY ? 0.f : m));
+        const auto both = [&](float x) {
+            x *= f;
+            return x + other_copy(x);
+        };
+        st.m = m;
+        st.l = both(st.l);
+        st.konst = both(st.konst);
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) st.o[x][r] = both(st.o[x][r]);
+    }
     st.l = over_groups_sum(st.l);
     st.konst = over_groups_sum(st.konst);
     float* stats = lds + kDecWaves * here * kStride;
@@ -637,7 +698,8 @@ __global__ __launch_bounds__(W * kWave, waves_per_simd(D, QP, W)) void decode_ke
 // call, 8 bits, 8 key-value heads of 128, groups of 4:
 //   one sequence, four waves and eight: 500 tokens 8.3, 10.2; 2000 10.0, 10.6; 4000
 //   12.8, 11.8; 32768 24, 22; eight waves and twelve: 8192 15.2, 14.3; 131071 at 4
-//   bits, groups of 8, 46.6, 43.5;
+//   bits, groups of 8, 46.6, 43.5; twelve and sixteen there, with two columns a head:
+//   42.2, 40.5;
 //   32 sequences of 17 .. 8192 tokens, four waves: one workgroup to a CU 79, twelve
 //   66 (eight waves, one to a CU 73); 32 of 2048 each: 34, 37.
 constexpr int kCus = 256, kFewItems = 48, kOneRound = 128;
@@ -659,7 +721,7 @@ DecodePlan plan_decode(const grinqh_kv_layout& L, int n_q_heads, int batch, int 
     // sequences of different lengths fill the card evenly.
     const bool few = p.items <= kFewItems;
     const auto units_of = [&](int waves) { return (static_cast<int64_t>(max_len) + waves * kTileTokens - 1) / (waves * kTileTokens); };
-    p.waves = few && p.items * units_of(4) > kOneRound ? big_waves(L.head_dim) : 4;
+    p.waves = few && p.items * units_of(4) > kOneRound ? big_waves(L.head_dim, copies_of(L.bits, group)) : 4;
     const int64_t units = units_of(p.waves);
     const auto at_most = [&](int64_t groups) {          // units of a part, for that many workgroups in all
         const int64_t parts = std::max<int64_t>(1, groups / std::max<int64_t>(p.items, 1));
@@ -678,24 +740,32 @@ DecodePlan plan_decode(const grinqh_kv_layout& L, int n_q_heads, int batch, int 
     return p;
 }
 
-template <int D, int BITS>
+template <int D, int BITS, int COPIES>
 grinqh_status launch_queries(const DecodeArgs& a, int waves, unsigned n, hipStream_t stream) {
     const int here = a.group < kHeadTile ? a.group : kHeadTile;
-    const size_t lds = static_cast<size_t>(waves) * std::max<size_t>(here * (D + 4 + 2) * sizeof(float), kWave * sizeof(f32x4));
+    const auto launch = [&](auto kernel, int w) {
+        const size_t lds = static_cast<size_t>(w) * std::max<size_t>(here * (D + 4 + 2) * sizeof(float), kWave * sizeof(f32x4));
+        return launch_kernel(kernel, dim3(n), w * kWave, lds, stream, a);
+    };
     if (waves > 4) {
-        constexpr int W = big_waves(D);
-        const auto kernel = a.q_dtype == GRINQH_BF16 ? decode_kernel<D, BITS, 1, W> : decode_kernel<D, BITS, 2, W>;
-        return launch_kernel(kernel, dim3(n), W * kWave, lds, stream, a);
+        constexpr int W1 = big_waves(D, COPIES, 1), W2 = big_waves(D, COPIES, 2);
+        return a.q_dtype == GRINQH_BF16 ? launch(decode_kernel<D, BITS, 1, W1, COPIES>, W1) : launch(decode_kernel<D, BITS, 2, W2, COPIES>, W2);
     }
-    const auto kernel = a.q_dtype == GRINQH_BF16 ? decode_kernel<D, BITS, 1, 4> : decode_kernel<D, BITS, 2, 4>;
-    return launch_kernel(kernel, dim3(n), 4 * kWave, lds, stream, a);
+    return a.q_dtype == GRINQH_BF16 ? launch(decode_kernel<D, BITS, 1, 4, COPIES>, 4) : launch(decode_kernel<D, BITS, 2, 4, COPIES>, 4);
+}
+
+template <int D, int BITS>
+grinqh_status launch_copies(const DecodeArgs& a, int waves, unsigned n, hipStream_t stream) {
+    if constexpr (BITS == 4)
+        if (copies_of(BITS, a.group) == 2) return launch_queries<D, BITS, 2>(a, waves, n, stream);
+    return launch_queries<D, BITS, 1>(a, waves, n, stream);
 }
 
 template <int D>
 grinqh_status launch_bits(const DecodeArgs& a, int bits, int waves, unsigned n, hipStream_t stream) {
-    if (bits == 4) return launch_queries<D, 4>(a, waves, n, stream);
-    if (bits == 8) return launch_queries<D, 8>(a, waves, n, stream);
-    return launch_queries<D, 16>(a, waves, n, stream);
+    if (bits == 4) return launch_copies<D, 4>(a, waves, n, stream);
+    if (bits == 8) return launch_copies<D, 8>(a, waves, n, stream);
+    return launch_copies<D, 16>(a, waves, n, stream);
 }
 
 bool valid_heads(const grinqh_kv_layout* L, int n_q_heads, int batch, int max_len) {

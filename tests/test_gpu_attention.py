@@ -82,6 +82,19 @@ def test_decode_over_a_long_cache(dev, bits, heads, group, dim, page, n):
     assert torch.equal(first, _decode(c, q, "bf16", "f32", dev)), "the same call twice, the same bits"
 
 
+@pytest.mark.parametrize("q_dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dim,group,page,n", [(64, 1, 16, 7003), (64, 8, 32, 5000), (128, 4, 64, 9001), (128, 8, 16, 6145),
+                                              (128, 7, 256, 513), (256, 3, 64, 4100)])
+def test_decode_of_four_bits_and_small_groups(dev, dim, group, page, n, q_dtype):
+    """A head's tokens are weighed in two columns; ends in either half of a tile."""
+    rng = np.random.default_rng(n)
+    c = Cache(rng, [n], 1, dim, 4, page, dev)
+    q = _queries(rng, 1, group, dim, q_dtype)
+    for length in (n, n - 16, 17, 16, 1):
+        c.dev_lens.fill_(length)
+        _decode(c, q, q_dtype, "f32", dev, max_len=n, lens=[length], what=str(length))
+
+
 def test_decode_of_many_sequences_of_very_different_lengths(dev):
     rng = np.random.default_rng(8)
     lens = [int(x) for x in rng.integers(0, 700, 40)] + [3001, 0, 1]
