@@ -15,7 +15,11 @@
 // Scores.  S^T = K Q^T (32 keys x 32 rows, v_mfma_f32_32x32x16_bf16): a lane
 // holds 16 of a row's 32 scores, the lane 32 further the others, so maximum and
 // sum need one exchange between the two.  The exponent is one fused
-// multiply-add, exp2(s c - max c) with c = scale log2 e.
+// multiply-add, exp2(s c - max c) with c = scale log2 e; the rounding of max c
+// multiplies all of a row's weights alike.  Past kFar it would not be small
+// any more (past 2^30 it alone makes weights 0 or infinite): the tiles of such
+// rows are used outside the inner loop, with (s - max) c.  At 8192 tokens, 32
+// heads of 128, the test for them takes 533 us from 530; with every row so, 2830.
 //
 // Values.  O^T = V^T P^T.  The scores a lane holds are its share of the
 // contraction as they are (the contraction's order is free), rounded to bf16
@@ -59,6 +63,10 @@ constexpr int kPreThreads = kPreWaves * kWave;
 constexpr int64_t kMaxPreGroups = 1 << 23;              // workgroups of a launch
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 constexpr float kSlack = 30.f;                          // log2 by which scores may exceed the maximum in use
+// Largest |max c| that is rounded: half a step there, 2^-9, changes weights by
+// 2^-9 ln 2, so that sums of different maxima (before and after a rescaling, of
+// two parts) fit together to less than the weights' own rounding to bf16, 2^-8.
+constexpr float kFar = 65536.f;
 
 template <int D>
 struct PreShape {
@@ -136,8 +144,12 @@ __device__ __forceinline__ void store_four(const Args& a, int64_t at, float y0, 
         *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + at) = u32x2{pack_bf16(y0, y1), pack_bf16(y2, y3)};
 }
 
-__device__ __forceinline__ float lse_of(float top, float sum, float c) {
-    return sum == 0.f ? -INFINITY : kLn2 * (top * c + __builtin_amdgcn_logf(sum));
+// Of weights 2^(s c - round(max c)), so with the same product; past kFar of
+// 2^((s - max) c), and the score itself may be close to the largest float.
+__device__ __forceinline__ float lse_of(float top, float sum, float c, float scale) {
+    if (sum == 0.f) return -INFINITY;
+    const float log_sum = __builtin_amdgcn_logf(sum);
+    return fabsf(top * c) > kFar ? __builtin_fmaf(top, fabsf(scale), kLn2 * log_sum) : kLn2 * (top * c + log_sum);
 }
 
 // Where the workspace holds a part: its rows' sums, then their (maximum, weight).
@@ -355,7 +367,8 @@ __global__ __launch_bounds__(kPreThreads, D == 256 ? 1 : D == 64 ? 3 : 2) void p
     // The inner loop never touches the output sums but to add to them.  A row whose
     // scores pass its maximum by too much leaves it and comes back to the same
     // tile with the new maximum; a tile with values that are not finite where some
-    // row does not see them is used outside.
+    // row does not see them, or with a row whose maximum is far from zero, is used
+    // outside.
     float mx = 0.f;
     bool again = false;
     for (int t = first;;) {
@@ -404,6 +417,7 @@ __global__ __launch_bounds__(kPreThreads, D == 256 ? 1 : D == 64 ? 3 : 2) void p
         const float mc1 = top == -INFINITY ? 0.f : top * c;
         mx = fmaxf(mx, mx1);
         passed = __any((mx - top) * c > kSlack);        // (no if both are infinite: NaN)
+        odd = __any(fabsf(mc1) > kFar);
         if (masked) {                                   // a value that is not finite where some row does not see it
             uint32_t high = 0;
 #pragma unroll
@@ -415,7 +429,7 @@ __global__ __launch_bounds__(kPreThreads, D == 256 ? 1 : D == 64 ? 3 : 2) void p
                     for (int x = 0; x < 4; ++x) high |= ((w[x] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
                     __builtin_amdgcn_sched_barrier(0);
                 }
-            odd = __any(high != 0);
+            odd |= __any(high != 0);
         }
         if (passed || odd) break;
 #pragma unroll
@@ -464,7 +478,16 @@ __global__ __launch_bounds__(kPreThreads, D == 256 ? 1 : D == 64 ? 3 : 2) void p
           }
           mask(s0, t0);
           mask(s1, t0 + 32);
-          const float mc = top == -INFINITY ? 0.f : top * c;
+          float mc = top == -INFINITY ? 0.f : top * c, shift = 0.f;
+          if (fabsf(mc) > kFar) {
+              shift = top;
+              mc = 0.f;
+          }
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+              s0[r] -= shift;
+              s1[r] -= shift;
+          }
 #pragma unroll
           for (int e = 0; e < 8; ++e) weigh(s0, e, mc, p0, sum);
           // The product would carry 0 * Inf into rows that do not see the
@@ -547,7 +570,7 @@ __global__ __launch_bounds__(kPreThreads, D == 256 ? 1 : D == 64 ? 3 : 2) void p
             *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.out) + out_row * D + 32 * d + 8 * x + 8 * (lane >> 5)) = w;
         }
     }
-    if (a.lse != nullptr && lane < 32) a.lse[out_row] = lse_of(top, sum, c);
+    if (a.lse != nullptr && lane < 32) a.lse[out_row] = lse_of(top, sum, c, a.scale);
 }
 
 // Joins the parts of every tile that has several.  A workgroup takes
@@ -613,7 +636,7 @@ __global__ __launch_bounds__(kPreThreads) void join_kernel(Args a, float c, int 
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const int64_t row = static_cast<int64_t>(q_begin + i) * a.n_q_heads + h;
         store_four(a, row * D + x, y.x * inv, y.y * inv, y.z * inv, y.w * inv);
-        if (a.lse != nullptr && x == 0) a.lse[row] = lse_of(top, l, c);
+        if (a.lse != nullptr && x == 0) a.lse[row] = lse_of(top, l, c, a.scale);
     }
 }
 

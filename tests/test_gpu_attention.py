@@ -359,6 +359,82 @@ def test_prefill_scales_and_extreme_scores(dev):
     _prefill(A.bf16(q * 100), k, v, cu_q, cu_k, dev, True, "f32")
 
 
+def _exact_prefill(q, k, v, cu_q, cu_k, scale, dev, want, split):
+    """Runs a causal call whose scores q . k are exact in fp32, against want(scores [m] of one row, values [m][dim]) ->
+    (output, lse).  Bounds, with u = 2^-24: an exponent (s - top) c is off by 4 u of itself (log2 e, its product with
+    the scale, the product, exp2), and counts down to -128 only, so a weight is off by 2^-22 2^7 = 2^-15, as is the
+    sum, and by 2^-8 where it is rounded to bf16; the sums by m u; lse = ln 2 (top c + log2 sum) by the roundings of
+    log2 e, c, top c, the sum, ln 2 and the product, 8 u of its size, and by what the weights' sum is off by."""
+    import input_adaptive_bit_amd as G
+    import torch
+    t = [to_bf16(x, dev) for x in (q, k, v)] + [torch.from_numpy(x).to(dev) for x in (cu_q, cu_k)]
+    out, lse = G.prefill_attention(*t, scale=scale, out_dtype=torch.float32, return_lse=True)
+    assert (G.grinqh_prefill_attention_workspace_bytes(*t, out) > 0) == split
+    o, l, mass = np.zeros(q.shape), np.zeros(q.shape[:2]), np.zeros(q.shape)
+    group = q.shape[1] // k.shape[1]
+    for b in range(len(cu_q) - 1):
+        n, m = cu_q[b + 1] - cu_q[b], cu_k[b + 1] - cu_k[b]
+        for i in range(n):
+            for h in range(q.shape[1]):
+                keys = slice(cu_k[b], cu_k[b] + max(0, i + m - n + 1))
+                s = k[keys, h // group].astype(np.float64) @ q[cu_q[b] + i, h].astype(np.float64)
+                o[cu_q[b] + i, h], l[cu_q[b] + i, h] = want(s, v[keys, h // group].astype(np.float64))
+                mass[cu_q[b] + i, h], _ = want(s, np.abs(v[keys, h // group]).astype(np.float64))
+    u = 2.0 ** -24
+    rel = 2.0 ** -8 + 2 * 2.0 ** -15 + (len(k) + 32) * u
+    with np.errstate(over="ignore"):
+        inside(_np(out), o, rel * mass + u * np.abs(o), f"out, scale {scale}")
+        l32 = np.where(np.isfinite(l.astype(np.float32)), l, l.astype(np.float32))
+        inside(_np(lse), l32, np.where(np.isfinite(l32), 8 * u * np.abs(l) + rel, 0.0), f"lse, scale {scale}")
+
+
+@pytest.mark.parametrize("lens_q,lens_k,split", [([90], [90], False), ([3, 2], [2100, 1500], True)])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_prefill_scores_far_from_zero_leave_the_largest_its_weight(dev, dim, lens_q, lens_k, split):
+    """Scores of whole numbers times a scale so large that every key but the best of a row (or, where several share the
+    largest score, those) weighs nothing."""
+    rng = np.random.default_rng(dim)
+    cu_q, cu_k = (np.concatenate([[0], np.cumsum(x)]).astype(np.int32) for x in (lens_q, lens_k))
+    q = rng.integers(-2, 3, (cu_q[-1], 4, dim)).astype(np.float32)
+    k = rng.integers(-2, 3, (cu_k[-1], 2, dim)).astype(np.float32)
+    v = rows(rng, cu_k[-1], 2, dim)
+    for size, scale in ((1, 1e8), (1, 1e9), (1, 1e12), (1, 1e30), (4096, 1e30), (1, -1e8), (1, -1e12), (4096, -1e30)):
+        say(f"prefill dim={dim} scale={scale} size={size} split={split}")
+
+        def best(s, values):
+            s = s * np.float64(np.float32(scale))
+            at = s == s.max()
+            return values[at].mean(0), s.max() + np.log(at.sum())
+
+        _exact_prefill(q * size, k * size, v, cu_q, cu_k, scale, dev, best, split)
+
+
+@pytest.mark.parametrize("lens_q,lens_k,split", [([90], [90], False), ([3, 2], [2100, 1500], True)])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_prefill_scores_with_a_large_common_part(dev, dim, lens_q, lens_k, split):
+    """Whole numbers 2^20 and 2^23 + 0 .. 60 times 1/2: a softmax of the small rest, rows whose maximum grows on the way
+    and parts with maxima of their own.  Then equal scores of 3e4 . 3e4 at the usual scale: the mean."""
+    rng = np.random.default_rng(dim + 1)
+    cu_q, cu_k = (np.concatenate([[0], np.cumsum(x)]).astype(np.int32) for x in (lens_q, lens_k))
+    v = rows(rng, cu_k[-1], 1, dim)
+
+    def softmax(scale):
+        def want(s, values):
+            a = s * scale
+            e = np.exp(a - a.max())
+            return e @ values / e.sum(), a.max() + np.log(e.sum())
+        return want
+
+    for power in (10, 11):
+        q, k = np.zeros((cu_q[-1], 2, dim), np.float32), np.zeros((cu_k[-1], 1, dim), np.float32)
+        q[..., 0], k[..., 0] = 2.0 ** power, 2.0 ** (10 if power == 10 else 12)
+        q[..., 1], k[..., 1] = 1.0, rng.integers(0, 9, k.shape[:2])
+        k[-40:, 0, 1] += rng.integers(0, 53, 40)
+        _exact_prefill(q, k, v, cu_q, cu_k, 0.5, dev, softmax(0.5), split)
+    q, k = (A.bf16(np.full((n, h, dim), 3e4, np.float32)) for n, h in ((cu_q[-1], 2), (cu_k[-1], 1)))
+    _exact_prefill(q, k, v, cu_q, cu_k, dim ** -0.5, dev, softmax(np.float64(np.float32(dim ** -0.5))), split)
+
+
 @pytest.mark.parametrize("dim", [64, 128, 256])
 def test_keys_that_are_not_seen_may_be_anything(dev, dim):
     """NaN and infinities in later keys, other sequences and rows behind the
