@@ -390,8 +390,11 @@ int64_t grinqh_debug_page_row(const grinqh_kv_layout* L, int32_t page, int32_t h
  *               aligned.
  *   lse         fp32 [batch][n_q_heads] or NULL.
  *   workspace   >= grinqh_attention_workspace_bytes(...) bytes, 256-byte
- *               aligned, zero-filled before its first use by this call; every
- *               call leaves it ready for the next, of any layout and sizes.
+ *               aligned, its first 16384 bytes zero-filled before its first use by
+ *               this call; every call leaves it ready for the next, of any layout
+ *               and sizes that it is large enough for.  The size never falls as
+ *               batch or max_len grow: a workspace for a program's largest call
+ *               serves all of its calls with that layout and n_q_heads.
  *               Calls that share it must not overlap in time, and
  *               grinqh_gemv must have its own.
  * The result of a call does not depend on timing: the parts of a long

@@ -26,6 +26,8 @@ if torch is not None:
     _CODES = {torch.bfloat16: GRINQH_BF16, torch.float32: GRINQH_F32}
     _BF16, _I32, _I64 = torch.bfloat16, torch.int32, torch.int64
 
+_COUNTER_BYTES = 16384                           # of a decode attention's workspace, zero before its first use
+
 
 # ------------------------------------------------------------------ host ----
 
@@ -157,14 +159,18 @@ def _empty_as(t, dtype, device, stream):
     return _empty(t.shape, dtype, device, stream)
 
 
-def _zeros(n, device, stream):
-    """A zero-filled byte tensor, filled on the call's stream."""
+def _workspace(n, device, stream):
+    """A decode attention's workspace, ready for its first call, on the call's stream."""
     if stream is None:
-        return torch.zeros(n, dtype=torch.uint8, device=device)
+        if n <= 1 << 20:
+            return torch.zeros(n, dtype=torch.uint8, device=device)
+        w = torch.empty(n, dtype=torch.uint8, device=device)
+        w[:_COUNTER_BYTES].zero_()               # sooner than to fill all of a large one
+        return w
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     with torch.cuda.stream(stream):
-        return torch.zeros(n, dtype=torch.uint8, device=device)
+        return _workspace(n, device, None)
 
 
 # ------------------------------------------------------------------ cache ---
@@ -204,7 +210,8 @@ def new_kv_cache(n_kv_heads: int, head_dim: int, page_size: int, n_pages: int, b
 
 
 def new_attention_workspace(L: KVLayout, n_q_heads: int, batch: int, max_len: int, device=None):
-    """A zero-filled workspace tensor for grinqh_decode_attention on `device`."""
+    """A zero-filled workspace tensor for grinqh_decode_attention on `device`: for
+    calls of up to this batch and max_len."""
     n = grinqh_attention_workspace_bytes(L, n_q_heads, batch, max_len)
     if n == 0:
         raise GrinqhError(GRINQH_EINVAL, "grinqh_attention_workspace_bytes")
@@ -331,7 +338,7 @@ def decode_attention(cache: KVCache, q, page_table, seq_lens, max_len=None, scal
     out = _empty_as(q, out_dtype or torch.bfloat16, device, stream)
     lse = _empty((batch, heads), torch.float32, device, stream) if return_lse else None
     if workspace is None:
-        workspace = _zeros(grinqh_attention_workspace_bytes(cache.layout, heads, batch, max_len), device, stream)
+        workspace = _workspace(grinqh_attention_workspace_bytes(cache.layout, heads, batch, max_len), device, stream)
     grinqh_decode_attention(cache, q, page_table, seq_lens, max_len, out, workspace, scale, lse, stream)
     return (out, lse) if return_lse else out
 

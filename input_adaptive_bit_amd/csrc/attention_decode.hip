@@ -710,6 +710,11 @@ struct DecodePlan {
     size_t ws_bytes;
 };
 
+size_t workspace_of(const grinqh_kv_layout& L, int group, int64_t parts) {
+    const size_t part = static_cast<size_t>(std::min(group, kHeadTile)) * (L.head_dim + 2) * sizeof(float);
+    return (kCounters * sizeof(unsigned) + parts * part + 255) / 256 * 256;
+}
+
 DecodePlan plan_decode(const grinqh_kv_layout& L, int n_q_heads, int batch, int max_len) {
     DecodePlan p;
     const int group = n_q_heads / L.n_kv_heads;
@@ -734,10 +739,25 @@ DecodePlan plan_decode(const grinqh_kv_layout& L, int n_q_heads, int batch, int 
     if (p.items > kCounters) per = units;
     p.chunk = static_cast<int>(per * p.waves * kTileTokens);
     p.splits = static_cast<int>((units + per - 1) / per);
-    const size_t part = static_cast<size_t>(std::min(group, kHeadTile)) * (L.head_dim + 2) * sizeof(float);
-    p.ws_bytes = kCounters * sizeof(unsigned) + (p.splits > 1 ? p.items * p.splits * part : 0);
-    p.ws_bytes = (p.ws_bytes + 255) / 256 * 256;
+    p.ws_bytes = workspace_of(L, group, p.splits > 1 ? p.items * p.splits : 0);
     return p;
+}
+
+// The workspace of a program's largest call, enough for every smaller one: the
+// parts that plan_decode makes, at most, for up to these items and tokens.  (Its
+// own count falls where a longer cache or a larger batch gives rounder parts.)
+// at_most(g) leaves no more than g workgroups in all, a part has a unit or more,
+// and four of them where there are many items and no part was made smaller for
+// want of 3 * kCus workgroups.
+size_t most_workspace(const grinqh_kv_layout& L, int n_q_heads, int batch, int max_len) {
+    const DecodePlan p = plan_decode(L, n_q_heads, batch, max_len);
+    const int64_t units = (static_cast<int64_t>(max_len) + 4 * kTileTokens - 1) / (4 * kTileTokens);
+    int64_t parts = 0;                                   // one unit is one part, which stores nothing
+    if (units > 1)
+        parts = p.items <= kFewItems ? std::min<int64_t>(kCus, p.items * units)
+                                     : std::max(std::min<int64_t>(12 * kCus, p.items * ((units + 3) / 4)),
+                                                std::min<int64_t>(3 * kCus, p.items * units));
+    return workspace_of(L, n_q_heads / L.n_kv_heads, parts);
 }
 
 template <int D, int BITS, int COPIES>
@@ -782,7 +802,7 @@ extern "C" {
 
 size_t grinqh_attention_workspace_bytes(const grinqh_kv_layout* L, int32_t n_q_heads, int32_t batch,
                                         int32_t max_len) {
-    return valid_heads(L, n_q_heads, batch, max_len) ? plan_decode(*L, n_q_heads, batch, max_len).ws_bytes : 0;
+    return valid_heads(L, n_q_heads, batch, max_len) ? most_workspace(*L, n_q_heads, batch, max_len) : 0;
 }
 
 grinqh_status grinqh_decode_attention(const grinqh_kv_layout* L, const grinqh_kv_pools* pools, const void* q,

@@ -201,6 +201,32 @@ def test_decode_attention_checks_its_arguments_before_any_device_call():
     assert G.grinqh_attention_workspace_bytes(L, 8, 3, 64) % 256 == 0
 
 
+@pytest.mark.parametrize("heads,dim,bits,n_q", [(8, 128, 8, 32), (8, 128, 4, 64), (1, 256, 16, 16), (2, 64, 4, 6), (4, 128, 8, 96),
+                                                (12, 64, 16, 12), (48, 64, 8, 48)])
+def test_decode_workspace_of_a_programs_largest_call_serves_its_smaller_ones(heads, dim, bits, n_q):
+    """The size never falls as batch or length grow, and a call takes a workspace of the size asked for any larger one.
+    (q and out overlap, which is refused after the workspace was found large enough: nothing is launched.)"""
+    lib = G.load()
+    L = G.grinqh_kv_layout_init(heads, dim, 64, 8, bits)
+    P = _pools(1 << 20)
+    batches = [*range(1, 66), 96, 127, 128, 129, 192, 193, 256, 384, 385, 511, 512, 513, 1000, 4097, 1 << 20]
+    lengths = [1, 128, 129, 256, 257, 384, 385, 500, 511, 512, 513, 768, 1000, 1024, 1025, 2000, 2049, 3001, 4096, 5000, 8192,
+               9001, 12288, 16384, 16385, 24065, 32768, 40000, 65536, 100001, 131071, 131072, 1 << 20, 1 << 28]
+    need = np.array([[G.grinqh_attention_workspace_bytes(L, n_q, b, n) for n in lengths] for b in batches], np.int64)
+    assert np.all(need % 256 == 0) and np.all(np.diff(need, axis=0) >= 0) and np.all(np.diff(need, axis=1) >= 0)
+
+    def status(b, n, size):
+        q = 1 << 16
+        return lib.grinqh_decode_attention(ctypes.byref(L), ctypes.byref(P), q, 0, n_q * dim, n_q, 1 << 43, 1 << 24, 1 << 24,
+                                           1 << 44, b, n, 0.1, q, 0, None, 1 << 42, size, None)
+
+    for i, b in enumerate(batches):
+        for j, n in enumerate(lengths):
+            if b * heads * -(-n_q // heads // 16) <= 1 << 23:
+                assert status(b, n, int(need[i, j])) == B.GRINQH_EINVAL, (b, n)
+    assert status(1, 32768, 0) == B.GRINQH_ENOSPACE
+
+
 def test_prefill_attention_checks_its_arguments_before_any_device_call():
     lib = G.load()
     Q, K, V, CQ, CK, OUT, LSE = (K64 * 16 * k for k in range(1, 8))

@@ -208,6 +208,31 @@ def test_one_workspace_for_calls_of_different_sizes_and_in_two_graphs(dev):
             inside(_np(out), o, bound, f"turn {turn}")
 
 
+def test_the_workspace_of_the_largest_call_serves_smaller_ones(dev):
+    """A batch that shrinks, with the longest of its lengths as the bound; then calls that make their own workspace."""
+    import input_adaptive_bit_amd as G
+    import torch
+    rng = np.random.default_rng(21)
+    lens = [int(x) for x in rng.integers(1, 1600, 32)]
+    c = Cache(rng, lens, 8, 64, 8, 64, dev)
+    q = _queries(rng, 32, 16, 64, "bf16")
+    q_dev = to_bf16(q, dev)
+    o, bound, _, _ = decode_reference(c, q, 0.125, "f32")
+    ws = G.new_attention_workspace(c.dev.layout, 16, 32, 8192, dev)
+    assert ws.nbytes > 1 << 20
+    for b in range(32, 0, -1):
+        for max_len in (max(lens[:b]), 8192 - 13 * b):
+            for w in (ws, None):
+                out = G.decode_attention(c.dev, q_dev[:b], c.dev_table[:b], c.dev_lens[:b], max_len, out_dtype=torch.float32,
+                                         workspace=w)
+                inside(_np(out), o[:b], bound[:b], f"batch {b}, max_len {max_len}")
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    out = G.decode_attention(c.dev, q_dev, c.dev_table, c.dev_lens, 8192, out_dtype=torch.float32, stream=other)
+    other.synchronize()
+    inside(_np(out), o, bound, "another stream")
+
+
 def test_decode_on_another_stream(dev):
     import input_adaptive_bit_amd as G
     import torch
