@@ -333,7 +333,8 @@ size_t grinqh_kv_grid_bytes(const grinqh_kv_layout* L);
  *              n_pages * page_size is not written (padding).  The slots
  *              written by one call must differ: a slot named twice is left
  *              holding a mixture of the rows.
- * k and v must not overlap the pools. */
+ * k and v must not overlap the pools, nor the pools one another (EINVAL; a
+ * cache whose keys and values share a pool can only be read). */
 grinqh_status grinqh_kv_write(const grinqh_kv_layout* L, const grinqh_kv_pools* pools, const void* k,
                               const void* v, grinqh_dtype dtype, int64_t k_stride, int64_t v_stride,
                               int32_t n_tokens, const int64_t* slots, void* stream);

@@ -296,6 +296,13 @@ grinqh_status grinqh_kv_write(const grinqh_kv_layout* L, const grinqh_kv_pools* 
         reinterpret_cast<uintptr_t>(slots) % 8 != 0)
         return GRINQH_EALIGN;
     const size_t code_bytes = grinqh_kv_code_bytes(L), grid_bytes = grinqh_kv_grid_bytes(L);
+    // Keys and values are written at the same time.
+    if (overlaps(pools->k_codes, code_bytes, pools->v_codes, code_bytes) ||
+        overlaps(pools->k_grid, grid_bytes, pools->v_grid, grid_bytes))
+        return GRINQH_EINVAL;
+    for (const void* codes : {pools->k_codes, pools->v_codes})
+        if (overlaps(codes, code_bytes, pools->k_grid, grid_bytes) || overlaps(codes, code_bytes, pools->v_grid, grid_bytes))
+            return GRINQH_EINVAL;
     const void* src[2] = {k, v};
     const int64_t stride[2] = {k_stride, v_stride};
     for (int i = 0; i < 2; ++i) {

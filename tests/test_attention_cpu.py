@@ -173,6 +173,23 @@ def test_cache_calls_check_their_arguments_before_any_device_call():
     assert read(v=K + 512) == B.GRINQH_EINVAL                                     # outputs overlap
 
 
+@pytest.mark.parametrize("bits", [4, 8, 16])
+def test_rows_are_not_written_to_pools_that_share_memory(bits):
+    """Keys and values are written at the same time: one buffer for both, or pools that overlap, would mix them."""
+    lib = G.load()
+    L = G.grinqh_kv_layout_init(2, 64, 16, 8, bits)
+    apart, codes, grid = _pools(), G.grinqh_kv_code_bytes(L), G.grinqh_kv_grid_bytes(L)
+    sizes = dict(k_codes=codes, v_codes=codes, k_grid=grid, v_grid=grid)
+    for one in sizes:
+        for other in sizes:
+            for at in (0, -sizes[one] + 16, sizes[other] - 16):
+                if one != other and sizes[one] and sizes[other]:
+                    P = B.KVPools(apart.k_codes, apart.v_codes, apart.k_grid, apart.v_grid)
+                    setattr(P, one, getattr(P, other) + at)
+                    assert lib.grinqh_kv_write(ctypes.byref(L), ctypes.byref(P), K64, 2 * K64, 0, 128, 128, 4, 3 * K64,
+                                               None) == B.GRINQH_EINVAL, (one, other, at)
+
+
 def test_decode_attention_checks_its_arguments_before_any_device_call():
     lib = G.load()
     L = G.grinqh_kv_layout_init(2, 64, 16, 8, 8)
