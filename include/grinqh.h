@@ -399,7 +399,8 @@ int64_t grinqh_debug_page_row(const grinqh_kv_layout* L, int32_t page, int32_t h
  *               Calls that share it must not overlap in time, and
  *               grinqh_gemv must have its own.
  * The result of a call does not depend on timing: the parts of a long
- * cache are joined in their order.  q and out must not overlap. */
+ * cache are joined in their order.  out, lse and the workspace (as much of it
+ * as the call uses) must not overlap one another nor anything that is read. */
 size_t grinqh_attention_workspace_bytes(const grinqh_kv_layout* L, int32_t n_q_heads, int32_t batch,
                                         int32_t max_len);
 grinqh_status grinqh_decode_attention(const grinqh_kv_layout* L, const grinqh_kv_pools* pools, const void* q,

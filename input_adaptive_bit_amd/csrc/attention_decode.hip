@@ -830,8 +830,15 @@ grinqh_status grinqh_decode_attention(const grinqh_kv_layout* L, const grinqh_kv
     const DecodePlan plan = plan_decode(*L, n_q_heads, batch, max_len);
     if (workspace_bytes < plan.ws_bytes) return GRINQH_ENOSPACE;
     if (plan.items * plan.splits > kMaxDecodeGroups) return GRINQH_EINVAL;
-    if (overlaps(q, static_cast<size_t>(((batch - 1) * q_stride + width) * qb), out,
-                 static_cast<size_t>(batch * width * ob)))
+    const size_t code_bytes = grinqh_kv_code_bytes(L), grid_bytes = grinqh_kv_grid_bytes(L);
+    if (written_overlaps({{out, static_cast<size_t>(batch * width * ob)},
+                          {lse, lse == nullptr ? 0 : static_cast<size_t>(batch) * n_q_heads * sizeof(float)},
+                          {workspace, plan.ws_bytes}},
+                         {{q, static_cast<size_t>(((batch - 1) * q_stride + width) * qb)},
+                          {page_table, static_cast<size_t>((batch - 1) * table_stride + max_pages) * sizeof(int32_t)},
+                          {seq_lens, static_cast<size_t>(batch) * sizeof(int32_t)},
+                          {pools->k_codes, code_bytes}, {pools->v_codes, code_bytes},
+                          {pools->k_grid, grid_bytes}, {pools->v_grid, grid_bytes}}))
         return GRINQH_EINVAL;
     const int64_t reach = static_cast<int64_t>(max_pages) * L->page_size;
     DecodeArgs a;

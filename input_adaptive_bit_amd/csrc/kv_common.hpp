@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <initializer_list>
 #include <type_traits>
 
 #include "device_common.hpp"
@@ -70,6 +71,23 @@ inline bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintpt
 inline bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
     const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
     return na > 0 && nb > 0 && a0 < b0 + nb && b0 < a0 + na;
+}
+
+struct Span {
+    const void* at;
+    size_t bytes;
+};
+
+// Whether something that a call writes overlaps something that it reads or
+// writes besides.
+inline bool written_overlaps(std::initializer_list<Span> written, std::initializer_list<Span> read) {
+    for (const Span* w = written.begin(); w != written.end(); ++w) {
+        for (const Span& r : read)
+            if (overlaps(w->at, w->bytes, r.at, r.bytes)) return true;
+        for (const Span* x = w + 1; x != written.end(); ++x)
+            if (overlaps(w->at, w->bytes, x->at, x->bytes)) return true;
+    }
+    return false;
 }
 
 bool valid_kv_layout(const grinqh_kv_layout* L);

@@ -218,6 +218,32 @@ def test_decode_attention_checks_its_arguments_before_any_device_call():
     assert G.grinqh_attention_workspace_bytes(L, 8, 3, 64) % 256 == 0
 
 
+@pytest.mark.parametrize("bits", [4, 16])
+def test_decode_attention_refuses_to_write_where_it_reads(bits):
+    """out, lse and the workspace against q, the page table, the lengths, the pools and one another, at both ends."""
+    lib = G.load()
+    L = G.grinqh_kv_layout_init(2, 64, 16, 8, bits)
+    ws = G.grinqh_attention_workspace_bytes(L, 8, 3, 64)
+    sizes = dict(q=3 * 512 * 2, t=(2 * 6 + 4) * 4, n=12, out=3 * 512 * 4, lse=3 * 8 * 4, ws=ws, k=G.grinqh_kv_code_bytes(L),
+                 v=G.grinqh_kv_code_bytes(L), kg=G.grinqh_kv_grid_bytes(L), vg=G.grinqh_kv_grid_bytes(L))
+    good = {name: (i + 1) << 24 for i, name in enumerate(sizes)}
+
+    def status(**at):
+        a = dict(good, **at)
+        P = B.KVPools(a["k"], a["v"], a["kg"], a["vg"])
+        return lib.grinqh_decode_attention(ctypes.byref(L), ctypes.byref(P), a["q"], 0, 512, 8, a["t"], 6, 4, a["n"], 3, 64,
+                                           0.1, a["out"], 1, a["lse"], a["ws"], ws, None)
+
+    for written in ("out", "lse", "ws"):
+        for other in sizes:
+            if other == written or not sizes[other]:
+                continue
+            step = {"out": 16, "lse": 4, "ws": 256}[written]
+            below = (sizes[written] - 1) // step * step
+            for at in (0, -below, (sizes[other] - 1) // step * step):
+                assert status(**{written: good[other] + at}) == B.GRINQH_EINVAL, (written, other, at)
+
+
 @pytest.mark.parametrize("heads,dim,bits,n_q", [(8, 128, 8, 32), (8, 128, 4, 64), (1, 256, 16, 16), (2, 64, 4, 6), (4, 128, 8, 96),
                                                 (12, 64, 16, 12), (48, 64, 8, 48)])
 def test_decode_workspace_of_a_programs_largest_call_serves_its_smaller_ones(heads, dim, bits, n_q):
