@@ -433,6 +433,8 @@ grinqh_status grinqh_decode_attention(const grinqh_kv_layout* L, const grinqh_kv
  *              are worked on in parts and joined by a second kernel.  The size
  *              follows from the sizes in args and causal alone (0: it would not
  *              be used, or a size is invalid).
+ * out, lse and a workspace that is used must not overlap one another nor
+ * anything that is read.
  * total_q * n_q_heads / 128 + min(batch, total_q) * n_kv_heads is at most 2^23.
  * The weights p_t are rounded to bf16 for the product with the values. */
 typedef struct {

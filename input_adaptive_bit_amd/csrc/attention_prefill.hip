@@ -701,12 +701,24 @@ size_t prefill_workspace(const Args& a) {
     return plan_prefill<D>(a).ws_bytes;
 }
 
+bool writes_what_it_reads(const Args& a, size_t ws_bytes) {
+    const int64_t q_width = static_cast<int64_t>(a.n_q_heads) * a.head_dim, width = static_cast<int64_t>(a.n_kv_heads) * a.head_dim;
+    const auto rows = [](int64_t n, int64_t stride, int64_t of) { return n > 0 ? static_cast<size_t>((n - 1) * stride + of) * 2 : 0; };
+    const size_t ends = (static_cast<size_t>(a.batch) + 1) * sizeof(int32_t);
+    const size_t out = static_cast<size_t>(a.total_q) * q_width * (a.out_dtype == GRINQH_BF16 ? 2 : 4);
+    const size_t lse = a.lse == nullptr ? 0 : static_cast<size_t>(a.total_q) * a.n_q_heads * sizeof(float);
+    return written_overlaps({{a.out, out}, {a.lse, lse}, {a.workspace, ws_bytes}},
+                            {{a.q, rows(a.total_q, a.q_stride, q_width)}, {a.k, rows(a.total_k, a.k_stride, width)},
+                             {a.v, rows(a.total_k, a.v_stride, width)}, {a.cu_q, ends}, {a.cu_k, ends}});
+}
+
 template <int D>
 grinqh_status launch_prefill_attention(const Args& a, hipStream_t stream) {
     PrePlan p = plan_prefill<D>(a);
     if (p.tiles * a.n_kv_heads > kMaxPreGroups) return GRINQH_EINVAL;
-    if (a.workspace == nullptr) p.parts = 1;
-    else if (a.workspace_bytes < p.ws_bytes) return GRINQH_ENOSPACE;
+    if (a.workspace == nullptr) p = PrePlan{p.tiles, 1, 0};
+    if (a.workspace_bytes < p.ws_bytes) return GRINQH_ENOSPACE;
+    if (writes_what_it_reads(a, p.ws_bytes)) return GRINQH_EINVAL;
     const float c = a.scale == 0.f ? 1.f : fabsf(a.scale) * kLog2e;
     const unsigned n = static_cast<unsigned>(p.tiles * a.n_kv_heads);
     const grinqh_status st = launch_kernel(prefill_attention_kernel<D>, dim3(n * p.parts), kPreThreads, 0, stream, a, c, p.parts);
@@ -759,12 +771,6 @@ extern "C" grinqh_status grinqh_prefill_attention(const grinqh_prefill_attention
         a.k_stride % 8 != 0 || a.v_stride % 8 != 0 || !aligned_to(a.cu_q, 4) || !aligned_to(a.cu_k, 4) ||
         !aligned_to(a.out, 16) || !aligned_to(a.lse, 4) || !aligned_to(a.workspace, 256))
         return GRINQH_EALIGN;
-    const size_t out_bytes = static_cast<size_t>(a.total_q) * qw * (a.out_dtype == GRINQH_BF16 ? 2 : 4);
-    if (overlaps(a.q, static_cast<size_t>((a.total_q - 1) * a.q_stride + qw) * 2, a.out, out_bytes)) return GRINQH_EINVAL;
-    if (a.total_k > 0 &&
-        (overlaps(a.k, static_cast<size_t>((a.total_k - 1) * a.k_stride + kw) * 2, a.out, out_bytes) ||
-         overlaps(a.v, static_cast<size_t>((a.total_k - 1) * a.v_stride + kw) * 2, a.out, out_bytes)))
-        return GRINQH_EINVAL;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     if (a.head_dim == 64) return launch_prefill_attention<64>(a, s);
     if (a.head_dim == 128) return launch_prefill_attention<128>(a, s);

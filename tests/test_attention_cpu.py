@@ -303,6 +303,25 @@ def test_prefill_attention_checks_its_arguments_before_any_device_call():
     assert call(total_q=0) == B.GRINQH_OK and call(batch=0) == B.GRINQH_OK
 
 
+def test_prefill_attention_refuses_to_write_where_it_reads():
+    """out, lse and a workspace that is used against q, k, v, the ends and one another, at both ends of each."""
+    lib = G.load()
+    a = dict(q_stride=512, k_stride=128, v_stride=128, batch=1, total_q=20, total_k=9000, n_q_heads=8, n_kv_heads=2,
+             head_dim=64, causal=1, scale=0.1, out_dtype=1)
+    ws = lib.grinqh_prefill_attention_workspace_bytes(ctypes.byref(B.PrefillAttentionArgs(**a)))
+    assert ws > 0
+    sizes = dict(q=20 * 512 * 2, k=9000 * 128 * 2, v=9000 * 128 * 2, cu_q=8, cu_k=8, out=20 * 512 * 4, lse=20 * 8 * 4,
+                 workspace=ws)
+    good = {name: (i + 1) << 24 for i, name in enumerate(sizes)}
+    for written, step in (("out", 16), ("lse", 4), ("workspace", 256)):
+        for other in sizes:
+            below = (sizes[written] - 1) // step * step
+            for at in (0, -below, (sizes[other] - 1) // step * step):
+                if other != written:
+                    p = B.PrefillAttentionArgs(**a, **dict(good, **{written: good[other] + at}), workspace_bytes=ws)
+                    assert lib.grinqh_prefill_attention(ctypes.byref(p), None) == B.GRINQH_EINVAL, (written, other, at)
+
+
 def test_binding_refuses_host_tensors_and_wrong_shapes():
     import torch
     x = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
