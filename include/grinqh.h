@@ -333,7 +333,7 @@ size_t grinqh_kv_grid_bytes(const grinqh_kv_layout* L);
  *              n_pages * page_size is not written (padding).  The slots
  *              written by one call must differ: a slot named twice is left
  *              holding a mixture of the rows.
- * k and v must not overlap the pools, nor the pools one another (EINVAL; a
+ * k, v and slots must not overlap the pools, nor the pools one another (EINVAL; a
  * cache whose keys and values share a pool can only be read). */
 grinqh_status grinqh_kv_write(const grinqh_kv_layout* L, const grinqh_kv_pools* pools, const void* k,
                               const void* v, grinqh_dtype dtype, int64_t k_stride, int64_t v_stride,
@@ -343,7 +343,8 @@ grinqh_status grinqh_kv_write(const grinqh_kv_layout* L, const grinqh_kv_pools* 
  * times each.
  *   k, v   [n_tokens][n_kv_heads][head_dim] of dtype out, contiguous, 16-byte
  *          aligned: s * (c + 1/2) + z in fp32 (one rounding), bf16 output
- *          rounded to nearest even; zeros for a slot outside the pool. */
+ *          rounded to nearest even; zeros for a slot outside the pool.  They
+ *          must not overlap each other, the slots or the pools. */
 grinqh_status grinqh_kv_read(const grinqh_kv_layout* L, const grinqh_kv_pools* pools, const int64_t* slots,
                              int32_t n_tokens, void* k, void* v, grinqh_dtype dtype, void* stream);
 

@@ -296,21 +296,11 @@ grinqh_status grinqh_kv_write(const grinqh_kv_layout* L, const grinqh_kv_pools* 
         reinterpret_cast<uintptr_t>(slots) % 8 != 0)
         return GRINQH_EALIGN;
     const size_t code_bytes = grinqh_kv_code_bytes(L), grid_bytes = grinqh_kv_grid_bytes(L);
-    // Keys and values are written at the same time.
-    if (overlaps(pools->k_codes, code_bytes, pools->v_codes, code_bytes) ||
-        overlaps(pools->k_grid, grid_bytes, pools->v_grid, grid_bytes))
+    const auto rows = [&](int64_t stride) { return static_cast<size_t>(((n_tokens - 1) * stride + width) * eb); };
+    if (written_overlaps({{pools->k_codes, code_bytes}, {pools->v_codes, code_bytes},      // keys and values at the same time
+                          {pools->k_grid, grid_bytes}, {pools->v_grid, grid_bytes}},
+                         {{k, rows(k_stride)}, {v, rows(v_stride)}, {slots, n_tokens * sizeof(int64_t)}}))
         return GRINQH_EINVAL;
-    for (const void* codes : {pools->k_codes, pools->v_codes})
-        if (overlaps(codes, code_bytes, pools->k_grid, grid_bytes) || overlaps(codes, code_bytes, pools->v_grid, grid_bytes))
-            return GRINQH_EINVAL;
-    const void* src[2] = {k, v};
-    const int64_t stride[2] = {k_stride, v_stride};
-    for (int i = 0; i < 2; ++i) {
-        const size_t n = static_cast<size_t>(((n_tokens - 1) * stride[i] + width) * eb);
-        if (overlaps(src[i], n, pools->k_codes, code_bytes) || overlaps(src[i], n, pools->v_codes, code_bytes) ||
-            overlaps(src[i], n, pools->k_grid, grid_bytes) || overlaps(src[i], n, pools->v_grid, grid_bytes))
-            return GRINQH_EINVAL;
-    }
     const KvWriteArgs a{kv_dims(*L), {k, v}, {pools->k_codes, pools->v_codes}, {pools->k_grid, pools->v_grid},
                         slots, {k_stride, v_stride}, n_tokens};
     return dispatch<WriteLaunch>(*L, dtype, row_grid(*L, n_tokens), static_cast<hipStream_t>(stream), a);
@@ -326,11 +316,10 @@ grinqh_status grinqh_kv_read(const grinqh_kv_layout* L, const grinqh_kv_pools* p
     if (!aligned16(k) || !aligned16(v) || reinterpret_cast<uintptr_t>(slots) % 8 != 0) return GRINQH_EALIGN;
     const size_t n = static_cast<size_t>(n_tokens) * L->n_kv_heads * L->head_dim * (dtype == GRINQH_BF16 ? 2 : 4);
     const size_t code_bytes = grinqh_kv_code_bytes(L), grid_bytes = grinqh_kv_grid_bytes(L);
-    if (overlaps(k, n, v, n)) return GRINQH_EINVAL;
-    for (const void* dst : {k, v})
-        if (overlaps(dst, n, pools->k_codes, code_bytes) || overlaps(dst, n, pools->v_codes, code_bytes) ||
-            overlaps(dst, n, pools->k_grid, grid_bytes) || overlaps(dst, n, pools->v_grid, grid_bytes))
-            return GRINQH_EINVAL;
+    if (written_overlaps({{k, n}, {v, n}}, {{slots, n_tokens * sizeof(int64_t)},
+                                            {pools->k_codes, code_bytes}, {pools->v_codes, code_bytes},
+                                            {pools->k_grid, grid_bytes}, {pools->v_grid, grid_bytes}}))
+        return GRINQH_EINVAL;
     const KvReadArgs a{kv_dims(*L), {pools->k_codes, pools->v_codes}, {pools->k_grid, pools->v_grid}, {k, v},
                        slots, n_tokens};
     return dispatch<ReadLaunch>(*L, dtype, row_grid(*L, n_tokens), static_cast<hipStream_t>(stream), a);

@@ -190,6 +190,23 @@ def test_rows_are_not_written_to_pools_that_share_memory(bits):
                                                None) == B.GRINQH_EINVAL, (one, other, at)
 
 
+@pytest.mark.parametrize("bits", [4, 16])
+def test_slots_must_not_lie_where_rows_are_stored(bits):
+    """In a pool that kv_write fills, in an output of kv_read."""
+    lib = G.load()
+    L = G.grinqh_kv_layout_init(2, 64, 16, 8, bits)
+    P = _pools()
+    codes, grid = G.grinqh_kv_code_bytes(L), G.grinqh_kv_grid_bytes(L)
+    for field, size in (("k_codes", codes), ("v_codes", codes), ("k_grid", grid), ("v_grid", grid)):
+        for at in (0, -24, size - 8):
+            if size:
+                assert lib.grinqh_kv_write(ctypes.byref(L), ctypes.byref(P), K64, 2 * K64, 0, 128, 128, 4,
+                                           getattr(P, field) + at, None) == B.GRINQH_EINVAL, (field, at)
+    for out in (K64, 2 * K64):
+        for at in (0, -24, 4 * 128 * 2 - 8):
+            assert lib.grinqh_kv_read(ctypes.byref(L), ctypes.byref(P), out + at, 4, K64, 2 * K64, 0, None) == B.GRINQH_EINVAL
+
+
 def test_decode_attention_checks_its_arguments_before_any_device_call():
     lib = G.load()
     L = G.grinqh_kv_layout_init(2, 64, 16, 8, 8)
