@@ -27,13 +27,20 @@ if torch is not None:
     _BF16, _I32, _I64 = torch.bfloat16, torch.int32, torch.int64
 
 _COUNTER_BYTES = 16384                           # of a decode attention's workspace, zero before its first use
+_LONGEST = 1 << 28                               # max_len that the library takes
 
 
 # ------------------------------------------------------------------ host ----
 
+def _fit(x, bits: int = 32) -> int:
+    """x, or the end of the type's range nearest to it: ctypes would drop the
+    higher bits, and the library refuses either end of every size."""
+    return max(-1 << bits - 1, min(int(x), (1 << bits - 1) - 1))
+
+
 def grinqh_kv_layout_init(n_kv_heads: int, head_dim: int, page_size: int, n_pages: int, bits: int) -> KVLayout:
     L = KVLayout()
-    _check(load().grinqh_kv_layout_init(int(n_kv_heads), int(head_dim), int(page_size), int(n_pages), int(bits),
+    _check(load().grinqh_kv_layout_init(_fit(n_kv_heads), _fit(head_dim), _fit(page_size), _fit(n_pages), _fit(bits),
                                         ctypes.byref(L)), "grinqh_kv_layout_init")
     return L
 
@@ -47,15 +54,16 @@ def grinqh_kv_grid_bytes(L: KVLayout) -> int:
 
 
 def grinqh_debug_kv_row(L: KVLayout, slot: int, head: int) -> int:
-    return int(load().grinqh_debug_kv_row(ctypes.byref(L), int(slot), int(head)))
+    return int(load().grinqh_debug_kv_row(ctypes.byref(L), _fit(slot, 64), _fit(head)))
 
 
 def grinqh_debug_page_row(L: KVLayout, page: int, head: int, t: int) -> int:
-    return int(load().grinqh_debug_page_row(ctypes.byref(L), int(page), int(head), int(t)))
+    return int(load().grinqh_debug_page_row(ctypes.byref(L), _fit(page), _fit(head),
+                                              int(t) if 0 <= t < 1 << 31 else -1))
 
 
 def grinqh_attention_workspace_bytes(L: KVLayout, n_q_heads: int, batch: int, max_len: int) -> int:
-    return int(load().grinqh_attention_workspace_bytes(ctypes.byref(L), int(n_q_heads), int(batch), int(max_len)))
+    return int(load().grinqh_attention_workspace_bytes(ctypes.byref(L), _fit(n_q_heads), _fit(batch), _fit(max_len)))
 
 
 # ---------------------------------------------------------------- checks ----
@@ -315,8 +323,8 @@ def grinqh_decode_attention(cache: KVCache, q, page_table, seq_lens, max_len: in
     if batch < 2:
         q_stride, table_stride = width, max_pages
     _run("grinqh_decode_attention", device, stream, *cache._refs, q.data_ptr(), _CODES[q.dtype], q_stride, heads,
-         page_table.data_ptr(), table_stride, max_pages, seq_lens.data_ptr(), batch, max_len,
-         dim ** -0.5 if scale is None else scale, out.data_ptr(), _CODES[out.dtype],
+         page_table.data_ptr(), table_stride, max_pages, seq_lens.data_ptr(), batch,
+         max_len if 0 < max_len <= _LONGEST else 0, dim ** -0.5 if scale is None else scale, out.data_ptr(), _CODES[out.dtype],
          None if lse is None else _plain(lse, "lse", torch.float32, device, batch * heads), workspace.data_ptr(),
          workspace.nbytes)
 
@@ -334,7 +342,7 @@ def decode_attention(cache: KVCache, q, page_table, seq_lens, max_len=None, scal
     if dim != cache.head_dim:
         raise ValueError(f"q must be [batch][n_q_heads][{cache.head_dim}], not {list(q.shape)}")
     if max_len is None:
-        max_len = min(max(1, page_table.shape[1] * cache.layout.page_size), 1 << 28)
+        max_len = min(max(1, page_table.shape[1] * cache.layout.page_size), _LONGEST)
     out = _empty_as(q, out_dtype or torch.bfloat16, device, stream)
     lse = _empty((batch, heads), torch.float32, device, stream) if return_lse else None
     if workspace is None:
@@ -376,8 +384,8 @@ def _prefill_args(q, k, v, cu_q, cu_k, out, causal, scale, lse):
         _floats(out, "out", device, q.numel())
     return PrefillAttentionArgs(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), qs if total_q > 1 else q_width, ks if total_k > 1 else width,
-        vs if total_k > 1 else width, cu_q.data_ptr(), cu_k.data_ptr(), ends - 1, total_q, total_k, heads, kv_heads, dim,
-        bool(causal), dim ** -0.5 if scale is None else scale, out.data_ptr(), _CODES[out.dtype],
+        vs if total_k > 1 else width, cu_q.data_ptr(), cu_k.data_ptr(), ends - 1 if ends <= 1 << 31 else -1,
+        total_q, total_k, heads, kv_heads, dim, bool(causal), dim ** -0.5 if scale is None else scale, out.data_ptr(), _CODES[out.dtype],
         None if lse is None else _plain(lse, "lse", torch.float32, device, total_q * heads))
 
 

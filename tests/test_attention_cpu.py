@@ -372,6 +372,55 @@ def test_prefill_workspace_of_many_empty_sequences():
             assert need(batch=batch, total_q=queries, total_k=1 << 24) <= tiles * 2 * parts * 128 * 130 * 4, (queries, batch)
 
 
+def test_binding_refuses_sizes_that_do_not_fit_32_bits():
+    """2^32 + n is not n: layouts, workspaces, the bound on the lengths and the number of sequences."""
+    import torch
+    from input_adaptive_bit_amd import attention as N
+    good = (2, 64, 16, 8, 8)
+    for at in range(5):
+        for wrap in (2 ** 32, -2 ** 32, 2 ** 40):
+            with pytest.raises(G.GrinqhError):
+                G.grinqh_kv_layout_init(*(x + wrap * (i == at) for i, x in enumerate(good)))
+    L = G.grinqh_kv_layout_init(*good)
+    for at in range(3):
+        for wrap in (2 ** 32, -2 ** 32):
+            sizes = [x + wrap * (i == at) for i, x in enumerate((4, 3, 100))]
+            assert G.grinqh_attention_workspace_bytes(L, *sizes) == 0
+            with pytest.raises(G.GrinqhError):
+                G.new_attention_workspace(L, *sizes)
+    for wrap in (2 ** 32, -2 ** 32):
+        assert G.grinqh_debug_kv_row(L, 3, 1 + wrap) == -1 and G.grinqh_debug_kv_row(L, 3 + wrap * 2 ** 32, 1) == -1
+        assert G.grinqh_debug_page_row(L, 3, 1 + wrap, 0) == -1 and G.grinqh_debug_page_row(L, 3, 1, wrap * 2) == -1
+        assert G.grinqh_debug_page_row(L, 3 + wrap, 1, 0) < 0
+
+    class Sizes:
+        """Stands for tensors on a GPU where only their sizes are asked for."""
+        def __init__(self, *shape, dtype=torch.bfloat16):
+            self.shape, self.dtype, self.device, self.is_cuda = torch.Size(shape), dtype, torch.device("cuda", 0), True
+            self.strides = [int(np.prod(shape[i + 1:], dtype=object)) for i in range(len(shape))]
+
+        stride = lambda self: self.strides                       # noqa: E731
+        numel = lambda self: self.shape.numel()                  # noqa: E731
+        get_device = lambda self: 0                              # noqa: E731
+        is_contiguous = lambda self: True                        # noqa: E731
+        data_ptr = lambda self: 1 << 20                          # noqa: E731
+        nbytes = 1 << 30
+
+    sent, orig = [], (N._run, torch.Tensor)
+    N._run, torch.Tensor = (lambda *a: sent.append(a)), Sizes
+    try:
+        cache = type("C", (), dict(device=torch.device("cuda", 0), n_kv_heads=2, head_dim=64, layout=L, _refs=()))()
+        q, i32 = Sizes(3, 4, 64), torch.int32
+        for max_len, passed in ((100, 100), (1 << 28, 1 << 28), (0, 0), (-5, 0), (2 ** 32 + 100, 0), (100 - 2 ** 32, 0)):
+            N.grinqh_decode_attention(cache, q, Sizes(3, 7, dtype=i32), Sizes(3, dtype=i32), max_len, q, Sizes(64))
+            assert sent.pop()[12] == passed
+        for ends, batch in ((3, 2), ((1 << 20) + 1, 1 << 20), (2 ** 32 + 3, -1)):
+            cu = Sizes(ends, dtype=i32)
+            assert N._prefill_args(q, Sizes(5, 2, 64), Sizes(5, 2, 64), cu, cu, q, True, None, None).batch == batch
+    finally:
+        N._run, torch.Tensor = orig
+
+
 def test_binding_says_what_does_not_fit():
     """Every condition of the calls' joint test has its own message."""
     import torch
