@@ -366,7 +366,8 @@ int64_t grinqh_debug_page_row(const grinqh_kv_layout* L, int32_t page, int32_t h
  *   o_h = sum_t p_t v_gt,  p_t = exp(a_t) / sum_u exp(a_u),  a_t = scale * q_h . k_gt,
  * over the tokens t that the query sees.  A query that sees none gets zeros.
  * lse_h = log(sum_t exp(a_t)) (-Inf where no token is seen).  Scores, softmax
- * statistics and sums are fp32.  Infinities and NaN in tokens that are seen go
+ * statistics and sums are fp32; fp32 queries enter the scores as the sum of two
+ * bf16 (2^-16 relative; a value past bf16's range counts as infinite).  Infinities and NaN in tokens that are seen go
  * through the formula (where an infinite value makes it infinite, an output may
  * be NaN; a query whose seen scores are all -Inf gets zeros); in tokens that are
  * not seen they have no effect.  Where q . k is finite but its product with

@@ -424,8 +424,10 @@ __device__ __forceinline__ void agent_store(float* p, float2 v) {
 // Columns of the score tile that a head has.
 __host__ __device__ constexpr int copies_of(int bits, int group) { return bits == 4 && group <= kHeadTile / 2 ? 2 : 1; }
 
-// Waves of a workgroup that has a CU to itself, as many as its registers allow
-// (fp32 queries: twelve at 128 dimensions; the plan does not know the type).
+// Waves of a workgroup that has a CU to itself, by its registers (fp32 queries:
+// twelve at 128 dimensions; the plan does not know the type).  Most fit; in
+// scratch are 9 registers of a wave at 16 bits and 256 dimensions, and with fp32
+// queries 71 there, 21 at 8 bits and 256 dimensions and 11 at 8 bits and 128.
 __host__ __device__ constexpr int big_waves(int D, int copies, int qp = 1) {
     return D == 256 ? 8 : copies == 2 && (D == 64 || qp == 1) ? 16 : 12;
 }

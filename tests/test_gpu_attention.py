@@ -95,6 +95,37 @@ def test_decode_of_four_bits_and_small_groups(dev, dim, group, page, n, q_dtype)
         _decode(c, q, q_dtype, "f32", dev, max_len=n, lens=[length], what=str(length))
 
 
+@pytest.mark.parametrize("bits,group", [(8, 3), (16, 3), (4, 16), (4, 5)])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_decode_of_full_queries_over_a_long_cache(dev, dim, bits, group):
+    """fp32 queries in the largest workgroups.  They enter the scores as the sum of two bf16, which is off by half a step
+    of half a step, 2^-16: a score by 2^-16 sum |q_d k_d|, an output by twice that of its sum p |v|."""
+    import input_adaptive_bit_amd as G
+    import torch
+    say(f"decode fp32 queries bits={bits} group={group} dim={dim}")
+    rng = np.random.default_rng(dim + bits + group)
+    c = Cache(rng, [5003, 31], 4, dim, bits, 64, dev)
+    q = _queries(rng, 2, 4 * group, dim, "f32")
+    scale = dim ** -0.5
+    for length in (5003, 4992, 33, 1, 0):
+        for batch in (1, 2):
+            lens = [length, 31][:batch]
+            out, lse = G.decode_attention(c.dev, torch.from_numpy(q[:batch]).to(dev), c.dev_table[:batch],
+                                          torch.tensor(lens, dtype=torch.int32, device=dev), 5003, out_dtype=torch.float32,
+                                          return_lse=True)
+            o, bound, l, l_bound = decode_reference(c, q[:batch], scale, "f32", lens)
+            for b in range(batch):
+                for h in range(4 * group):
+                    (k, terms), (v, v_terms) = (c.gathered(b, h // group, which, lens[b]) for which in range(2))
+                    if len(k):
+                        _, _, p = A.attend(q[b, h:h + 1], k, v, scale)
+                        off = 2.0 ** -16 * scale * (terms @ np.abs(q[b, h].astype(np.float64))).max()
+                        bound[b, h] += 2 * off * (p @ v_terms)[0]
+                        l_bound[b, h] += off
+            inside(_np(out), o, bound, f"out, length {length}")
+            inside(_np(lse), l, l_bound, f"lse, length {length}")
+
+
 def test_decode_of_many_sequences_of_very_different_lengths(dev):
     rng = np.random.default_rng(8)
     lens = [int(x) for x in rng.integers(0, 700, 40)] + [3001, 0, 1]
