@@ -367,10 +367,11 @@ int64_t grinqh_debug_page_row(const grinqh_kv_layout* L, int32_t page, int32_t h
  * over the tokens t that the query sees.  A query that sees none gets zeros.
  * lse_h = log(sum_t exp(a_t)) (-Inf where no token is seen).  Scores, softmax
  * statistics and sums are fp32; fp32 queries enter the scores as the sum of two
- * bf16 (2^-16 relative; a value past bf16's range counts as infinite).  Infinities and NaN in tokens that are seen go
- * through the formula (where an infinite value makes it infinite, an output may
- * be NaN; a query whose seen scores are all -Inf gets zeros); in tokens that are
- * not seen they have no effect.  Where q . k is finite but its product with
+ * bf16 (2^-16 relative; a value past bf16's range counts as infinite).
+ * Infinities and NaN in tokens that are seen go through the formula (where an
+ * infinite value makes it infinite, an output may be NaN; a query whose seen
+ * scores are all -Inf gets zeros); in tokens that are not seen they have no
+ * effect.  Where q . k is finite but its product with
  * scale passes fp32's range, lse is infinite; the prefill stage still gives the
  * formula's output, in the decode stage such a score counts as infinite.
  *
@@ -387,7 +388,8 @@ int64_t grinqh_debug_page_row(const grinqh_kv_layout* L, int32_t page, int32_t h
  *               negative and as min(max_len, max_pages * page_size) if above.
  *   batch       0 .. 2^20 (0: nothing is launched), and batch * n_kv_heads *
  *               ceil(n_q_heads / n_kv_heads / 16) at most 2^23; max_len 1 ..
- *               2^28, the host's bound on the lengths.
+ *               2^28, the host's bound on the lengths: a long cache is cut into
+ *               parts by it, so one near the longest length is faster.
  *   scale       -1e30 .. 1e30.
  *   out         [batch][n_q_heads][head_dim] of out_dtype, contiguous, 16-byte
  *               aligned.

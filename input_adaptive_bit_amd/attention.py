@@ -333,8 +333,9 @@ def decode_attention(cache: KVCache, q, page_table, seq_lens, max_len=None, scal
                      return_lse: bool = False, workspace=None, stream=None):
     """Attention of one new token of every sequence over its cached tokens:
     out [batch][n_q_heads][head_dim], and lse if asked for (allocates them and,
-    if not given, a zero-filled workspace).  max_len: the host's bound on
-    seq_lens, by default what the page table can hold."""
+    if not given, a workspace).  max_len: the host's bound on seq_lens, by default
+    what the page table can hold; a long cache is cut into parts by it, so one
+    near the longest length is faster."""
     device = cache.device
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a [batch][n_q_heads][head_dim] tensor")

@@ -39,7 +39,8 @@
 // length, 2 for the queries and the first tile, 1.5 to store a part and count
 // its arrival, 2 to 3 to join.  At 4 bits unpacking is half of the vector
 // instructions (380 for a tile), which take half of the cycles: 131071 tokens and 64
-// heads (143 MB) in 39 us.
+// heads (143 MB) in 39 us.  All of these with the longest length as max_len (the
+// times of kernels alone, as the others in this paragraph).
 #include <math.h>
 
 #include <algorithm>
@@ -120,9 +121,10 @@ struct Shape {
 // At 4 bits the heads of groups of up to 8 have two columns of the score tile each
 // (COPIES 2): column i and column i + 8 hold the same scores, and the lanes of the
 // first weigh the tokens of the tile's first half, those of the second the others,
-// as states of their own until the end.  Half the softmax work for each lane:
-// 131071 tokens take 42 us instead of 44 (and 40 with the waves that the registers
-// then allow), 32 sequences of 2048 22 instead of 24.  At 8 bits it gained nothing.
+// as states of their own until the end.  Half the softmax work for each lane: in a
+// captured graph 131071 tokens take 42 us instead of 44 (and 41 with the waves that
+// the registers then allow), 32 sequences of 2048 22 instead of 24.  At 8 bits it
+// gained nothing.
 __device__ __forceinline__ bool second_copy(int lane) { return (lane & 8) != 0; }
 
 // A wave's 32 tokens as loaded: keys of two score tiles, values of this lane's
@@ -696,8 +698,10 @@ __global__ __launch_bounds__(W * kWave, waves_per_simd(D, QP, W)) void decode_ke
     }
 }
 
-// How a call is cut up (host arithmetic on its sizes alone).  Measured in us a
-// call, 8 bits, 8 key-value heads of 128, groups of 4:
+// How a call is cut up (host arithmetic on its sizes alone, so by max_len and not
+// by the lengths: 4000 tokens take 11.4 us with that as max_len and 31.9 with
+// 131072, whose parts are of 4224 tokens).  Measured in us a call in a captured
+// graph, 8 bits, 8 key-value heads of 128, groups of 4, max_len the longest length:
 //   one sequence, four waves and eight: 500 tokens 8.3, 10.2; 2000 10.0, 10.6; 4000
 //   12.8, 11.8; 32768 24, 22; eight waves and twelve: 8192 15.2, 14.3; 131071 at 4
 //   bits, groups of 8, 46.6, 43.5; twelve and sixteen there, with two columns a head:

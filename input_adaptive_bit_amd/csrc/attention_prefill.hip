@@ -19,7 +19,8 @@
 // multiplies all of a row's weights alike.  Past kFar it would not be small
 // any more (past 2^30 it alone makes weights 0 or infinite): the tiles of such
 // rows are used outside the inner loop, with (s - max) c.  At 8192 tokens, 32
-// heads of 128, the test for them takes 533 us from 530; with every row so, 2830.
+// heads of 128, the test for them takes 533 us from 530 (one card, in a captured
+// graph); with every row so, 2830.
 //
 // Values.  O^T = V^T P^T.  The scores a lane holds are its share of the
 // contraction as they are (the contraction's order is free), rounded to bf16
@@ -30,11 +31,12 @@
 // hardly ever rescaled.
 //
 // What bounds it.  Matrix and vector instructions together: at 8192 tokens, 32
-// heads of 128 (520 - 570 us, 960 - 1060 TFLOP/s), the matrix cores are busy for 53%
-// of the cycles and the vector units for 53%, 40% of the matrix cycles with
-// vector work beside them, at 1.8 - 1.9 GHz; LDS reads take 26% and have no bank
-// conflicts.  A wave's own overlap (the halves of a tile) took it from 594 us; 64
-// rows to a wave would halve the LDS reads but leave one wave per SIMD.  Heads of
+// heads of 128 (525 - 547 us in a program, by the card, 1005 - 1047 TFLOP/s; 550 - 602
+// under the kernel trace), the matrix cores are busy for 51% of the cycles and the
+// vector units for 52%, 41% of the matrix cycles with vector work beside them, at
+// 1.8 - 1.9 GHz; LDS reads take 26% and have no bank conflicts.  A wave's own
+// overlap (the halves of a tile) took it from 594 us; 64 rows to a wave would
+// halve the LDS reads but leave one wave per SIMD.  Heads of
 // 64 have half the matrix work for the same exponentials: 720 TFLOP/s at 4096
 // tokens, the vector units busy for 60% of the cycles, the matrix cores for 32%.
 // Short prompts: a workgroup takes 2 us to find its rows, 3 to its first tile,
