@@ -371,9 +371,9 @@ int64_t grinqh_debug_page_row(const grinqh_kv_layout* L, int32_t page, int32_t h
  * Infinities and NaN in tokens that are seen go through the formula (where an
  * infinite value makes it infinite, an output may be NaN; a query whose seen
  * scores are all -Inf gets zeros); in tokens that are not seen they have no
- * effect.  Where q . k is finite but its product with
- * scale passes fp32's range, lse is infinite; the prefill stage still gives the
- * formula's output, in the decode stage such a score counts as infinite.
+ * effect.  Where q . k is finite but a score passes fp32's range, lse is
+ * infinite; the prefill stage still gives the formula's output, in the decode
+ * stage a score past 2.3e38 counts as infinite.
  *
  * Decode stage: one new token of every sequence attends to its cached
  * tokens (the new one among them, if it was written first).

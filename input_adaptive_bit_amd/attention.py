@@ -324,8 +324,8 @@ def grinqh_decode_attention(cache: KVCache, q, page_table, seq_lens, max_len: in
         q_stride, table_stride = width, max_pages
     _run("grinqh_decode_attention", device, stream, *cache._refs, q.data_ptr(), _CODES[q.dtype], q_stride, heads,
          page_table.data_ptr(), table_stride, max_pages, seq_lens.data_ptr(), batch,
-         max_len if 0 < max_len <= _LONGEST else 0, dim ** -0.5 if scale is None else scale, out.data_ptr(), _CODES[out.dtype],
-         None if lse is None else _plain(lse, "lse", torch.float32, device, batch * heads), workspace.data_ptr(),
+         max_len if 0 < max_len <= _LONGEST else 0, dim ** -0.5 if scale is None else scale, out.data_ptr(),
+         _CODES[out.dtype], None if lse is None else _plain(lse, "lse", torch.float32, device, batch * heads), workspace.data_ptr(),
          workspace.nbytes)
 
 
@@ -386,8 +386,8 @@ def _prefill_args(q, k, v, cu_q, cu_k, out, causal, scale, lse):
     return PrefillAttentionArgs(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), qs if total_q > 1 else q_width, ks if total_k > 1 else width,
         vs if total_k > 1 else width, cu_q.data_ptr(), cu_k.data_ptr(), ends - 1 if ends <= 1 << 31 else -1,
-        total_q, total_k, heads, kv_heads, dim, bool(causal), dim ** -0.5 if scale is None else scale, out.data_ptr(), _CODES[out.dtype],
-        None if lse is None else _plain(lse, "lse", torch.float32, device, total_q * heads))
+        total_q, total_k, heads, kv_heads, dim, bool(causal), dim ** -0.5 if scale is None else scale,
+        out.data_ptr(), _CODES[out.dtype], None if lse is None else _plain(lse, "lse", torch.float32, device, total_q * heads))
 
 
 def grinqh_prefill_attention_workspace_bytes(q, k, v, cu_q, cu_k, out, causal: bool = True) -> int:

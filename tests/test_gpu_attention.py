@@ -492,6 +492,28 @@ def test_prefill_scores_with_a_large_common_part(dev, dim, lens_q, lens_k, split
 
 
 @pytest.mark.parametrize("dim", [64, 128, 256])
+def test_a_row_far_from_zero_leaves_its_neighbours_alone(dev, dim):
+    """One query 2^16 times as large, scores past 2^16 in its row alone: every other row keeps its bits."""
+    import input_adaptive_bit_amd as G
+    import torch
+    rng = np.random.default_rng(dim + 2)
+    q, k, v, cu, _ = _packed(rng, 4, 2, dim, [200, 90], [200, 90])
+    t = [to_bf16(x, dev) for x in (k, v)] + [torch.from_numpy(cu).to(dev)]
+    base, lse = G.prefill_attention(to_bf16(q, dev), *t, out_dtype=torch.float32, return_lse=True)
+    far = q.copy()
+    far[137, 2] *= 65536.0
+    out, far_lse = G.prefill_attention(to_bf16(far, dev), *t, out_dtype=torch.float32, return_lse=True)
+    others = torch.ones(290, 4, dtype=torch.bool, device=dev)
+    others[137, 2] = False
+    assert torch.equal(out[others], base[others]) and torch.equal(far_lse[others], lse[others])
+    # its largest score leads by more than 2^7: that key's value, in bf16 as it is
+    s = k[:138, 1].astype(np.float64) @ far[137, 2].astype(np.float64) * dim ** -0.5
+    first, second = np.argsort(s)[::-1][:2]
+    assert s[first] - s[second] > 128 and abs(s[first]) > 2 ** 16
+    assert np.array_equal(_np(out)[137, 2], v[first, 1])
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
 def test_keys_that_are_not_seen_may_be_anything(dev, dim):
     """NaN and infinities in later keys, other sequences and rows behind the
     last: the queries that do not see them are those of a call without."""
