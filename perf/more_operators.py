@@ -294,7 +294,8 @@ def _pages_plain(s):
     # pages from the end of the free list, sequence after sequence
     column = torch.arange(s["table"].shape[1], device="cuda")
     taken = granted[:, None] & (column >= held[:, None]) & (column < total[:, None])
-    number = (upto - need)[:, None] + column - held[:, None]
+    given = torch.where(granted, need, 0)
+    number = (given.cumsum(0) - given)[:, None] + column - held[:, None]
     table = torch.where(taken, s["free"][(s["n_free"] - 1 - number).clamp(0, len(s["free"]) - 1).long()], s["table"])
     s["table"].copy_(table)
     # slots and positions, padded
@@ -306,7 +307,7 @@ def _pages_plain(s):
     slot = table[seq, (position // page).clamp(0, table.shape[1] - 1)].long() * page + position % page
     slots = torch.where(there & granted[seq], slot, -1)
     positions = torch.where(there, position, 0)
-    left = s["n_free"] - torch.where(granted, need, 0).sum()
+    left = s["n_free"] - given.sum()
     return {"slots": slots, "positions": positions.int(), "lens": lens.int(), "cu_q": cu_q.int(), "cu_k": cu_k.int(),
             "table": s["table"], "n_free": left.int(), "refused": (~granted).sum().view(1).int()}
 
