@@ -461,6 +461,209 @@ typedef struct {
 size_t grinqh_prefill_attention_workspace_bytes(const grinqh_prefill_attention_args* args);
 grinqh_status grinqh_prefill_attention(const grinqh_prefill_attention_args* args, void* stream);
 
+/* ---- 4-bit weights with group scales -------------------------------------
+ *
+ * Matrices whose every `group` neighbouring input channels of an output
+ * channel share a scale and a zero point, on the grid of grinqh_quantize_rtn at
+ * b_max 4 (KD3 at b = b_max), for products that take every channel:
+ *   w_ij = s_jg * (q_ji + 1/2) + z_jg,   g = i / group,
+ *   y[t][j] = sum_i x[t][i] * w_ij.
+ * n_experts matrices of one shape lie behind one another; a plain layer has one.
+ * Codes are stored in the order in which the matrix cores take them: tiles of
+ * 16 outputs x 128 inputs, uint32 [n_experts][row_tiles][k_tiles][64][4]; in a
+ * tile word m of lane 16 * c + r holds the codes of output r and inputs
+ * 32 * m + 8 * c + e, e = 0 .. 7, each in the four bits from bit
+ * 3 + 4 * (e / 2) + 16 * (e % 2) on (modulo 32).  The grid is fp16
+ * [n_experts][row_tiles][k_tiles * 128 / group][16][2]: s, z.  Outputs and inputs
+ * past the ends are zeros. */
+typedef struct {
+    int32_t d_in;         /* input channels, a multiple of group, up to 2^20 */
+    int32_t d_out;        /* output channels, 1 .. 2^20 */
+    int32_t group;        /* 32, 64 or 128 */
+    int32_t n_experts;    /* 1 .. 1024 */
+    int32_t k_tiles;      /* ceil(d_in / 128) */
+    int32_t row_tiles;    /* ceil(d_out / 16) */
+} grinqh_fourbit_layout;
+
+/* Fill *out (host pointer); EINVAL for a value outside the ranges above, or
+ * for more than 2^40 bytes of codes. */
+grinqh_status grinqh_fourbit_layout_init(int32_t d_in, int32_t d_out, int32_t group, int32_t n_experts,
+                                         grinqh_fourbit_layout* out);
+
+/* Bytes of the packed codes and of the packed grid; 0 if L is NULL or invalid.
+ * Host only. */
+size_t grinqh_fourbit_code_bytes(const grinqh_fourbit_layout* L);
+size_t grinqh_fourbit_grid_bytes(const grinqh_fourbit_layout* L);
+
+/* Offline packing.
+ *   q      uint8 [n_experts][d_out][d_in], codes masked to 4 bits; 8-byte aligned.
+ *   s, z   fp16 [n_experts][d_out][d_in / group].
+ *   codes, grid   out, 16-byte aligned, fully overwritten, padding included.
+ * With grinqh_quantize_rtn(group, n_experts * d_out * d_in / group, 4, ...) on
+ * the bf16 weights as they lie, its q, s and z are this call's.  The outputs
+ * must not overlap each other or the inputs. */
+grinqh_status grinqh_fourbit_pack(const grinqh_fourbit_layout* L, const uint8_t* q, const uint16_t* s,
+                                  const uint16_t* z, uint8_t* codes, uint16_t* grid, void* stream);
+
+/* y = x times the matrix, for n_tokens tokens (one and a few stream the weights
+ * once; many go through larger tiles).
+ *   L          of one expert.
+ *   x          [n_tokens][d_in] of x_dtype, 16-byte aligned, tokens x_stride
+ *              elements apart (a multiple of 16 bytes, from d_in to 2^24).
+ *   n_tokens   0 .. 2^20 (0: nothing is launched).
+ *   codes, grid   as written by grinqh_fourbit_pack, 16-byte aligned.
+ *   y          [n_tokens][d_out] of y_dtype, contiguous, overwritten; bf16 output is
+ *              the fp32 result rounded to nearest even.
+ * Codes enter the products exactly and activations as they are (fp32 ones as
+ * the sum of three bf16; many tokens of fp32 are worked on five at a time, so a
+ * long prompt is better in bf16); sums are fp32, and the same call gives the
+ * same bits.  An infinite or NaN activation makes its token's outputs
+ * non-finite and no other's.  y must not overlap anything that is read. */
+grinqh_status grinqh_fourbit_linear(const grinqh_fourbit_layout* L, const void* x, grinqh_dtype x_dtype,
+                                    int64_t x_stride, int32_t n_tokens, const uint8_t* codes,
+                                    const uint16_t* grid, void* y, grinqh_dtype y_dtype, void* stream);
+
+/* The same for rows grouped by expert: row r of y, for ends[e] <= r < ends[e + 1],
+ * is a row of x times expert e's matrix.
+ *   x       [n_x][d_in] as above; n_x 1 .. 2^20.
+ *   rows    int32 [n_rows]: row r of y takes row rows[r] of x, any row any number
+ *           of times; a row outside 0 .. n_x - 1 counts as zeros.  NULL: row r
+ *           takes row r (rows from n_x on count as zeros).
+ *   ends    int32 [n_experts + 1], ascending; entries are clamped to 0 .. n_rows.
+ *           An expert may have no rows; rows before the first end and behind the
+ *           last are left as they are.
+ *   n_rows  0 .. 2^20 (0: nothing is launched).
+ *   y       [n_rows][d_out], as above. */
+typedef struct {
+    const void* x;
+    int64_t x_stride;
+    grinqh_dtype x_dtype;
+    int32_t n_x;
+    const int32_t* rows;
+    const int32_t* ends;
+    int32_t n_rows;
+    const uint8_t* codes;
+    const uint16_t* grid;
+    void* y;
+    grinqh_dtype y_dtype;
+} grinqh_expert_args;
+grinqh_status grinqh_expert_linear(const grinqh_fourbit_layout* L, const grinqh_expert_args* args, void* stream);
+
+/* ---- Norms of queries and keys, rotation by position ----------------------
+ *
+ * For every head row x of a token's queries and keys, in one pass:
+ *   x_i <- x_i * weight_i / sqrt(mean(x^2) + eps)       (where there is a weight)
+ *   (a, b) <- (a cos t - b sin t, b cos t + a sin t),   t = position * freqs[p],
+ * for the p-th of rope_dim / 2 pairs of the first rope_dim channels: (p, p +
+ * rope_dim / 2), or with neighbours nonzero (2p, 2p + 1).  The other channels
+ * are only normed.  Sums are fp32, angles fp64 up to the last turn; the result
+ * is rounded once to dtype.  With a cache, the keys as rounded and the values as
+ * they are go into their slots as grinqh_kv_write would put them.
+ *   q, k       [n_tokens][heads][head_dim] of dtype, 16-byte aligned, tokens
+ *              q_stride and k_stride elements apart (multiples of 16 bytes, from
+ *              heads * head_dim to 2^24).  n_q_heads, n_kv_heads 1 .. 1024;
+ *              head_dim 64, 128 or 256.
+ *   n_tokens   0 .. 2^24 (0: nothing is launched).
+ *   q_weight, k_weight   [head_dim] of weight_dtype, 16-byte aligned, or NULL: no norm.
+ *   eps        0 or more, finite (not used without weights).
+ *   positions  int32 [n_tokens], any sign.
+ *   freqs      fp64 [rope_dim / 2], radians per position; NULL only at rope_dim 0.
+ *   rope_dim   0 .. head_dim, a multiple of 16.
+ *   q_out, k_out   as q and k, with strides of their own; either may be its input
+ *              itself (same pointer and stride).  k_out NULL: not wanted (with a
+ *              cache only).
+ *   cache      NULL, or the layout of a cache with these n_kv_heads and head_dim;
+ *              then pools, v (as k, v_stride) and slots (int64 [n_tokens]; a token
+ *              whose slot is outside the pool is not written, the slots of one
+ *              call must differ) are needed.
+ * Outputs must not overlap one another nor, but for the case above, anything
+ * that is read; the pools neither. */
+typedef struct {
+    const void* q;
+    const void* k;
+    const void* v;
+    int64_t q_stride, k_stride, v_stride;
+    int32_t n_tokens, n_q_heads, n_kv_heads, head_dim;
+    grinqh_dtype dtype;
+    const void* q_weight;
+    const void* k_weight;
+    grinqh_dtype weight_dtype;
+    float eps;
+    const int32_t* positions;
+    const double* freqs;
+    int32_t rope_dim, neighbours;
+    void* q_out;
+    void* k_out;
+    int64_t q_out_stride, k_out_stride;
+    const grinqh_kv_layout* cache;
+    const grinqh_kv_pools* pools;
+    const int64_t* slots;
+} grinqh_rope_args;
+grinqh_status grinqh_qk_rope(const grinqh_rope_args* args, void* stream);
+
+/* ---- Pages of a batch -----------------------------------------------------
+ *
+ * The cache's pages are handed out on the GPU from the requests' lengths, so
+ * that a step can be captured and needs no copy to the host.  A pool's unused
+ * pages are a list: free_pages int32 [n_pages], of which the first n_free[0]
+ * count (clamped to 0 .. n_pages) and the last of these is handed out first.
+ * The two calls on a pool must be ordered on one stream.
+ *
+ * grinqh_kv_extend makes room for n_new[b] new tokens behind the seq_lens[b]
+ * cached ones of every sequence b (negative counts as 0) and writes what
+ * the other calls of the step take.  Sequences are served in order: one whose
+ * pages, with those of the sequences before it (served or not), are more than
+ * the list holds is refused, and so is one that would pass max_pages or whose
+ * tokens do not fit into capacity; a refused sequence keeps its length and
+ * pages, and its new tokens have no slots.  A sequence without new tokens is
+ * never refused.
+ *   page_table  int32 [batch][max_pages], rows table_stride entries apart: entries
+ *               of new pages are written, the others left.
+ *   new_lens    int32 [batch] out: lengths with the new tokens (may be seq_lens).
+ *   n_free_out  int32 [1] out (may be n_free).
+ *   refused     int32 [1] out: how many sequences were refused.
+ *   cu_q, cu_k  int32 [batch + 1] out: ends of the packed new tokens (as n_new
+ *               says, refused or not; clamped to 2^31 - 1), and of all tokens (of new_lens).
+ *   slots       int64 [capacity] out: slot of each new token, packed; -1 for a
+ *               refused sequence's, for a token whose page is not of the pool, and
+ *               behind the last token.
+ *   positions   int32 [capacity] out: place in its sequence; 0 behind the last token.
+ *   capacity    0 .. 2^24; batch 0 .. 2^20 (0: the outputs are as for none);
+ *               max_pages 1 .. 2^24; page_size as in a layout; n_pages 1 .. 2^24.
+ *   workspace   >= grinqh_kv_extend_workspace_bytes(batch) bytes, 16-byte aligned,
+ *               any contents.
+ * All pointers are aligned to their type.  Nothing that is written may overlap
+ * anything else, but for the two cases above. */
+typedef struct {
+    int32_t* page_table;
+    int64_t table_stride;
+    const int32_t* seq_lens;
+    const int32_t* n_new;
+    const int32_t* free_pages;
+    const int32_t* n_free;
+    int32_t batch, max_pages, page_size, n_pages, capacity;
+    int32_t* new_lens;
+    int32_t* n_free_out;
+    int32_t* refused;
+    int32_t* cu_q;
+    int32_t* cu_k;
+    int64_t* slots;
+    int32_t* positions;
+    void* workspace;
+    size_t workspace_bytes;
+} grinqh_extend_args;
+size_t grinqh_kv_extend_workspace_bytes(int32_t batch);
+grinqh_status grinqh_kv_extend(const grinqh_extend_args* args, void* stream);
+
+/* Give the pages of finished sequences back: for every b with finished[b]
+ * nonzero (uint8 [batch]), the pages that seq_lens[b] tokens take are put behind
+ * the list in their order (entries that name no page of the pool are passed
+ * over, and what would pass n_pages is dropped), the entries become -1 and the
+ * length 0. */
+grinqh_status grinqh_kv_release(int32_t* page_table, int64_t table_stride, int32_t* seq_lens,
+                                const uint8_t* finished, int32_t batch, int32_t max_pages, int32_t page_size,
+                                int32_t* free_pages, int32_t* n_free, int32_t n_pages, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

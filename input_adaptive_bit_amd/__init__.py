@@ -22,3 +22,12 @@ from .attention import (  # noqa: F401
     grinqh_prefill_attention, grinqh_prefill_attention_workspace_bytes, new_kv_cache, new_attention_workspace, kv_write, kv_read, decode_attention,
     prefill_attention,
 )
+from .fourbit import (  # noqa: F401
+    FourbitLayout, FourbitWeight, grinqh_fourbit_layout_init, grinqh_fourbit_code_bytes, grinqh_fourbit_grid_bytes,
+    grinqh_fourbit_pack, grinqh_fourbit_linear, grinqh_expert_linear, fourbit_pack, fourbit_quantize, fourbit_linear,
+    expert_linear,
+)
+from .rope import grinqh_qk_rope, qk_rope  # noqa: F401
+from .pages import (  # noqa: F401
+    Step, grinqh_kv_extend_workspace_bytes, grinqh_kv_extend, grinqh_kv_release, new_page_list, kv_extend, kv_release,
+)

@@ -1,0 +1,96 @@
+// The 4-bit weights' layout and the pieces that their products share.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "device_common.hpp"
+#include "grinqh.h"
+#include "internal.h"
+#include "kv_common.hpp"
+
+namespace grinqh {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kTileOut = 16, kTileIn = 128;        // a tile of codes: 1024 bytes, one 16-byte load of a wave
+constexpr int kMaxRows = 1 << 20, kMaxExperts = 1024;
+
+// A product's operands, for the kernels (ends NULL: one expert has all rows).
+struct FourbitArgs {
+    const void* x;
+    const int32_t* rows;
+    const int32_t* ends;
+    const uint8_t* codes;
+    const uint16_t* grid;
+    void* y;
+    int64_t x_stride;
+    int n_x, n_rows, d_in, d_out, k_tiles, row_tiles, n_experts, y_dtype;
+};
+
+// Eight codes (one word of a tile) as the bf16 values 16 + q, in the order of the
+// inputs: between 16 and 32 a bf16 steps by 1/8, so a code's four bits, put at
+// bit 3, add q to 16 exactly.  Seven instructions for eight codes.
+__device__ __forceinline__ bf16x8 codes_to_bf16(uint32_t w) {
+    constexpr uint32_t kMask = 0x00780078u, kSixteen = 0x41804180u;
+    const u32x4 v{(w & kMask) | kSixteen, ((w >> 4) & kMask) | kSixteen, ((w >> 8) & kMask) | kSixteen,
+                  (__builtin_amdgcn_alignbit(w, w, 12) & kMask) | kSixteen};
+    return __builtin_bit_cast(bf16x8, v);
+}
+constexpr float kCodeBias = 15.5f;                 // 16 + q - kCodeBias = q + 1/2
+
+// Rows of one expert's run that a tile of TM rows works on.
+struct RunTile {
+    int expert, row, count;                        // count 0: no such tile
+};
+
+__device__ __forceinline__ int run_sum_up_to(int x, int lane) {                // over lanes 0 .. lane
+#pragma unroll
+    for (int k = 1; k < kWave; k <<= 1) {
+        const int y = __shfl_up(x, k);
+        if (lane >= k) x += y;
+    }
+    return x;
+}
+
+// Tile `number` of all experts' tiles, in order; every lane of the wave comes here.
+__device__ __forceinline__ RunTile find_run_tile(const FourbitArgs& a, int tm, int number, int lane) {
+    if (a.ends == nullptr) return RunTile{0, number * tm, min(tm, a.n_rows - number * tm)};
+    const auto end_of = [&](int e) { return min(max(a.ends[e], 0), a.n_rows); };
+    int first = 0, count = a.n_experts, before = 0;
+    while (true) {
+        const int run = (count + kWave - 1) / kWave;
+        const int e0 = min(first + lane * run, first + count), e1 = min(e0 + run, first + count);
+        int tiles = 0;
+        int begin = end_of(e0);
+        for (int e = e0; e < e1; ++e) {
+            const int end = end_of(e + 1);
+            tiles += (max(end - begin, 0) + tm - 1) / tm;
+            begin = end;
+        }
+        const int sum = run_sum_up_to(tiles, lane);
+        const uint64_t over = __ballot(before + sum > number);
+        if (over == 0) return RunTile{0, 0, 0};
+        const int at = __builtin_ctzll(over);
+        before += __builtin_amdgcn_readlane(sum, at) - __builtin_amdgcn_readlane(tiles, at);
+        first = __builtin_amdgcn_readlane(e0, at);
+        count = __builtin_amdgcn_readlane(e1, at) - first;
+        if (run == 1) break;
+    }
+    const int begin = end_of(first), end = end_of(first + 1);
+    const int row = begin + (number - before) * tm;
+    return RunTile{first, row, min(tm, end - row)};
+}
+
+// The row of x that row r of the result takes, or -1: none, it counts as zeros.
+__device__ __forceinline__ int source_row(const FourbitArgs& a, int r) {
+    const int s = a.rows == nullptr ? r : a.rows[r];
+    return static_cast<unsigned>(s) < static_cast<unsigned>(a.n_x) ? s : -1;
+}
+
+bool valid_fourbit_layout(const grinqh_fourbit_layout* L);
+
+}  // namespace grinqh

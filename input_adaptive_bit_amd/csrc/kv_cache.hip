@@ -21,13 +21,12 @@
 
 #include "internal.h"
 #include "kv_common.hpp"
-#include "rtn.hpp"
+#include "kv_store.hpp"
 
 namespace grinqh {
 namespace {
 
 constexpr int kKvThreads = 256;
-constexpr int kPerLane = 8;               // values of a row per lane
 constexpr int kMaxKvGroups = 1 << 16;     // workgroups of a launch; more rows than they hold go round again
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -46,7 +45,6 @@ struct KvWriteArgs {
 // Row r of one call's rows; the lanes of a row come here together.
 template <int D, int BITS, typename T>
 __device__ __forceinline__ void write_row(const KvWriteArgs& a, int which, int64_t r, int lane) {
-    constexpr int kLanes = D / kPerLane;
     const int64_t token = r / a.d.heads;
     const int head = static_cast<int>(r - token * a.d.heads);
     const int64_t row = kv_row(a.d, a.slots[token], head);
@@ -68,8 +66,8 @@ __device__ __forceinline__ void write_row(const KvWriteArgs& a, int which, int64
             w[4 + i] = __uint_as_float(more[i]);
         }
     }
-    uint8_t* dst = a.codes[which] + row * (D * BITS / 8) + lane * (kPerLane * BITS / 8);
     if constexpr (BITS == 16) {
+        uint8_t* dst = a.codes[which] + row * (D * 2) + lane * (kPerLane * 2);
         if constexpr (sizeof(T) == 4) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -77,33 +75,7 @@ __device__ __forceinline__ void write_row(const KvWriteArgs& a, int which, int64
         }
         *reinterpret_cast<u32x4*>(dst) = raw;
     } else {
-        float lo = w[0], hi = w[0];                           // fminf and fmaxf ignore NaN
-#pragma unroll
-        for (int i = 1; i < kPerLane; ++i) {
-            lo = fminf(lo, w[i]);
-            hi = fmaxf(hi, w[i]);
-        }
-#pragma unroll
-        for (int m = 1; m < kLanes; m <<= 1) {
-            lo = fminf(lo, __shfl_xor(lo, m, kLanes));
-            hi = fmaxf(hi, __shfl_xor(hi, m, kLanes));
-        }
-        const __half sh = rtn_scale(lo, hi, BITS), zh = rtn_zero(lo);
-        const float s = __half2float(sh), z = __half2float(zh);
-        constexpr float top = static_cast<float>((1 << BITS) - 1);
-        uint32_t c[2] = {0u, 0u};
-#pragma unroll
-        for (int i = 0; i < kPerLane; ++i) {
-            const uint32_t q = s == 0.f ? 0u : rtn_code(w[i], z, s, top);
-            c[i * BITS / 32] |= q << (i * BITS % 32);
-        }
-        if constexpr (BITS == 8)
-            *reinterpret_cast<u32x2*>(dst) = u32x2{c[0], c[1]};
-        else
-            *reinterpret_cast<uint32_t*>(dst) = c[0];
-        if (lane == 0)
-            *reinterpret_cast<uint32_t*>(a.grid[which] + row * 2) =
-                __half_as_ushort(sh) | static_cast<uint32_t>(__half_as_ushort(zh)) << 16;
+        store_quantised_row<D, BITS>(w, a.codes[which], a.grid[which], row, lane);
     }
 }
 

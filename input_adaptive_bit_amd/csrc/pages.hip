@@ -1,0 +1,305 @@
+// The page plan of a batch's step: pages for the new tokens, their slots and
+// positions, the new lengths and the ends of the packed sequences.
+//
+// With h = ceil(len / page) pages held, t = ceil((len + new) / page) needed and
+// need = t - h, sequence b takes the pages
+//   free[n_free - 1 - (sum_{c < b} need_c + i)],  i = 0 .. need - 1,
+// if the sums of need up to b fit.  So one scan over the sequences decides all
+// of it (fourfold: pages, new tokens, granted pages, lengths), and then every new token can be
+// worked on alone: its sequence by a search in the ends, its page from the table
+// (the page that was begun before) or from the list.  The token that begins a
+// page writes the table's entry.
+//
+// The scan is one workgroup's.  A small step's tokens are done by the same
+// workgroup, in one launch; more tokens by a second launch over the whole card.
+#include <algorithm>
+
+#include "internal.h"
+#include "kv_common.hpp"
+
+namespace grinqh {
+namespace {
+
+constexpr int kPageThreads = 1024, kPageWaves = kPageThreads / kWave, kSpreadThreads = 256;
+constexpr int kOneLaunch = 4096;                   // tokens up to which the scan's workgroup does them too
+
+struct PagesArgs {
+    grinqh_extend_args p;
+    int page_shift;
+};
+
+// What the scan leaves of a sequence for its tokens: its length before, and the
+// place of its first new page among all that are taken (-1: refused).
+struct Sequence {
+    int32_t before, first;
+};
+
+struct Scanned {
+    int64_t need, fresh, granted, all;
+};
+
+__device__ __forceinline__ int64_t shfl_up64(int64_t x, int k) {
+    const int lo = __shfl_up(static_cast<int>(x), k), hi = __shfl_up(static_cast<int>(x >> 32), k);
+    return static_cast<int64_t>(static_cast<uint32_t>(lo)) | static_cast<int64_t>(hi) << 32;
+}
+
+// Inclusive sum over the workgroup's threads; `total` is the last.
+__device__ __forceinline__ int64_t block_sum_up_to(int64_t x, int64_t* waves, int64_t* total) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int k = 1; k < kWave; k <<= 1) {
+        const int64_t y = shfl_up64(x, k);
+        if (lane >= k) x += y;
+    }
+    __syncthreads();                                          // the waves' sums of the scan before have been read
+    if (lane == kWave - 1) waves[wave] = x;
+    __syncthreads();
+    int64_t before = 0, all = 0;
+    for (int w = 0; w < kPageWaves; ++w) {
+        before += w < wave ? waves[w] : 0;
+        all += waves[w];
+    }
+    *total = all;
+    return x + before;
+}
+
+__device__ __forceinline__ int32_t clamp32(int64_t x) { return static_cast<int32_t>(min(x, int64_t{0x7FFFFFFF})); }
+
+// New token t of sequence b, whose new tokens begin at `begin`.
+__device__ __forceinline__ void place_token(const PagesArgs& a, const Sequence& s, int n_free, int b, int t, int begin) {
+    const auto& p = a.p;
+    const int64_t position = static_cast<int64_t>(s.before) + (t - begin);
+    p.positions[t] = clamp32(position);
+    int64_t slot = -1;
+    if (s.first >= 0) {
+        const int64_t at = position >> a.page_shift, held = (static_cast<int64_t>(s.before) + p.page_size - 1) >> a.page_shift;
+        int32_t* entry = p.page_table + b * p.table_stride + at;
+        int page;
+        if (at < held) {
+            page = *entry;
+        } else {
+            page = p.free_pages[n_free - 1 - (s.first + (at - held))];
+            if ((position & (p.page_size - 1)) == 0) *entry = page;
+        }
+        page = page_or_absent(page, p.n_pages);
+        if (page >= 0) slot = (static_cast<int64_t>(page) << a.page_shift) + (position & (p.page_size - 1));
+    }
+    p.slots[t] = slot;
+}
+
+// The sequence of token t: the last whose new tokens begin at t or before (those
+// without new tokens end where the next begins).  lo .. hi bound it.
+__device__ __forceinline__ int sequence_of(const int32_t* cu, int t, int lo, int hi) {
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cu[mid] <= t)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
+template <bool TOKENS>
+__global__ __launch_bounds__(kPageThreads) void extend_scan_kernel(PagesArgs a) {
+    __shared__ int64_t waves[kPageWaves];
+    __shared__ int refused;
+    const auto& p = a.p;
+    Sequence* seqs = static_cast<Sequence*>(p.workspace);
+    if (threadIdx.x == 0) refused = 0;
+    const int n_free = min(max(p.n_free[0], 0), p.n_pages);
+    Scanned upto{0, 0, 0, 0};
+    for (int base = 0; base < p.batch; base += kPageThreads) {
+        const int b = base + threadIdx.x;
+        const bool there = b < p.batch;
+        const int64_t old = there ? max(p.seq_lens[b], 0) : 0, fresh = there ? max(p.n_new[b], 0) : 0;
+        const int64_t held = (old + p.page_size - 1) >> a.page_shift, wanted = (old + fresh + p.page_size - 1) >> a.page_shift;
+        const int64_t need = wanted - held;
+        int64_t total;
+        const int64_t needed = upto.need + block_sum_up_to(need, waves, &total);
+        upto.need += total;
+        const int64_t end = upto.fresh + block_sum_up_to(fresh, waves, &total);
+        upto.fresh += total;
+        const bool granted = fresh == 0 || (needed <= n_free && wanted <= p.max_pages && end <= p.capacity);
+        // Pages are taken by their place among those of all sequences, served or
+        // not: the pages of one that is refused for its own sake stay unused in
+        // the list only if none behind it are taken, so places are counted again
+        // over what is granted.
+        const int64_t mine = granted ? need : 0;
+        const int64_t given = upto.granted + block_sum_up_to(mine, waves, &total);
+        upto.granted += total;
+        const int64_t len = granted ? old + fresh : old;
+        const int64_t all = upto.all + block_sum_up_to(len, waves, &total);
+        upto.all += total;
+        if (there) {
+            seqs[b] = Sequence{static_cast<int32_t>(old), granted ? static_cast<int32_t>(given - mine) : -1};
+            p.new_lens[b] = clamp32(len);
+            p.cu_q[b + 1] = clamp32(end);
+            p.cu_k[b + 1] = clamp32(all);
+            if (!granted) atomicAdd(&refused, 1);
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        p.cu_q[0] = p.cu_k[0] = 0;
+        p.refused[0] = refused;
+        p.n_free_out[0] = n_free - static_cast<int>(upto.granted);
+        if (!TOKENS) reinterpret_cast<int32_t*>(seqs + p.batch)[0] = n_free;
+    }
+    if (TOKENS) {
+        __threadfence_block();
+        __syncthreads();
+        for (int t = threadIdx.x; t < p.capacity; t += kPageThreads) {
+            if (t >= upto.fresh) {
+                p.slots[t] = -1;
+                p.positions[t] = 0;
+            } else {
+                const int b = sequence_of(p.cu_q, t, 0, p.batch - 1);
+                place_token(a, seqs[b], n_free, b, t, p.cu_q[b]);
+            }
+        }
+    }
+}
+
+__global__ __launch_bounds__(kSpreadThreads) void extend_tokens_kernel(PagesArgs a) {
+    const auto& p = a.p;
+    const Sequence* seqs = static_cast<const Sequence*>(p.workspace);
+    const int n_free = reinterpret_cast<const int32_t*>(seqs + p.batch)[0];
+    const int t = blockIdx.x * kSpreadThreads + threadIdx.x;
+    if (t >= p.capacity) return;
+    if (p.batch == 0 || t >= p.cu_q[p.batch]) {
+        p.slots[t] = -1;
+        p.positions[t] = 0;
+        return;
+    }
+    const int b = sequence_of(p.cu_q, t, 0, p.batch - 1);
+    place_token(a, seqs[b], n_free, b, t, p.cu_q[b]);
+}
+
+// One workgroup.  Of every 1024 sequences the finished ones are listed, in order;
+// then a wave takes one at a time, in two rounds for every kPageWaves of them:
+// how many of its entries name a page, then where they go.
+__global__ __launch_bounds__(kPageThreads) void release_kernel(int32_t* table, int64_t stride, int32_t* lens, const uint8_t* finished,
+                                                               int batch, int max_pages, int page_shift, int32_t* free_pages,
+                                                               int32_t* n_free, int n_pages) {
+    __shared__ int list[kPageThreads], listed_of[kPageWaves], counts[2][kPageWaves];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int64_t listed = min(max(n_free[0], 0), n_pages);
+    for (int base = 0; base < batch; base += kPageThreads) {
+        const int mine = base + threadIdx.x;
+        const uint64_t over = __ballot(mine < batch && finished[min(mine, batch - 1)] != 0);
+        if (lane == 0) listed_of[wave] = __popcll(over);
+        __syncthreads();
+        int before = 0, all = 0;
+        for (int w = 0; w < kPageWaves; ++w) {
+            before += w < wave ? listed_of[w] : 0;
+            all += listed_of[w];
+        }
+        if (over >> lane & 1) list[before + __popcll(over & ((uint64_t{1} << lane) - 1))] = mine;
+        __syncthreads();
+        for (int first = 0, turn = 0; first < all; first += kPageWaves, turn ^= 1) {
+            const bool done = first + wave < all;
+            const int b = done ? list[first + wave] : 0;
+            const int64_t len = done ? max(lens[b], 0) : 0;
+            const int held = static_cast<int>(min((len + (int64_t{1} << page_shift) - 1) >> page_shift, static_cast<int64_t>(max_pages)));
+            int32_t* row = table + static_cast<int64_t>(b) * stride;
+            int count = 0;
+            for (int i = 0; i < held; i += kWave)
+                count += __popcll(__ballot(i + lane < held && page_or_absent(row[min(i + lane, held - 1)], n_pages) >= 0));
+            if (lane == 0) counts[turn][wave] = count;
+            __syncthreads();
+            int64_t to = listed;
+            for (int w = 0; w < kPageWaves; ++w) {
+                to += w < wave ? counts[turn][w] : 0;
+                listed += counts[turn][w];
+            }
+            for (int i = 0; i < held; i += kWave) {
+                const int page = i + lane < held ? page_or_absent(row[i + lane], n_pages) : -1;
+                const uint64_t there = __ballot(page >= 0);
+                const int64_t at = to + __popcll(there & ((uint64_t{1} << lane) - 1));
+                if (page >= 0 && at < n_pages) free_pages[at] = page;
+                if (i + lane < held) row[i + lane] = -1;
+                to += __popcll(there);
+            }
+            if (done && lane == 0) lens[b] = 0;
+        }
+        __syncthreads();                                      // the list has been read
+    }
+    if (threadIdx.x == 0) n_free[0] = static_cast<int32_t>(min(listed, static_cast<int64_t>(n_pages)));
+}
+
+bool valid_pages(int batch, int max_pages, int64_t table_stride, int page_size, int n_pages) {
+    if (batch < 0 || batch > kMaxBatch || max_pages < 1 || max_pages > (1 << 24)) return false;
+    if (table_stride < max_pages || table_stride > kMaxStride || n_pages < 1 || n_pages > (1 << 24)) return false;
+    return page_size == 16 || page_size == 32 || page_size == 64 || page_size == 128 || page_size == 256;
+}
+
+size_t table_bytes(int batch, int max_pages, int64_t stride) {
+    return batch == 0 ? 0 : static_cast<size_t>((batch - 1) * stride + max_pages) * 4;
+}
+
+}  // namespace
+}  // namespace grinqh
+
+using namespace grinqh;
+
+extern "C" {
+
+size_t grinqh_kv_extend_workspace_bytes(int32_t batch) {
+    if (batch < 0 || batch > kMaxBatch) return 0;
+    return static_cast<size_t>(batch) * sizeof(Sequence) + 16;
+}
+
+grinqh_status grinqh_kv_extend(const grinqh_extend_args* args, void* stream) {
+    if (args == nullptr) return GRINQH_EINVAL;
+    const grinqh_extend_args& p = *args;
+    if (!valid_pages(p.batch, p.max_pages, p.table_stride, p.page_size, p.n_pages)) return GRINQH_EINVAL;
+    if (p.capacity < 0 || p.capacity > kMaxPacked) return GRINQH_EINVAL;
+    if (p.n_free == nullptr || p.n_free_out == nullptr || p.refused == nullptr || p.cu_q == nullptr || p.cu_k == nullptr ||
+        p.free_pages == nullptr || p.workspace == nullptr)
+        return GRINQH_EINVAL;
+    if (p.batch > 0 && (p.page_table == nullptr || p.seq_lens == nullptr || p.n_new == nullptr || p.new_lens == nullptr))
+        return GRINQH_EINVAL;
+    if (p.capacity > 0 && (p.slots == nullptr || p.positions == nullptr)) return GRINQH_EINVAL;
+    for (const void* at : {static_cast<const void*>(p.page_table), static_cast<const void*>(p.seq_lens), static_cast<const void*>(p.n_new),
+                           static_cast<const void*>(p.free_pages), static_cast<const void*>(p.n_free), static_cast<const void*>(p.new_lens),
+                           static_cast<const void*>(p.n_free_out), static_cast<const void*>(p.refused), static_cast<const void*>(p.cu_q),
+                           static_cast<const void*>(p.cu_k), static_cast<const void*>(p.positions)})
+        if (!aligned_to(at, 4)) return GRINQH_EALIGN;
+    if (!aligned_to(p.slots, 8) || !aligned_to(p.workspace, 16)) return GRINQH_EALIGN;
+    const size_t ws = grinqh_kv_extend_workspace_bytes(p.batch);
+    if (p.workspace_bytes < ws) return GRINQH_ENOSPACE;
+    const size_t batch = static_cast<size_t>(p.batch) * 4, ends = batch + 4, room = static_cast<size_t>(p.capacity);
+    const bool lens_same = p.new_lens == p.seq_lens, free_same = p.n_free_out == p.n_free;
+    if (written_overlaps({{p.page_table, table_bytes(p.batch, p.max_pages, p.table_stride)}, {p.new_lens, batch}, {p.n_free_out, 4},
+                          {p.refused, 4}, {p.cu_q, ends}, {p.cu_k, ends}, {p.slots, room * 8}, {p.positions, room * 4}, {p.workspace, ws}},
+                         {{p.n_new, batch}, {p.free_pages, static_cast<size_t>(p.n_pages) * 4},
+                          {p.seq_lens, lens_same ? 0 : batch}, {p.n_free, free_same ? size_t{0} : size_t{4}}}))
+        return GRINQH_EINVAL;
+    const PagesArgs a{p, log2_of(p.page_size)};
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    if (p.capacity <= kOneLaunch) return launch_kernel(extend_scan_kernel<true>, dim3(1), kPageThreads, 0, st, a);
+    const grinqh_status status = launch_kernel(extend_scan_kernel<false>, dim3(1), kPageThreads, 0, st, a);
+    if (status != GRINQH_OK) return status;
+    return launch_kernel(extend_tokens_kernel, dim3((p.capacity + kSpreadThreads - 1) / kSpreadThreads), kSpreadThreads, 0, st, a);
+}
+
+grinqh_status grinqh_kv_release(int32_t* page_table, int64_t table_stride, int32_t* seq_lens,
+                                const uint8_t* finished, int32_t batch, int32_t max_pages, int32_t page_size,
+                                int32_t* free_pages, int32_t* n_free, int32_t n_pages, void* stream) {
+    if (!valid_pages(batch, max_pages, table_stride, page_size, n_pages)) return GRINQH_EINVAL;
+    if (batch == 0) return GRINQH_OK;
+    if (page_table == nullptr || seq_lens == nullptr || finished == nullptr || free_pages == nullptr || n_free == nullptr)
+        return GRINQH_EINVAL;
+    if (!aligned_to(page_table, 4) || !aligned_to(seq_lens, 4) || !aligned_to(free_pages, 4) || !aligned_to(n_free, 4))
+        return GRINQH_EALIGN;
+    const size_t n = static_cast<size_t>(batch);
+    if (written_overlaps({{page_table, table_bytes(batch, max_pages, table_stride)}, {seq_lens, n * 4},
+                          {free_pages, static_cast<size_t>(n_pages) * 4}, {n_free, 4}}, {{finished, n}}))
+        return GRINQH_EINVAL;
+    return launch_kernel(release_kernel, dim3(1), kPageThreads, 0, static_cast<hipStream_t>(stream), page_table, table_stride,
+                         seq_lens, finished, static_cast<int>(batch), static_cast<int>(max_pages), log2_of(page_size), free_pages,
+                         n_free, static_cast<int>(n_pages));
+}
+
+}  // extern "C"

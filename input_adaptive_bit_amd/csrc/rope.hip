@@ -1,0 +1,336 @@
+// Norms of queries and keys for each head, the rotation by position, and the
+// cache's write, in one pass over the rows.
+//
+//   x <- x * weight / sqrt(mean(x^2) + eps)
+//   (a, b) <- (a cos t - b sin t, b cos t + a sin t),  t = position * freq
+//
+// D / 8 neighbouring lanes hold a row, 8 values each (one 16-byte load of bf16,
+// two of fp32): the mean comes from exchanges between them, the other half of a
+// rotated pair from the lane that holds it, and a row of the cache is quantised
+// from the same registers (kv_store.hpp).  Angles are the same for all heads of a
+// token, so such a group of lanes stays with one token and takes several of its
+// rows.  An angle's turns are counted in fp64 and only the fraction of a turn is
+// rounded to fp32 (at position 10^5 a 32-bit product would be off by 0.01
+// radian); sine and cosine are of that fraction.
+#include <algorithm>
+
+#include "internal.h"
+#include "kv_common.hpp"
+#include "kv_store.hpp"
+
+namespace grinqh {
+namespace {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kRopeThreads = 256;
+constexpr int kMaxRopeGroups = 1 << 20;            // workgroups; more items than they hold go round again
+
+struct RopeArgs {
+    KvDims d;
+    const void* src[3];                            // queries, keys, values
+    int64_t src_stride[3];
+    void* dst[2];
+    int64_t dst_stride[2];
+    uint8_t* codes[2];
+    uint16_t* grid[2];
+    const int64_t* slots;
+    const int32_t* positions;
+    const double* freqs;
+    const void* weight[2];
+    int64_t n_tokens;
+    int n_q, n_kv, rows, parts;                    // rows of a token, and how many lane groups share them
+    int rope_dim, neighbours, weight_dtype;
+    float eps;
+};
+
+template <typename T>
+struct RawRow {
+    u32x4 v[sizeof(T) / 2];
+};
+
+template <typename T>
+__device__ __forceinline__ void widen(const RawRow<T>& raw, float (&w)[kPerLane]) {
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[2 * i] = __uint_as_float(raw.v[0][i] << 16);
+            w[2 * i + 1] = __uint_as_float(raw.v[0][i] & 0xFFFF0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = __uint_as_float(raw.v[i >> 2][i & 3]);
+    }
+}
+
+// Rounds to T (a choice of the caller's: the type of queries and keys), and
+// leaves in w what that stands for.
+template <typename T>
+__device__ __forceinline__ RawRow<T> narrow(float (&w)[kPerLane]) {
+    RawRow<T> raw;
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            raw.v[0][i] = f32_to_bf16(w[2 * i]) | static_cast<uint32_t>(f32_to_bf16(w[2 * i + 1])) << 16;
+        widen<T>(raw, w);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) raw.v[i >> 2][i & 3] = __float_as_uint(w[i]);
+    }
+    return raw;
+}
+
+template <int D, typename T, int BITS>
+__global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a) {
+    constexpr int kLanes = D / kPerLane, kItems = kRopeThreads / kLanes;
+    const int lane = threadIdx.x % kLanes;
+    const int64_t items = a.n_tokens * a.parts, step = static_cast<int64_t>(gridDim.x) * kItems;
+    // Where the other half of this lane's pairs is, and its sign.
+    const int across = a.rope_dim / (2 * kPerLane);
+    const bool turned = lane * kPerLane < a.rope_dim, second = lane >= across;
+    const int partner = !turned || a.neighbours ? lane : second ? lane - across : lane + across;
+    const float sign = second ? 1.f : -1.f;
+
+    for (int64_t item = static_cast<int64_t>(blockIdx.x) * kItems + threadIdx.x / kLanes; item < items; item += step) {
+        const int64_t token = item / a.parts;
+        const int part = static_cast<int>(item - token * a.parts);
+        const auto row_of = [&](int r, int which, int first) {
+            return static_cast<const T*>(a.src[which]) + token * a.src_stride[which] + (r - first) * D + lane * kPerLane;
+        };
+        const auto load = [&](int r) {
+            const T* p = r < a.n_q ? row_of(r, 0, 0) : r < a.n_q + a.n_kv ? row_of(r, 1, a.n_q) : row_of(r, 2, a.n_q + a.n_kv);
+            RawRow<T> raw;
+#pragma unroll
+            for (unsigned i = 0; i < sizeof(T) / 2; ++i) raw.v[i] = reinterpret_cast<const u32x4*>(p)[i];
+            return raw;
+        };
+        RawRow<T> next = load(part);
+        float cs[kPerLane], sn[kPerLane];
+        if (turned) {
+            const double position = a.positions[token];
+            const double* freq = a.freqs + (a.neighbours ? lane * (kPerLane / 2) : (second ? lane - across : lane) * kPerLane);
+#pragma unroll
+            for (int i = 0; i < kPerLane; ++i) {
+                if (i >= kPerLane / 2 && a.neighbours) break;
+                const double turns = position * freq[i] * 0.15915494309189533577;          // 1 / (2 pi)
+                sincospif(static_cast<float>(2.0 * (turns - rint(turns))), &sn[i], &cs[i]);
+            }
+        }
+        const int64_t slot = BITS == 0 ? 0 : a.slots[token];
+
+        for (int r = part; r < a.rows; r += a.parts) {
+            RawRow<T> raw = next;
+            if (r + a.parts < a.rows) next = load(r + a.parts);
+            const bool is_q = r < a.n_q, is_v = r >= a.n_q + a.n_kv;
+            float w[kPerLane];
+            widen<T>(raw, w);
+            if (!is_v) {
+                const void* weight = a.weight[is_q ? 0 : 1];
+                if (weight != nullptr) {
+                    float sum = 0.f;
+#pragma unroll
+                    for (int i = 0; i < kPerLane; ++i) sum = __builtin_fmaf(w[i], w[i], sum);
+#pragma unroll
+                    for (int m = 1; m < kLanes; m <<= 1) sum += __shfl_xor(sum, m, kLanes);
+                    const float scale = 1.f / sqrtf(sum * (1.f / D) + a.eps);
+                    float g[kPerLane];
+                    if (a.weight_dtype == GRINQH_BF16) {
+                        RawRow<uint16_t> raw_g;
+                        raw_g.v[0] = reinterpret_cast<const u32x4*>(weight)[lane];
+                        widen<uint16_t>(raw_g, g);
+                    } else {
+                        RawRow<float> raw_g;
+                        raw_g.v[0] = reinterpret_cast<const u32x4*>(weight)[2 * lane];
+                        raw_g.v[1] = reinterpret_cast<const u32x4*>(weight)[2 * lane + 1];
+                        widen<float>(raw_g, g);
+                    }
+#pragma unroll
+                    for (int i = 0; i < kPerLane; ++i) w[i] = w[i] * scale * g[i];
+                }
+                if (a.neighbours) {
+                    if (turned) {
+#pragma unroll
+                        for (int i = 0; i < kPerLane; i += 2) {
+                            const float x = w[i], y = w[i + 1], c = cs[i / 2], s = sn[i / 2];
+                            w[i] = __builtin_fmaf(x, c, -(y * s));
+                            w[i + 1] = __builtin_fmaf(y, c, x * s);
+                        }
+                    }
+                } else {
+                    float other[kPerLane];
+#pragma unroll
+                    for (int i = 0; i < kPerLane; ++i) other[i] = __shfl(w[i], partner, kLanes);
+                    if (turned) {
+#pragma unroll
+                        for (int i = 0; i < kPerLane; ++i) w[i] = __builtin_fmaf(w[i], cs[i], sign * (other[i] * sn[i]));
+                    }
+                }
+                raw = narrow<T>(w);
+                T* to = static_cast<T*>(a.dst[is_q ? 0 : 1]);
+                if (to != nullptr) {
+                    to += token * a.dst_stride[is_q ? 0 : 1] + (is_q ? r : r - a.n_q) * D + lane * kPerLane;
+#pragma unroll
+                    for (unsigned i = 0; i < sizeof(T) / 2; ++i) reinterpret_cast<u32x4*>(to)[i] = raw.v[i];
+                }
+            }
+            if constexpr (BITS != 0) {
+                if (is_q) continue;
+                const int which = is_v ? 1 : 0;
+                const int64_t row = kv_row(a.d, slot, r - a.n_q - which * a.n_kv);
+                if (row < 0) continue;
+                if constexpr (BITS == 16) {
+                    if constexpr (sizeof(T) == 4) {
+                        const RawRow<uint16_t> kept = narrow<uint16_t>(w);
+                        *reinterpret_cast<u32x4*>(a.codes[which] + row * (D * 2) + lane * 16) = kept.v[0];
+                    } else {
+                        *reinterpret_cast<u32x4*>(a.codes[which] + row * (D * 2) + lane * 16) = raw.v[0];
+                    }
+                } else {
+                    store_quantised_row<D, BITS>(w, a.codes[which], a.grid[which], row, lane);
+                }
+            }
+        }
+    }
+}
+
+template <int D, typename T, int BITS>
+grinqh_status rope_launch(RopeArgs& a, hipStream_t stream) {
+    constexpr int kItems = kRopeThreads / (D / kPerLane);
+    // Few tokens: a group of lanes for every row.  Many: up to eight rows to a
+    // group, as long as there are two thousand workgroups, so that angles are worked out once for them.
+    const int64_t wanted = (int64_t{2048} * kItems + a.n_tokens - 1) / a.n_tokens;
+    a.parts = static_cast<int>(std::min<int64_t>(a.rows, std::max<int64_t>(wanted, (a.rows + 7) / 8)));
+    const int64_t groups = (a.n_tokens * a.parts + kItems - 1) / kItems;
+    return launch_kernel(rope_kernel<D, T, BITS>, dim3(static_cast<unsigned>(std::min<int64_t>(groups, kMaxRopeGroups))),
+                         kRopeThreads, 0, stream, a);
+}
+
+template <int D, typename T>
+grinqh_status rope_bits(RopeArgs& a, int bits, hipStream_t stream) {
+    if (bits == 0) return rope_launch<D, T, 0>(a, stream);
+    if (bits == 4) return rope_launch<D, T, 4>(a, stream);
+    if (bits == 8) return rope_launch<D, T, 8>(a, stream);
+    return rope_launch<D, T, 16>(a, stream);
+}
+
+template <typename T>
+grinqh_status rope_dim(RopeArgs& a, int head_dim, int bits, hipStream_t stream) {
+    if (head_dim == 64) return rope_bits<64, T>(a, bits, stream);
+    if (head_dim == 128) return rope_bits<128, T>(a, bits, stream);
+    return rope_bits<256, T>(a, bits, stream);
+}
+
+bool valid_type(int dtype) { return dtype == GRINQH_BF16 || dtype == GRINQH_F32; }
+
+}  // namespace
+}  // namespace grinqh
+
+using namespace grinqh;
+
+extern "C" {
+
+grinqh_status grinqh_qk_rope(const grinqh_rope_args* p, void* stream) {
+    if (p == nullptr) return GRINQH_EINVAL;
+    const bool cached = p->cache != nullptr;
+    if (cached) {
+        const grinqh_status st = check_kv_pools(p->cache, p->pools);
+        if (st != GRINQH_OK) return st;
+        if (p->cache->n_kv_heads != p->n_kv_heads || p->cache->head_dim != p->head_dim) return GRINQH_EINVAL;
+    }
+    if (!valid_type(p->dtype) || p->n_tokens < 0 || p->n_tokens > kMaxPacked) return GRINQH_EINVAL;
+    if (p->n_q_heads < 1 || p->n_q_heads > kMaxQHeads || p->n_kv_heads < 1 || p->n_kv_heads > kMaxKvHeads) return GRINQH_EINVAL;
+    if (p->head_dim != 64 && p->head_dim != 128 && p->head_dim != 256) return GRINQH_EINVAL;
+    if (p->rope_dim < 0 || p->rope_dim > p->head_dim || p->rope_dim % 16 != 0) return GRINQH_EINVAL;
+    const bool normed = p->q_weight != nullptr || p->k_weight != nullptr;
+    if (normed && (!valid_type(p->weight_dtype) || !(p->eps >= 0.f && p->eps < INFINITY))) return GRINQH_EINVAL;
+    if (p->n_tokens == 0) return GRINQH_OK;
+    if (p->q == nullptr || p->k == nullptr || p->q_out == nullptr || (p->k_out == nullptr && !cached)) return GRINQH_EINVAL;
+    if (p->rope_dim > 0 && (p->positions == nullptr || p->freqs == nullptr)) return GRINQH_EINVAL;
+    if (cached && (p->v == nullptr || p->slots == nullptr)) return GRINQH_EINVAL;
+    const int64_t n = p->n_tokens, eb = p->dtype == GRINQH_BF16 ? 2 : 4;
+    const int64_t q_width = static_cast<int64_t>(p->n_q_heads) * p->head_dim, k_width = static_cast<int64_t>(p->n_kv_heads) * p->head_dim;
+    const auto bad_stride = [](int64_t stride, int64_t width) { return stride < width || stride > kMaxStride; };
+    if (bad_stride(p->q_stride, q_width) || bad_stride(p->k_stride, k_width) || bad_stride(p->q_out_stride, q_width) ||
+        (p->k_out != nullptr && bad_stride(p->k_out_stride, k_width)) || (cached && bad_stride(p->v_stride, k_width)))
+        return GRINQH_EINVAL;
+    const auto off = [&](const void* at, int64_t stride) { return at != nullptr && (!aligned_to(at, 16) || stride * eb % 16 != 0); };
+    if (off(p->q, p->q_stride) || off(p->k, p->k_stride) || off(p->q_out, p->q_out_stride) || off(p->k_out, p->k_out_stride) ||
+        (cached && off(p->v, p->v_stride)) || !aligned_to(p->q_weight, 16) || !aligned_to(p->k_weight, 16) ||
+        !aligned_to(p->positions, 4) || !aligned_to(p->freqs, 8) || (cached && !aligned_to(p->slots, 8)))
+        return GRINQH_EALIGN;
+    const auto rows = [&](int64_t stride, int64_t width) { return static_cast<size_t>(((n - 1) * stride + width) * eb); };
+    const size_t q_bytes = rows(p->q_stride, q_width), k_bytes = rows(p->k_stride, k_width);
+    const size_t weight_bytes = p->head_dim * (p->weight_dtype == GRINQH_BF16 ? 2u : 4u);
+    const size_t code_bytes = cached ? grinqh_kv_code_bytes(p->cache) : 0, grid_bytes = cached ? grinqh_kv_grid_bytes(p->cache) : 0;
+    const grinqh_kv_pools none{nullptr, nullptr, nullptr, nullptr};
+    const grinqh_kv_pools& pools = cached ? *p->pools : none;
+    const Span q_out{p->q_out, rows(p->q_out_stride, q_width)};
+    const Span k_out{p->k_out, p->k_out == nullptr ? 0 : rows(p->k_out_stride, k_width)};
+    // an output may be its input itself
+    const bool q_same = p->q_out == p->q && p->q_out_stride == p->q_stride, k_same = p->k_out == p->k && p->k_out_stride == p->k_stride;
+    const Span more[] = {{p->v, cached ? rows(p->v_stride, k_width) : 0},
+                         {p->slots, cached ? static_cast<size_t>(n) * 8 : 0},
+                         {p->positions, p->rope_dim > 0 ? static_cast<size_t>(n) * 4 : 0},
+                         {p->freqs, static_cast<size_t>(p->rope_dim) * 4},
+                         {p->q_weight, p->q_weight == nullptr ? 0 : weight_bytes},
+                         {p->k_weight, p->k_weight == nullptr ? 0 : weight_bytes}};
+    // Rows of one fused projection lie between one another: what is shared there is
+    // a stretch of memory, not a value, so an output that is its input is held
+    // against the other inputs row by row.
+    const auto apart = [&](const void* out, int64_t out_stride, int64_t out_width, const void* in, int64_t in_stride, int64_t in_width) {
+        const uintptr_t o = reinterpret_cast<uintptr_t>(out), i = reinterpret_cast<uintptr_t>(in);
+        if (!overlaps(out, rows(out_stride, out_width), in, rows(in_stride, in_width))) return true;
+        if (out_stride != in_stride) return false;
+        const int64_t period = out_stride * eb, gap = static_cast<int64_t>(i - o), at = ((gap % period) + period) % period;
+        return at >= out_width * eb && at + in_width * eb <= period;                // the same place between two tokens' rows
+    };
+    if (!q_same && !apart(p->q_out, p->q_out_stride, q_width, p->q, p->q_stride, q_width)) return GRINQH_EINVAL;
+    if (!apart(p->q_out, p->q_out_stride, q_width, p->k, p->k_stride, k_width)) return GRINQH_EINVAL;
+    if (cached && !apart(p->q_out, p->q_out_stride, q_width, p->v, p->v_stride, k_width)) return GRINQH_EINVAL;
+    if (p->k_out != nullptr) {
+        if (!apart(p->k_out, p->k_out_stride, k_width, p->q, p->q_stride, q_width)) return GRINQH_EINVAL;
+        if (!k_same && !apart(p->k_out, p->k_out_stride, k_width, p->k, p->k_stride, k_width)) return GRINQH_EINVAL;
+        if (cached && !apart(p->k_out, p->k_out_stride, k_width, p->v, p->v_stride, k_width)) return GRINQH_EINVAL;
+        if (!apart(p->k_out, p->k_out_stride, k_width, p->q_out, p->q_out_stride, q_width)) return GRINQH_EINVAL;
+    }
+    for (int i = 1; i < 6; ++i)                                                     // the values were held against the outputs above
+        if (overlaps(q_out.at, q_out.bytes, more[i].at, more[i].bytes) || overlaps(k_out.at, k_out.bytes, more[i].at, more[i].bytes))
+            return GRINQH_EINVAL;
+    if (cached && written_overlaps({{pools.k_codes, code_bytes}, {pools.v_codes, code_bytes}, {pools.k_grid, grid_bytes}, {pools.v_grid, grid_bytes}},
+                                   {q_out, k_out, {p->q, q_bytes}, {p->k, k_bytes}, more[0], more[1], more[2], more[3], more[4], more[5]}))
+        return GRINQH_EINVAL;
+    RopeArgs a{};
+    if (cached) a.d = kv_dims(*p->cache);
+    a.src[0] = p->q;
+    a.src[1] = p->k;
+    a.src[2] = p->v;
+    a.src_stride[0] = p->q_stride;
+    a.src_stride[1] = p->k_stride;
+    a.src_stride[2] = p->v_stride;
+    a.dst[0] = p->q_out;
+    a.dst[1] = p->k_out;
+    a.dst_stride[0] = p->q_out_stride;
+    a.dst_stride[1] = p->k_out_stride;
+    a.codes[0] = pools.k_codes;
+    a.codes[1] = pools.v_codes;
+    a.grid[0] = pools.k_grid;
+    a.grid[1] = pools.v_grid;
+    a.slots = p->slots;
+    a.positions = p->positions;
+    a.freqs = p->freqs;
+    a.weight[0] = p->q_weight;
+    a.weight[1] = p->k_weight;
+    a.n_tokens = n;
+    a.n_q = p->n_q_heads;
+    a.n_kv = p->n_kv_heads;
+    a.rows = p->n_q_heads + p->n_kv_heads * (cached ? 2 : 1);
+    a.rope_dim = p->rope_dim;
+    a.neighbours = p->neighbours != 0;
+    a.weight_dtype = p->weight_dtype;
+    a.eps = p->eps;
+    const int bits = cached ? p->cache->bits : 0;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    return p->dtype == GRINQH_BF16 ? rope_dim<uint16_t>(a, p->head_dim, bits, st) : rope_dim<float>(a, p->head_dim, bits, st);
+}
+
+}  // extern "C"

@@ -67,6 +67,43 @@ class PrefillAttentionArgs(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_size_t)]
 
 
+class FourbitLayout(ctypes.Structure):
+    """Shape of 4-bit weights with group scales (grinqh_fourbit_layout_init)."""
+    _fields_ = [("d_in", ctypes.c_int32), ("d_out", ctypes.c_int32), ("group", ctypes.c_int32),
+                ("n_experts", ctypes.c_int32), ("k_tiles", ctypes.c_int32), ("row_tiles", ctypes.c_int32)]
+
+    def __repr__(self):
+        return f"FourbitLayout(d_in={self.d_in}, d_out={self.d_out}, group={self.group}, n_experts={self.n_experts})"
+
+
+class ExpertArgs(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64), ("x_dtype", ctypes.c_int), ("n_x", ctypes.c_int32),
+                ("rows", ctypes.c_void_p), ("ends", ctypes.c_void_p), ("n_rows", ctypes.c_int32),
+                ("codes", ctypes.c_void_p), ("grid", ctypes.c_void_p), ("y", ctypes.c_void_p), ("y_dtype", ctypes.c_int)]
+
+
+class RopeArgs(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("n_tokens", ctypes.c_int32), ("n_q_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p), ("weight_dtype", ctypes.c_int), ("eps", ctypes.c_float),
+                ("positions", ctypes.c_void_p), ("freqs", ctypes.c_void_p), ("rope_dim", ctypes.c_int32),
+                ("neighbours", ctypes.c_int32), ("q_out", ctypes.c_void_p), ("k_out", ctypes.c_void_p),
+                ("q_out_stride", ctypes.c_int64), ("k_out_stride", ctypes.c_int64),
+                ("cache", ctypes.POINTER(KVLayout)), ("pools", ctypes.POINTER(KVPools)), ("slots", ctypes.c_void_p)]
+
+
+class ExtendArgs(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("seq_lens", ctypes.c_void_p),
+                ("n_new", ctypes.c_void_p), ("free_pages", ctypes.c_void_p), ("n_free", ctypes.c_void_p),
+                ("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("capacity", ctypes.c_int32), ("new_lens", ctypes.c_void_p),
+                ("n_free_out", ctypes.c_void_p), ("refused", ctypes.c_void_p), ("cu_q", ctypes.c_void_p),
+                ("cu_k", ctypes.c_void_p), ("slots", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
 MAX_GROUP = 8
 
 EXPORTS = ("grinqh_version", "grinqh_status_string", "grinqh_layout_init", "grinqh_packed_bytes",
@@ -77,7 +114,10 @@ EXPORTS = ("grinqh_version", "grinqh_status_string", "grinqh_layout_init", "grin
            "grinqh_prefill_workspace_bytes", "grinqh_prefill_gemm",
            "grinqh_kv_layout_init", "grinqh_kv_code_bytes", "grinqh_kv_grid_bytes", "grinqh_kv_write",
            "grinqh_kv_read", "grinqh_debug_kv_row", "grinqh_debug_page_row", "grinqh_attention_workspace_bytes",
-           "grinqh_decode_attention", "grinqh_prefill_attention", "grinqh_prefill_attention_workspace_bytes")
+           "grinqh_decode_attention", "grinqh_prefill_attention", "grinqh_prefill_attention_workspace_bytes",
+           "grinqh_fourbit_layout_init", "grinqh_fourbit_code_bytes", "grinqh_fourbit_grid_bytes", "grinqh_fourbit_pack",
+           "grinqh_fourbit_linear", "grinqh_expert_linear", "grinqh_qk_rope", "grinqh_kv_extend_workspace_bytes",
+           "grinqh_kv_extend", "grinqh_kv_release")
 
 _lib = None
 
@@ -162,6 +202,27 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.grinqh_prefill_attention.restype = ctypes.c_int
     lib.grinqh_prefill_attention_workspace_bytes.argtypes = [ctypes.POINTER(PrefillAttentionArgs)]
     lib.grinqh_prefill_attention_workspace_bytes.restype = sz
+    FP = ctypes.POINTER(FourbitLayout)
+    lib.grinqh_fourbit_layout_init.argtypes = [i32, i32, i32, i32, FP]
+    lib.grinqh_fourbit_layout_init.restype = ctypes.c_int
+    lib.grinqh_fourbit_code_bytes.argtypes = [FP]
+    lib.grinqh_fourbit_code_bytes.restype = sz
+    lib.grinqh_fourbit_grid_bytes.argtypes = [FP]
+    lib.grinqh_fourbit_grid_bytes.restype = sz
+    lib.grinqh_fourbit_pack.argtypes = [FP, vp, vp, vp, vp, vp, vp]
+    lib.grinqh_fourbit_pack.restype = ctypes.c_int
+    lib.grinqh_fourbit_linear.argtypes = [FP, vp, ctypes.c_int, i64, i32, vp, vp, vp, ctypes.c_int, vp]
+    lib.grinqh_fourbit_linear.restype = ctypes.c_int
+    lib.grinqh_expert_linear.argtypes = [FP, ctypes.POINTER(ExpertArgs), vp]
+    lib.grinqh_expert_linear.restype = ctypes.c_int
+    lib.grinqh_qk_rope.argtypes = [ctypes.POINTER(RopeArgs), vp]
+    lib.grinqh_qk_rope.restype = ctypes.c_int
+    lib.grinqh_kv_extend_workspace_bytes.argtypes = [i32]
+    lib.grinqh_kv_extend_workspace_bytes.restype = sz
+    lib.grinqh_kv_extend.argtypes = [ctypes.POINTER(ExtendArgs), vp]
+    lib.grinqh_kv_extend.restype = ctypes.c_int
+    lib.grinqh_kv_release.argtypes = [vp, i64, vp, vp, i32, i32, i32, vp, vp, i32, vp]
+    lib.grinqh_kv_release.restype = ctypes.c_int
     if path is None:
         _lib = lib
     return lib
