@@ -34,10 +34,17 @@ struct FourbitArgs {
 // Eight codes (one word of a tile) as the bf16 values 16 + q, in the order of the
 // inputs: between 16 and 32 a bf16 steps by 1/8, so a code's four bits, put at
 // bit 3, add q to 16 exactly.  Seven instructions for eight codes.
-__device__ __forceinline__ bf16x8 codes_to_bf16(uint32_t w) {
-    constexpr uint32_t kMask = 0x00780078u, kSixteen = 0x41804180u;
-    const u32x4 v{(w & kMask) | kSixteen, ((w >> 4) & kMask) | kSixteen, ((w >> 8) & kMask) | kSixteen,
-                  (__builtin_amdgcn_alignbit(w, w, 12) & kMask) | kSixteen};
+// (seven, if the constants are in registers: 16 in a vector register, which the
+// compiler has to be kept from folding, and the mask in a scalar one.)
+__device__ __forceinline__ uint32_t bf16_sixteens() {
+    uint32_t v = 0x41804180u;
+    asm("" : "+v"(v));                             // no instruction: one that wrote a register here would need waits of its own
+    return v;
+}
+__device__ __forceinline__ bf16x8 codes_to_bf16(uint32_t w, uint32_t sixteens) {
+    constexpr uint32_t kMask = 0x00780078u;
+    const u32x4 v{(w & kMask) | sixteens, ((w >> 4) & kMask) | sixteens, ((w >> 8) & kMask) | sixteens,
+                  (__builtin_amdgcn_alignbit(w, w, 12) & kMask) | sixteens};
     return __builtin_bit_cast(bf16x8, v);
 }
 constexpr float kCodeBias = 15.5f;                 // 16 + q - kCodeBias = q + 1/2
@@ -91,6 +98,33 @@ __device__ __forceinline__ int source_row(const FourbitArgs& a, int r) {
     return static_cast<unsigned>(s) < static_cast<unsigned>(a.n_x) ? s : -1;
 }
 
+// 16 (4) bytes per lane from memory straight into LDS, lane after lane from `lds`
+// (uniform).  Written out because the compiler, not knowing which buffer an LDS
+// read is from, would wait for every such load before it; the kernels wait for
+// them themselves.
+__device__ __forceinline__ void load_to_lds(const void* from, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 1\n\tglobal_load_lds_dwordx4 %1, off"
+                 :
+                 : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(from)
+                 : "memory", "m0");
+}
+__device__ __forceinline__ void load_word_to_lds(const void* from, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 1\n\tglobal_load_lds_dword %1, off"
+                 :
+                 : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(from)
+                 : "memory", "m0");
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char*)p));
+}
+
+// Chunk c (16 bytes) of row r of 128 bf16 lies at c ^ (r & 15): the 16 rows of an
+// operand's read fall on different banks.
+__device__ __forceinline__ int chunk_at(int r, int c) { return r * 256 + ((c ^ (r & 15)) * 16); }
+
 bool valid_fourbit_layout(const grinqh_fourbit_layout* L);
+
+// The kernel for many rows (fourbit_tile.hip; bf16 activations), in tiles of 64 or 128.
+grinqh_status launch_fourbit_tile(const FourbitArgs& a, int group, int rows, hipStream_t stream);
 
 }  // namespace grinqh

@@ -1,23 +1,23 @@
 // Products of few rows with 4-bit weights: the weights are streamed once, on
-// the matrix cores.
+// the matrix cores.  Here too: the host's checks, and which kernel a call takes.
 //
-//   y[t][j] = sum_g s_jg * (A_tjg - 15.5 S_tg) + z_jg * S_tg,
+//   y[t][j] = sum_g s_jg * A_tjg + (z_jg - 15.5 s_jg) * S_tg,
 //   A_tjg = sum_{i in g} x_ti (16 + q_ji),   S_tg = sum_{i in g} x_ti.
 //
-// A workgroup makes 16 R outputs of up to 16 NB rows; its waves take the tiles of
-// 128 inputs in turn and add their sums up through LDS, so nothing is split
-// across workgroups, nothing needs a workspace, and the order of the sums is
-// fixed.  A wave loads a tile of 16 x 128 codes with one 16-byte load a lane,
-// straight in the matrix operand's order, and makes eight bf16 values 16 + q of a
-// word in seven instructions (codes_to_bf16); products of those with bf16
-// activations are exact.  With the weights as the first operand a lane holds four
-// outputs of one row (16x16x32 MFMA), and S comes from the same instruction with
-// a first operand of ones, in the same place.  Scales and zero points: each lane
-// loads one pair of the tile's (up to four groups x four outputs a quad of lanes),
-// and a broadcast within the 16 lanes of a row (DPP) hands them out.
+// A workgroup makes 16 R outputs of some rows; its waves take the tiles of 128
+// inputs in turn and add their sums up through LDS, so nothing is split across
+// workgroups, nothing needs a workspace, and the order of the sums is fixed.  A
+// tile of 16 x 128 codes is one 16-byte load a lane, straight in the matrix
+// operand's order, and a word of it becomes eight bf16 values 16 + q in seven
+// instructions (codes_to_bf16); products of those with bf16 activations are
+// exact.  With the weights as the first operand a lane holds four outputs of one
+// row (16x16x32 MFMA), and S comes from the same instruction with a first operand
+// of ones, in the same place.  Scales and zero points: each lane has one pair
+// of the tile's (up to four groups x four outputs a quad of lanes), and a broadcast
+// within the 16 lanes of a row (DPP) hands them out.
 //
-// fp32 activations are split into three bf16 (8 + 8 + 8 bits, exact but for
-// what lies below the smallest bf16), which take three neighbouring columns: five rows a pass.
+// fp32 activations are split into three bf16 (8 + 8 + 8 bits, exact but for what
+// lies below the smallest bf16), which take three neighbouring columns: five rows a pass.
 #include <algorithm>
 
 #include "fourbit_common.hpp"
@@ -26,137 +26,97 @@ namespace grinqh {
 namespace {
 
 constexpr int kStreamTilesY = 1 << 15;             // row tiles in a launch's second dimension
-template <bool F32, int NB>
-constexpr int kStreamRows = F32 ? 5 : 16 * NB;     // rows of a workgroup
+constexpr int kDepth = 4;                          // tiles of codes that a wave has under way (and fp32 tiles split at a time)
 
 template <int N>
 __device__ __forceinline__ float row_bcast(float v) {                          // lane N of each 16
     return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x150 + N, 0xF, 0xF, false));
 }
 
-// The PART-th of the three bf16 that add up to x, as the upper half of a word.  Truncation:
-// no part rounds up past the largest float.  What is not finite is all in the first.
-__device__ __forceinline__ uint32_t bf16_part(float x, int part) {
-    const uint32_t hi = __float_as_uint(x) & 0xFFFF0000u;
+// Three bf16 that add up to x, each as the upper half of a word.  Truncation: no
+// part rounds up past the largest float.  What is not finite is all in the first.
+__device__ __forceinline__ void split(float x, uint32_t (&part)[3]) {
+    const uint32_t bits = __float_as_uint(x), hi = bits & 0xFFFF0000u;
     const float rest = x - __uint_as_float(hi);
     const uint32_t mid = __float_as_uint(rest) & 0xFFFF0000u;
-    const uint32_t lo = __float_as_uint(rest - __uint_as_float(mid)) & 0xFFFF0000u;
-    if ((__float_as_uint(x) & 0x7F800000u) == 0x7F800000u)                     // a NaN's bits may all lie in the lower half
-        return part != 0 ? 0u : x != x ? 0x7FC00000u : hi;
-    return part == 0 ? hi : part == 1 ? mid : lo;
+    const bool finite = (bits & 0x7F800000u) != 0x7F800000u;
+    part[0] = x != x ? 0x7FC00000u : hi;                                       // a NaN's bits may all lie in the lower half
+    part[1] = finite ? mid : 0u;
+    part[2] = finite ? __float_as_uint(rest - __uint_as_float(mid)) & 0xFFFF0000u : 0u;
 }
 
-template <bool F32, int R, int NB>
-struct Stage {
+// Codes of a tile of R x 16 outputs, and this lane's (s, z) pair of each.
+template <int R>
+struct Codes {
     u32x4 code[R];
     uint32_t grid[R];
-    u32x4 x[NB][4][F32 ? 2 : 1];
 };
 
-template <int GROUP, bool F32, int R, int NB, int W, int DEPTH>
-__global__ __launch_bounds__(W * kWave) void fourbit_stream_kernel(FourbitArgs a, int vector_store) {
-    constexpr int NG = kTileIn / GROUP, STEPS = 4 / NG;
-    __shared__ f32x4 red[W][R * NB][kWave];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const RunTile run = find_run_tile(a, kStreamRows<F32, NB>, blockIdx.z * kStreamTilesY + blockIdx.y, lane);
-    if (run.count <= 0) return;
-    const int col = lane & 15, quad = lane >> 4;
-    const int tile0 = blockIdx.x * R;
-
-    // This lane's rows of x: a column of every block of 16 (rows past the run's
-    // last take it again; what comes out is not stored).
-    const char* from[NB];
-    bool there[NB];
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        const int t = F32 ? min(col / 3, run.count - 1) : min(16 * b + col, run.count - 1);
-        const int src = source_row(a, run.row + t);
-        there[b] = src >= 0;
-        from[b] = static_cast<const char*>(a.x) + (max(src, 0) * a.x_stride + 8 * quad) * (F32 ? 4 : 2);
-    }
+template <int R>
+struct WeightAt {
     const uint8_t* codes[R];
     const uint16_t* grid[R];
+};
+
+template <int GROUP, int R>
+__device__ __forceinline__ WeightAt<R> weight_at(const FourbitArgs& a, int expert, int tile0, int lane) {
+    constexpr int NG = kTileIn / GROUP;
+    const int col = lane & 15, quad = lane >> 4;
+    WeightAt<R> at;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const int64_t tile = (static_cast<int64_t>(run.expert) * a.row_tiles + min(tile0 + r, a.row_tiles - 1)) * a.k_tiles;
-        codes[r] = a.codes + tile * 1024 + lane * 16;
-        grid[r] = a.grid + (tile * NG * 16 + min(col >> 2, NG - 1) * 16 + 4 * quad + (col & 3)) * 2;
+        const int64_t tile = (static_cast<int64_t>(expert) * a.row_tiles + min(tile0 + r, a.row_tiles - 1)) * a.k_tiles;
+        at.codes[r] = a.codes + tile * 1024 + lane * 16;
+        at.grid[r] = a.grid + (tile * NG * 16 + min(col >> 2, NG - 1) * 16 + 4 * quad + (col & 3)) * 2;
     }
-    const auto load = [&](Stage<F32, R, NB>& st, int kt) {
-        kt = min(kt, a.k_tiles - 1);
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            st.code[r] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(codes[r] + static_cast<int64_t>(kt) * 1024));
-            st.grid[r] = *reinterpret_cast<const uint32_t*>(grid[r] + static_cast<int64_t>(kt) * (NG * 32));
-        }
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const int k = kt * kTileIn + 32 * m;
-                const u32x4* p = reinterpret_cast<const u32x4*>(from[b] + static_cast<int64_t>(k < a.d_in ? k : 0) * (F32 ? 4 : 2));
-                st.x[b][m][0] = p[0];
-                if constexpr (F32) st.x[b][m][1] = p[1];
-            }
-    };
+    return at;
+}
 
-    f32x4 total[R][NB];
+template <int GROUP, int R>
+__device__ __forceinline__ void load_codes(Codes<R>& c, const WeightAt<R>& at, int kt) {
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int b = 0; b < NB; ++b) total[r][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int r = 0; r < R; ++r) {
+        c.code[r] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(at.codes[r] + static_cast<int64_t>(kt) * 1024));
+        c.grid[r] = *reinterpret_cast<const uint32_t*>(at.grid[r] + static_cast<int64_t>(kt) * (kTileIn / GROUP * 32));
+    }
+}
+
+// Adds a tile's products to y[row tile][block of 16 rows]: lane 16 q + c has outputs 4 q .. 4 q + 3 of row c.
+template <int GROUP, int R, int NB>
+__device__ __forceinline__ void multiply(f32x4 (&y)[R][NB], const Codes<R>& c, const bf16x8 (&x)[NB][4]) {
+    constexpr int NG = kTileIn / GROUP, STEPS = 4 / NG;
     const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
-
-    const auto work = [&](const Stage<F32, R, NB>& st, int kt) {
-        bf16x8 x[NB][4];
+    const uint32_t sixteens = bf16_sixteens();
+    f32x4 sum[NB][NG];
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                u32x4 v;
-                if constexpr (F32) {
-                    const int part = col % 3;
+        for (int g = 0; g < NG; ++g) {
+            sum[b][g] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const u32x4 w = st.x[b][m][i >> 1];
-                        v[i] = bf16_part(__uint_as_float(w[2 * (i & 1)]), part) >> 16 |
-                               bf16_part(__uint_as_float(w[2 * (i & 1) + 1]), part);
-                    }
-                } else {
-                    v = st.x[b][m][0];
-                }
-                const bool in = there[b] && kt * kTileIn + 32 * m < a.d_in;
-                x[b][m] = __builtin_bit_cast(bf16x8, in ? v : u32x4{0u, 0u, 0u, 0u});
-            }
-        bf16x8 w[R][4];
-        float s[R], z[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-#pragma unroll
-            for (int m = 0; m < 4; ++m) w[r][m] = codes_to_bf16(st.code[r][m]);
-            s[r] = f16_to_f32(static_cast<uint16_t>(st.grid[r]));
-            z[r] = __builtin_fmaf(-kCodeBias, s[r], f16_to_f32(static_cast<uint16_t>(st.grid[r] >> 16)));
+            for (int m = g * STEPS; m < (g + 1) * STEPS; ++m)
+                sum[b][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, x[b][m], sum[b][g], 0, 0, 0);
         }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        bf16x8 w[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) w[m] = codes_to_bf16(c.code[r][m], sixteens);
+        const float s = f16_to_f32(static_cast<uint16_t>(c.grid[r]));
+        const float z = __builtin_fmaf(-kCodeBias, s, f16_to_f32(static_cast<uint16_t>(c.grid[r] >> 16)));
         const auto of_group = [&](auto group) {
             constexpr int G = decltype(group)::value;
+            const float s4[4] = {row_bcast<4 * G>(s), row_bcast<4 * G + 1>(s), row_bcast<4 * G + 2>(s), row_bcast<4 * G + 3>(s)};
+            const float z4[4] = {row_bcast<4 * G>(z), row_bcast<4 * G + 1>(z), row_bcast<4 * G + 2>(z), row_bcast<4 * G + 3>(z)};
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                f32x4 sum{0.f, 0.f, 0.f, 0.f};
+                f32x4 t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int m = G * STEPS; m < (G + 1) * STEPS; ++m)
-                    sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, x[b][m], sum, 0, 0, 0);
+                    t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[m], x[b][m], t, 0, 0, 0);
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    f32x4 t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int m = G * STEPS; m < (G + 1) * STEPS; ++m)
-                        t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[r][m], x[b][m], t, 0, 0, 0);
-                    f32x4& y = total[r][b];
-                    y[0] = __builtin_fmaf(row_bcast<4 * G>(s[r]), t[0], __builtin_fmaf(row_bcast<4 * G>(z[r]), sum[0], y[0]));
-                    y[1] = __builtin_fmaf(row_bcast<4 * G + 1>(s[r]), t[1], __builtin_fmaf(row_bcast<4 * G + 1>(z[r]), sum[1], y[1]));
-                    y[2] = __builtin_fmaf(row_bcast<4 * G + 2>(s[r]), t[2], __builtin_fmaf(row_bcast<4 * G + 2>(z[r]), sum[2], y[2]));
-                    y[3] = __builtin_fmaf(row_bcast<4 * G + 3>(s[r]), t[3], __builtin_fmaf(row_bcast<4 * G + 3>(z[r]), sum[3], y[3]));
-                }
+                for (int i = 0; i < 4; ++i)
+                    y[r][b][i] = __builtin_fmaf(s4[i], t[i], __builtin_fmaf(z4[i], sum[b][G][0], y[r][b][i]));
             }
         };
         of_group(std::integral_constant<int, 0>());
@@ -165,83 +125,269 @@ __global__ __launch_bounds__(W * kWave) void fourbit_stream_kernel(FourbitArgs a
             of_group(std::integral_constant<int, 2>());
             of_group(std::integral_constant<int, 3>());
         }
-    };
-
-    // A ring of DEPTH tiles under way.
-    Stage<F32, R, NB> ring[DEPTH];
-#pragma unroll
-    for (int d = 0; d < DEPTH; ++d) load(ring[d], wave + d * W);
-    for (int kt = wave; kt < a.k_tiles; kt += DEPTH * W) {
-#pragma unroll
-        for (int d = 0; d < DEPTH; ++d) {
-            if (kt + d * W < a.k_tiles) {
-                work(ring[d], kt + d * W);
-                if (kt + (d + DEPTH) * W < a.k_tiles) load(ring[d], kt + (d + DEPTH) * W);
-            }
-        }
     }
+}
 
+// Four outputs j .. j + 3 of a row.
+__device__ __forceinline__ void store_outputs(const FourbitArgs& a, int vector_store, int row, int j, const f32x4& y) {
+    const int64_t to = static_cast<int64_t>(row) * a.d_out + j;
+    if (vector_store) {
+        if (a.y_dtype == GRINQH_F32)
+            *reinterpret_cast<f32x4*>(static_cast<float*>(a.y) + to) = y;
+        else
+            *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.y) + to) =
+                u32x2{f32_to_bf16(y[0]) | static_cast<uint32_t>(f32_to_bf16(y[1])) << 16,
+                      f32_to_bf16(y[2]) | static_cast<uint32_t>(f32_to_bf16(y[3])) << 16};
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (j + i >= a.d_out) break;
+        if (a.y_dtype == GRINQH_F32)
+            static_cast<float*>(a.y)[to + i] = y[i];
+        else
+            static_cast<uint16_t*>(a.y)[to + i] = f32_to_bf16(y[i]);
+    }
+}
+
+// bf16 activations.  What a wave works on goes through a piece of LDS of its own:
+// rows read in the operand's order would ask for 16 lines an instruction, lane
+// after lane in another one (64 rows 4096 to 14336 took 37 us, 23 so); brought into
+// LDS four whole lines at a time, and with them the codes, D tiles are under way
+// without a register held.  XR: rows in fours (4 XR of them).
+template <int R, int XR>
+struct WaveStage {
+    static constexpr int kCodes = XR * 1024, kGrid = kCodes + R * 1024, kBytes = kGrid + R * 256, kLoads = XR + 2 * R;
+};
+
+template <int GROUP, int R, int XR, int W, int D>
+__global__ __launch_bounds__(W * kWave) void fourbit_wave_kernel(FourbitArgs a, int vector_store) {
+    using S = WaveStage<R, XR>;
+    constexpr int NB = (XR + 3) / 4;
+    constexpr int kRed = W * R * NB * 1024;
+    __shared__ __attribute__((aligned(1024))) char lds[W * D * S::kBytes > kRed ? W * D * S::kBytes : kRed];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const RunTile run = find_run_tile(a, 4 * XR, blockIdx.z * kStreamTilesY + blockIdx.y, lane);
+    if (run.count <= 0) return;
+    const int col = lane & 15, quad = lane >> 4, tile0 = blockIdx.x * R;
+    const WeightAt<R> at = weight_at<GROUP, R>(a, run.expert, tile0, lane);
+    // Rows past the run read its last one, rows gathered from nowhere the first of
+    // x (and are stored as zeros); inputs past the last read the row's last
+    // ones, and the padded groups' s and z of zero take them out.
+    const uint16_t* from[XR];
+#pragma unroll
+    for (int i = 0; i < XR; ++i)
+        from[i] = static_cast<const uint16_t*>(a.x) + max(source_row(a, run.row + min(4 * i + quad, run.count - 1)), 0) * a.x_stride;
+    char* mine = lds + wave * (D * S::kBytes);
+    const uint32_t lds0 = lds_address(mine);
+    const auto bring = [&](int stage, int kt) {
+        kt = min(kt, a.k_tiles - 1);
+        const uint32_t to = lds0 + stage * S::kBytes;
+#pragma unroll
+        for (int i = 0; i < XR; ++i)
+            load_to_lds(from[i] + min(kt * kTileIn + 8 * (col ^ ((4 * i + quad) & 15)), a.d_in - 8), to + i * 1024);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            load_to_lds(at.codes[r] + static_cast<int64_t>(kt) * 1024, to + S::kCodes + r * 1024);
+            load_word_to_lds(at.grid[r] + static_cast<int64_t>(kt) * (kTileIn / GROUP * 32), to + S::kGrid + r * 256);
+        }
+    };
+#pragma unroll
+    for (int d = 0; d < D; ++d) bring(d, wave + d * W);
+    f32x4 y[R][NB];
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int b = 0; b < NB; ++b) red[wave][r * NB + b][lane] = total[r][b];
+        for (int b = 0; b < NB; ++b) y[r][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    int stage = 0;
+    for (int kt = wave; kt < a.k_tiles; kt += W) {
+        constexpr int kUnderWay = (D - 1) * S::kLoads;             // loads that may be: those of the stages behind this one
+        static_assert(kUnderWay < 64, "a count that the wait can name");
+        __builtin_amdgcn_s_waitcnt(0x0F70 | (kUnderWay & 15) | (kUnderWay >> 4) << 14);
+        asm volatile("" ::: "memory");
+        const char* from_lds = mine + stage * S::kBytes;
+        Codes<R> c;
+        bf16x8 x[NB][4];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            c.code[r] = *reinterpret_cast<const u32x4*>(from_lds + S::kCodes + r * 1024 + lane * 16);
+            c.grid[r] = *reinterpret_cast<const uint32_t*>(from_lds + S::kGrid + r * 256 + lane * 4);
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+                x[b][m] = *reinterpret_cast<const bf16x8*>(from_lds + chunk_at(XR == 1 ? col & 3 : 16 * b + col, 4 * m + quad));
+        __builtin_amdgcn_s_waitcnt(0xC07F);                        // lgkmcnt(0): the stage has been read and may be filled again
+        asm volatile("" ::: "memory");
+        bring(stage, kt + D * W);
+        stage = stage + 1 == D ? 0 : stage + 1;
+        multiply<GROUP, R, NB>(y, c, x);
+    }
+    __builtin_amdgcn_s_waitcnt(0x0F70);                            // vmcnt(0): nothing is brought into LDS any more
     __syncthreads();
-    for (int at = threadIdx.x; at < R * NB * kWave; at += W * kWave) {
-        const int rb = at >> 6;
-        f32x4 y = red[0][rb][lane];
+    f32x4* red = reinterpret_cast<f32x4*>(lds);
 #pragma unroll
-        for (int w = 1; w < W; ++w) y += red[w][rb][lane];
-        int t = 16 * (rb % NB) + col;
-        if constexpr (F32) {                                                   // three parts of a row, the largest last
-            f32x4 up = y;
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) up[i] = __shfl_down(y[i], 2, 16);
-            f32x4 mid = y;
+        for (int b = 0; b < NB; ++b) red[(wave * R * NB + r * NB + b) * kWave + lane] = y[r][b];
+    __syncthreads();
+    for (int rb = wave; rb < R * NB; rb += W) {
+        f32x4 sum = red[rb * kWave + lane];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mid[i] = __shfl_down(y[i], 1, 16);
-            y = up + mid + y;
-            t = col % 3 == 0 && col < 15 ? col / 3 : run.count;
-        }
-        const int j = (tile0 + rb / NB) * kTileOut + 4 * quad;
+        for (int w = 1; w < W; ++w) sum += red[(w * R * NB + rb) * kWave + lane];
+        const int t = 16 * (rb % NB) + col, j = (tile0 + rb / NB) * kTileOut + 4 * quad;
         if (t >= run.count || j >= a.d_out) continue;
-        const int64_t to = static_cast<int64_t>(run.row + t) * a.d_out + j;
-        if (vector_store) {
-            if (a.y_dtype == GRINQH_F32)
-                *reinterpret_cast<f32x4*>(static_cast<float*>(a.y) + to) = y;
-            else
-                *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.y) + to) =
-                    u32x2{f32_to_bf16(y[0]) | static_cast<uint32_t>(f32_to_bf16(y[1])) << 16,
-                          f32_to_bf16(y[2]) | static_cast<uint32_t>(f32_to_bf16(y[3])) << 16};
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (j + i >= a.d_out) break;
-                if (a.y_dtype == GRINQH_F32)
-                    static_cast<float*>(a.y)[to + i] = y[i];
-                else
-                    static_cast<uint16_t*>(a.y)[to + i] = f32_to_bf16(y[i]);
-            }
-        }
+        if (source_row(a, run.row + t) < 0) sum = f32x4{0.f, 0.f, 0.f, 0.f};
+        store_outputs(a, vector_store, run.row + t, j, sum);
     }
 }
 
-template <int GROUP, bool F32, int R, int NB, int W, int DEPTH>
-grinqh_status stream_launch(const FourbitArgs& a, int vector_store, hipStream_t stream) {
-    constexpr int kRows = kStreamRows<F32, NB>;
-    // at most a tile more for every expert that can have rows
-    const int64_t tiles = a.ends == nullptr ? (a.n_rows + kRows - 1) / kRows
-                                            : a.n_rows / kRows + std::min(a.n_rows, a.n_experts);
-    const unsigned y = static_cast<unsigned>(std::min<int64_t>(tiles, kStreamTilesY));
-    const dim3 grid((a.row_tiles + R - 1) / R, y, static_cast<unsigned>((tiles + kStreamTilesY - 1) / kStreamTilesY));
-    return launch_kernel(fourbit_stream_kernel<GROUP, F32, R, NB, W, DEPTH>, grid, W * kWave, 0, stream, a, vector_store);
+// fp32 activations of up to MT rows: the three parts of a row take three
+// neighbouring columns.  A wave splits the activations of kDepth of its tiles at a
+// time (eight values a lane) and passes them to the operand's order through a
+// piece of LDS of its own.
+template <int GROUP, int MT, int W>
+__global__ __launch_bounds__(W * kWave) void fourbit_stream_f32_kernel(FourbitArgs a, int vector_store) {
+    constexpr int kCols = 3 * MT;
+    __shared__ u32x4 parts[W][kDepth * 16 * kCols];        // [tile][16-byte chunk of its inputs][column]
+    __shared__ f32x4 red[W][kWave];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const RunTile run = find_run_tile(a, MT, blockIdx.z * kStreamTilesY + blockIdx.y, lane);
+    if (run.count <= 0) return;
+    const int col = lane & 15, quad = lane >> 4;
+    const WeightAt<1> at = weight_at<GROUP, 1>(a, run.expert, blockIdx.x, lane);
+    Codes<1> ring[kDepth];
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d)
+        if (wave + d * W < a.k_tiles) load_codes<GROUP>(ring[d], at, wave + d * W);
+
+    // This lane splits chunk `col` of tile `quad` of the kDepth.
+    const float* from[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+        const int src = t < run.count ? source_row(a, run.row + t) : -1;
+        from[t] = src < 0 ? nullptr : static_cast<const float*>(a.x) + src * a.x_stride + 8 * col;
+    }
+    u32x4 raw[MT][2];
+    const auto load_x = [&](int kt) {
+        const int k = (kt + quad * W) * kTileIn;
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            raw[t][0] = raw[t][1] = u32x4{0u, 0u, 0u, 0u};
+            if (from[t] != nullptr && k + 8 * col < a.d_in) {
+                raw[t][0] = *reinterpret_cast<const u32x4*>(from[t] + k);
+                raw[t][1] = *reinterpret_cast<const u32x4*>(from[t] + k + 4);
+            }
+        }
+    };
+    load_x(wave);
+
+    f32x4 y[1][1] = {{f32x4{0.f, 0.f, 0.f, 0.f}}};
+    for (int kt = wave; kt < a.k_tiles; kt += kDepth * W) {
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            u32x4 part[3];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t even[3], odd[3];
+                split(__uint_as_float(raw[t][i >> 1][2 * (i & 1)]), even);
+                split(__uint_as_float(raw[t][i >> 1][2 * (i & 1) + 1]), odd);
+#pragma unroll
+                for (int p = 0; p < 3; ++p) part[p][i] = even[p] >> 16 | odd[p];
+            }
+#pragma unroll
+            for (int p = 0; p < 3; ++p) parts[wave][lane * kCols + 3 * t + p] = part[p];
+        }
+        load_x(kt + kDepth * W);
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d) {
+            const int now = kt + d * W;
+            if (now < a.k_tiles) {
+                bf16x8 x[1][4];
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+                    x[0][m] = __builtin_bit_cast(bf16x8, parts[wave][(16 * d + 4 * m + quad) * kCols + min(col, kCols - 1)]);
+                multiply<GROUP, 1, 1>(y, ring[d], x);
+                if (now + kDepth * W < a.k_tiles) load_codes<GROUP>(ring[d], at, now + kDepth * W);
+            }
+        }
+    }
+    red[wave][lane] = y[0][0];
+    __syncthreads();
+    if (wave != 0) return;
+    f32x4 sum = red[0][lane];
+#pragma unroll
+    for (int w = 1; w < W; ++w) sum += red[w][lane];
+    f32x4 mid, low;                                                            // the row's other parts, two and one columns on
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        mid[i] = __shfl_down(sum[i], 1, 16);
+        low[i] = __shfl_down(sum[i], 2, 16);
+    }
+    sum = low + mid + sum;
+    const int j = blockIdx.x * kTileOut + 4 * quad;
+    if (col % 3 == 0 && col / 3 < run.count && j < a.d_out) store_outputs(a, vector_store, run.row + col / 3, j, sum);
 }
 
+// At most a tile more for every expert that can have rows.
+dim3 stream_grid(const FourbitArgs& a, int rows, int outputs) {
+    const int64_t tiles = a.ends == nullptr ? (a.n_rows + rows - 1) / rows : a.n_rows / rows + std::min(a.n_rows, a.n_experts);
+    return dim3((a.row_tiles + outputs - 1) / outputs, static_cast<unsigned>(std::min<int64_t>(tiles, kStreamTilesY)),
+                static_cast<unsigned>((tiles + kStreamTilesY - 1) / kStreamTilesY));
+}
+
+template <int GROUP, int R, int XR, int W, int D>
+grinqh_status wave_launch(const FourbitArgs& a, int vector_store, hipStream_t stream) {
+    return launch_kernel(fourbit_wave_kernel<GROUP, R, XR, W, D>, stream_grid(a, 4 * XR, R), W * kWave, 0, stream, a, vector_store);
+}
+
+template <int GROUP, int MT, int W>
+grinqh_status stream_f32_launch(const FourbitArgs& a, int vector_store, hipStream_t stream) {
+    return launch_kernel(fourbit_stream_f32_kernel<GROUP, MT, W>, stream_grid(a, MT, 1), W * kWave, 0, stream, a, vector_store);
+}
+
+// Tiles of tm rows that a call has, about: half of an expert's last one is empty.
+int64_t expected_tiles(const FourbitArgs& a, int tm) {
+    if (a.ends == nullptr) return (a.n_rows + tm - 1) / tm;
+    return a.n_rows / tm + std::max(1, std::min(a.n_rows, a.n_experts) / 2);
+}
+
+// Which kernel, by the sizes that the host knows.  Times in us on 256 CUs, groups
+// of 128, of codes that come from memory:
+//                          wave kernel   64-row tiles   128-row tiles
+//   4096 to 4096, 256 rows     22.6          38.8           59
+//   4096 to 14336, 128 rows    42.8          40.0           61
+//   4096 to 14336, 256 rows    73            42.6           63
+//   4096 to 14336, 1024 rows   280           168            141
+//   14336 to 4096, 1024 rows   230           151            198
+// A step of 128 inputs takes a 64-row tile 1.3 us and a 128-row tile 2.1, whether
+// few of them run or one on every CU; the wave kernel takes 0.15 ns for 16 rows x
+// 16 outputs x 128 inputs where there are enough of them to fill the card.
 template <int GROUP>
 grinqh_status stream_group(const FourbitArgs& a, int x_dtype, int vector_store, hipStream_t stream) {
-    if (x_dtype == GRINQH_F32) return stream_launch<GROUP, true, 1, 1, 8, 2>(a, vector_store, stream);
-    const int rows = a.n_rows / a.n_experts;       // of an expert, on average
-    if (rows <= 16) return stream_launch<GROUP, false, 1, 1, 8, 4>(a, vector_store, stream);
-    return stream_launch<GROUP, false, 2, 2, 8, 2>(a, vector_store, stream);
+    const int64_t rows = a.n_rows / a.n_experts;                   // of an expert, on average
+    if (x_dtype == GRINQH_F32) {
+        if (rows <= 1) return stream_f32_launch<GROUP, 1, 16>(a, vector_store, stream);
+        return stream_f32_launch<GROUP, 5, 8>(a, vector_store, stream);
+    }
+    const int64_t pieces = expected_tiles(a, 16) * a.row_tiles;
+    const auto rounds = [&](int tm) { return (expected_tiles(a, tm) * ((a.d_out + 255) / 256) + 255) / 256; };
+    const double waves = 0.15e-3 * pieces, small = 1.3 * rounds(64), large = 2.1 * rounds(128);
+    if (std::min(small, large) < waves) return launch_fourbit_tile(a, GROUP, small <= large ? 64 : 128, stream);
+    // Up to four rows: a quarter of the rows' traffic, and the least to do before the
+    // first product (one row 4096 to 4096: 4.3 us, 5.0 through 16 rows).
+    if (rows <= 4 && (a.ends == nullptr || rows <= 2)) {
+        if (a.row_tiles * expected_tiles(a, 4) <= 512) return wave_launch<GROUP, 1, 1, 8, 4>(a, vector_store, stream);
+        return wave_launch<GROUP, 1, 1, 4, 4>(a, vector_store, stream);        // 8192 to 28672: 25 us, 27 with eight waves
+    }
+    // Wider and taller where that leaves work for every CU (16 rows, R1 / R2 / R4: 4096
+    // to 4096 5.3 / 6.2 / 9.2, 4096 to 14336 16 / 10.3 / 10.0).
+    if (pieces <= 320) return wave_launch<GROUP, 1, 4, 8, 2>(a, vector_store, stream);
+    if (pieces <= 640) return wave_launch<GROUP, 2, 4, 8, 2>(a, vector_store, stream);
+    if (rows <= 16) return wave_launch<GROUP, 4, 4, 4, 2>(a, vector_store, stream);
+    if (pieces <= 1280) return wave_launch<GROUP, 2, 8, 4, 2>(a, vector_store, stream);
+    return wave_launch<GROUP, 4, 8, 4, 2>(a, vector_store, stream);
 }
 
 // Host checks of a product, and its kernel.

@@ -274,7 +274,6 @@ def test_same_call_same_bits_and_graph_replays(dev):
         step()
         torch.cuda.synchronize()
         assert torch.equal(got[0], y) and torch.equal(got[1], t)
-        assert torch.equal(t, y[:3])                                                 # the same weights and rows
 
 
 def test_another_stream(dev):
