@@ -10,8 +10,15 @@
 // (the page that was begun before) or from the list.  The token that begins a
 // page writes the table's entry.
 //
-// The scan is one workgroup's.  A small step's tokens are done by the same
-// workgroup, in one launch; more tokens by a second launch over the whole card.
+// A workgroup scans 1024 sequences at a time, with sums that stop at the type's end:
+// what counts is whether they pass a bound of 2^24, and the largest int32 stands for
+// all beyond it.  Nothing here is more than a few kB a workgroup, and what
+// bounds a call is the chain: the lengths' loads, the scan, a token's search, its
+// page's load.  So for up to 1024 sequences every workgroup scans them all for itself
+// and keeps the result in LDS for its own tokens: one launch.  Lengths that are updated in
+// place cannot be read by other workgroups meanwhile, and of more sequences the
+// scan itself takes longer than a launch: then one workgroup scans, and a second
+// launch does the tokens (up to 4096 of few sequences: that same workgroup).
 #include <algorithm>
 
 #include "internal.h"
@@ -21,7 +28,8 @@ namespace grinqh {
 namespace {
 
 constexpr int kPageThreads = 1024, kPageWaves = kPageThreads / kWave, kSpreadThreads = 256;
-constexpr int kOneLaunch = 4096;                   // tokens up to which the scan's workgroup does them too
+constexpr int kOneGroup = 4096;                    // tokens up to which one workgroup does the scan and them
+constexpr int kMostGroups = 512;                   // of a launch whose workgroups all scan: two to a CU
 
 struct PagesArgs {
     grinqh_extend_args p;
@@ -34,42 +42,55 @@ struct Sequence {
     int32_t before, first;
 };
 
-struct Scanned {
-    int64_t need, fresh, granted, all;
-};
+// Sums that stop at 2^32 - 1, in any order the same.
+__device__ __forceinline__ uint32_t add(uint32_t a, uint32_t b) { return __builtin_elementwise_add_sat(a, b); }
 
-__device__ __forceinline__ int64_t shfl_up64(int64_t x, int k) {
-    const int lo = __shfl_up(static_cast<int>(x), k), hi = __shfl_up(static_cast<int>(x >> 32), k);
-    return static_cast<int64_t>(static_cast<uint32_t>(lo)) | static_cast<int64_t>(hi) << 32;
+// x of the lane that CTRL names (0 where there is none or the row is not among ROWS).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t from_lane(uint32_t x) {
+    return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), CTRL, ROWS, 0xF, false));
 }
 
-// Inclusive sum over the workgroup's threads; `total` is the last.
-__device__ __forceinline__ int64_t block_sum_up_to(int64_t x, int64_t* waves, int64_t* total) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-    for (int k = 1; k < kWave; k <<= 1) {
-        const int64_t y = shfl_up64(x, k);
-        if (lane >= k) x += y;
-    }
-    __syncthreads();                                          // the waves' sums of the scan before have been read
+// Sums up to and with a lane: of its row of 16, of the wave.
+__device__ __forceinline__ uint32_t row_sum_up_to(uint32_t x) {
+    x = add(x, from_lane<0x111, 0xF>(x));                     // row_shr 1, 2, 4, 8
+    x = add(x, from_lane<0x112, 0xF>(x));
+    x = add(x, from_lane<0x114, 0xF>(x));
+    return add(x, from_lane<0x118, 0xF>(x));
+}
+__device__ __forceinline__ uint32_t wave_sum_up_to(uint32_t x) {
+    x = row_sum_up_to(x);
+    x = add(x, from_lane<0x142, 0xA>(x));                     // row_bcast 15: rows 1 and 3
+    return add(x, from_lane<0x143, 0xC>(x));                  // row_bcast 31: rows 2 and 3
+}
+
+struct Pair {
+    uint32_t a, b;
+};
+__device__ __forceinline__ Pair add(Pair x, Pair y) { return Pair{add(x.a, y.a), add(x.b, y.b)}; }
+
+// Sums up to and with a thread of the workgroup; `all` is what they come to.  One
+// barrier: `waves` is another one at the next call, and free again at the one after.
+template <int WAVES>
+__device__ __forceinline__ Pair group_sum_up_to(Pair x, Pair* waves, Pair& all) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    x = Pair{wave_sum_up_to(x.a), wave_sum_up_to(x.b)};
     if (lane == kWave - 1) waves[wave] = x;
     __syncthreads();
-    int64_t before = 0, all = 0;
-    for (int w = 0; w < kPageWaves; ++w) {
-        before += w < wave ? waves[w] : 0;
-        all += waves[w];
-    }
-    *total = all;
-    return x + before;
+    const Pair of = waves[lane & (WAVES - 1)];
+    const uint32_t a = row_sum_up_to(of.a), b = row_sum_up_to(of.b);
+    const auto at = [](uint32_t v, int l) { return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), l)); };
+    all = Pair{at(a, WAVES - 1), at(b, WAVES - 1)};
+    return wave == 0 ? x : add(x, Pair{at(a, wave - 1), at(b, wave - 1)});
 }
 
-__device__ __forceinline__ int32_t clamp32(int64_t x) { return static_cast<int32_t>(min(x, int64_t{0x7FFFFFFF})); }
+__device__ __forceinline__ int32_t clamp32(uint32_t x) { return static_cast<int32_t>(min(x, 0x7FFFFFFFu)); }
 
 // New token t of sequence b, whose new tokens begin at `begin`.
 __device__ __forceinline__ void place_token(const PagesArgs& a, const Sequence& s, int n_free, int b, int t, int begin) {
     const auto& p = a.p;
     const int64_t position = static_cast<int64_t>(s.before) + (t - begin);
-    p.positions[t] = clamp32(position);
+    p.positions[t] = static_cast<int32_t>(min(position, int64_t{0x7FFFFFFF}));
     int64_t slot = -1;
     if (s.first >= 0) {
         const int64_t at = position >> a.page_shift, held = (static_cast<int64_t>(s.before) + p.page_size - 1) >> a.page_shift;
@@ -86,77 +107,96 @@ __device__ __forceinline__ void place_token(const PagesArgs& a, const Sequence& 
     }
     p.slots[t] = slot;
 }
+__device__ __forceinline__ void no_token(const PagesArgs& a, int t) {
+    a.p.slots[t] = -1;
+    a.p.positions[t] = 0;
+}
 
 // The sequence of token t: the last whose new tokens begin at t or before (those
 // without new tokens end where the next begins).  lo .. hi bound it.
-__device__ __forceinline__ int sequence_of(const int32_t* cu, int t, int lo, int hi) {
+__device__ __forceinline__ int sequence_of(const int32_t* begins, int t, int lo, int hi) {
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (cu[mid] <= t)
+        if (begins[mid] <= t)
             lo = mid;
         else
             hi = mid - 1;
     }
     return lo;
 }
+// The same for a wave's one token, 64 places at a time.
+__device__ __forceinline__ int sequence_of_wave(const int32_t* begins, int t, int count, int lane) {
+    int lo = 0;
+    while (count > 1) {
+        const int step = (count + kWave - 1) / kWave;
+        const int passed = __popcll(__ballot(lane * step < count && begins[lo + min(lane * step, count - 1)] <= t)) - 1;
+        lo += passed * step;
+        count = min(step, count - passed * step);
+    }
+    return lo;
+}
 
-template <bool TOKENS>
-__global__ __launch_bounds__(kPageThreads) void extend_scan_kernel(PagesArgs a) {
-    __shared__ int64_t waves[kPageWaves];
+// TOKENS: the tokens too (of up to THREADS sequences; every workgroup scans, the
+// first one's results are written); else one workgroup, which leaves the
+// sequences in the workspace.
+template <bool TOKENS, int THREADS>
+__global__ __launch_bounds__(THREADS) void extend_scan_kernel(PagesArgs a) {
+    constexpr int WAVES = THREADS / kWave;
+    __shared__ Pair waves[2][WAVES];
     __shared__ int refused;
+    __shared__ Sequence here[TOKENS ? THREADS : 1];
+    __shared__ int32_t begins[TOKENS ? THREADS : 1];
     const auto& p = a.p;
     Sequence* seqs = static_cast<Sequence*>(p.workspace);
     if (threadIdx.x == 0) refused = 0;
-    const int n_free = min(max(p.n_free[0], 0), p.n_pages);
-    Scanned upto{0, 0, 0, 0};
-    for (int base = 0; base < p.batch; base += kPageThreads) {
+    const uint32_t n_free = min(max(p.n_free[0], 0), p.n_pages), page = p.page_size;
+    const bool writes = !TOKENS || blockIdx.x == 0;
+    const auto pages_of = [&](uint32_t tokens) { return (tokens >> a.page_shift) + ((tokens & (page - 1)) != 0); };
+    Pair asked{0u, 0u}, given{0u, 0u};                        // pages and new tokens; pages and lengths
+    for (int base = 0; base < p.batch; base += THREADS) {
         const int b = base + threadIdx.x;
         const bool there = b < p.batch;
-        const int64_t old = there ? max(p.seq_lens[b], 0) : 0, fresh = there ? max(p.n_new[b], 0) : 0;
-        const int64_t held = (old + p.page_size - 1) >> a.page_shift, wanted = (old + fresh + p.page_size - 1) >> a.page_shift;
-        const int64_t need = wanted - held;
-        int64_t total;
-        const int64_t needed = upto.need + block_sum_up_to(need, waves, &total);
-        upto.need += total;
-        const int64_t end = upto.fresh + block_sum_up_to(fresh, waves, &total);
-        upto.fresh += total;
-        const bool granted = fresh == 0 || (needed <= n_free && wanted <= p.max_pages && end <= p.capacity);
+        const uint32_t old = there ? max(p.seq_lens[b], 0) : 0, fresh = there ? max(p.n_new[b], 0) : 0;
+        const uint32_t held = pages_of(old), wanted = pages_of(old + fresh), need = wanted - held;
+        Pair all;
+        const Pair upto = add(asked, group_sum_up_to<WAVES>(Pair{need, fresh}, waves[0], all));
+        asked = add(asked, all);
+        const bool granted = fresh == 0 || (upto.a <= n_free && wanted <= static_cast<uint32_t>(p.max_pages) &&
+                                            upto.b <= static_cast<uint32_t>(p.capacity));
         // Pages are taken by their place among those of all sequences, served or
         // not: the pages of one that is refused for its own sake stay unused in
         // the list only if none behind it are taken, so places are counted again
         // over what is granted.
-        const int64_t mine = granted ? need : 0;
-        const int64_t given = upto.granted + block_sum_up_to(mine, waves, &total);
-        upto.granted += total;
-        const int64_t len = granted ? old + fresh : old;
-        const int64_t all = upto.all + block_sum_up_to(len, waves, &total);
-        upto.all += total;
-        if (there) {
-            seqs[b] = Sequence{static_cast<int32_t>(old), granted ? static_cast<int32_t>(given - mine) : -1};
+        const uint32_t mine = granted ? need : 0u, len = granted ? old + fresh : old;
+        const Pair to = add(given, group_sum_up_to<WAVES>(Pair{mine, len}, waves[1], all));
+        given = add(given, all);
+        const Sequence s{static_cast<int32_t>(old), granted ? static_cast<int32_t>(to.a - mine) : -1};
+        if (TOKENS) {
+            here[threadIdx.x] = s;
+            begins[threadIdx.x] = clamp32(upto.b - fresh);
+        }
+        if (there && writes) {
+            if (!TOKENS) seqs[b] = s;
             p.new_lens[b] = clamp32(len);
-            p.cu_q[b + 1] = clamp32(end);
-            p.cu_k[b + 1] = clamp32(all);
+            p.cu_q[b + 1] = clamp32(upto.b);
+            p.cu_k[b + 1] = clamp32(to.b);
             if (!granted) atomicAdd(&refused, 1);
         }
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 0 && writes) {
         p.cu_q[0] = p.cu_k[0] = 0;
         p.refused[0] = refused;
-        p.n_free_out[0] = n_free - static_cast<int>(upto.granted);
-        if (!TOKENS) reinterpret_cast<int32_t*>(seqs + p.batch)[0] = n_free;
+        p.n_free_out[0] = static_cast<int>(n_free - given.a);
+        if (!TOKENS) reinterpret_cast<uint32_t*>(seqs + p.batch)[0] = n_free;
     }
-    if (TOKENS) {
-        __threadfence_block();
-        __syncthreads();
-        for (int t = threadIdx.x; t < p.capacity; t += kPageThreads) {
-            if (t >= upto.fresh) {
-                p.slots[t] = -1;
-                p.positions[t] = 0;
-            } else {
-                const int b = sequence_of(p.cu_q, t, 0, p.batch - 1);
-                place_token(a, seqs[b], n_free, b, t, p.cu_q[b]);
-            }
+    if (!TOKENS) return;
+    for (int t = blockIdx.x * THREADS + threadIdx.x; t < p.capacity; t += gridDim.x * THREADS) {
+        if (static_cast<uint32_t>(t) >= asked.b) {
+            no_token(a, t);
+        } else {
+            const int b = sequence_of(begins, t, 0, p.batch - 1);
+            place_token(a, here[b], static_cast<int>(n_free), b, t, begins[b]);
         }
     }
 }
@@ -165,15 +205,20 @@ __global__ __launch_bounds__(kSpreadThreads) void extend_tokens_kernel(PagesArgs
     const auto& p = a.p;
     const Sequence* seqs = static_cast<const Sequence*>(p.workspace);
     const int n_free = reinterpret_cast<const int32_t*>(seqs + p.batch)[0];
-    const int t = blockIdx.x * kSpreadThreads + threadIdx.x;
-    if (t >= p.capacity) return;
-    if (p.batch == 0 || t >= p.cu_q[p.batch]) {
-        p.slots[t] = -1;
-        p.positions[t] = 0;
-        return;
+    const int lane = threadIdx.x & 63, first = __builtin_amdgcn_readfirstlane(blockIdx.x * kSpreadThreads + (threadIdx.x & ~63));
+    const int t = first + lane, all = p.batch == 0 ? 0 : p.cu_q[p.batch];
+    int lo = 0, hi = 0;
+    if (first < all) {
+        lo = sequence_of_wave(p.cu_q, first, p.batch, lane);
+        hi = sequence_of_wave(p.cu_q, min(first + kWave, all) - 1, p.batch, lane);
     }
-    const int b = sequence_of(p.cu_q, t, 0, p.batch - 1);
-    place_token(a, seqs[b], n_free, b, t, p.cu_q[b]);
+    if (t >= p.capacity) return;
+    if (t >= all) {
+        no_token(a, t);
+    } else {
+        const int b = sequence_of(p.cu_q, t, lo, hi);
+        place_token(a, seqs[b], n_free, b, t, p.cu_q[b]);
+    }
 }
 
 // One workgroup.  Of every 1024 sequences the finished ones are listed, in order;
@@ -278,9 +323,15 @@ grinqh_status grinqh_kv_extend(const grinqh_extend_args* args, void* stream) {
         return GRINQH_EINVAL;
     const PagesArgs a{p, log2_of(p.page_size)};
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    if (p.capacity <= kOneLaunch) return launch_kernel(extend_scan_kernel<true>, dim3(1), kPageThreads, 0, st, a);
-    const grinqh_status status = launch_kernel(extend_scan_kernel<false>, dim3(1), kPageThreads, 0, st, a);
+    const bool shared = !lens_same && !free_same;             // others may scan while one workgroup writes
+    if (p.batch <= 256 && p.capacity <= 256) return launch_kernel(extend_scan_kernel<true, 256>, dim3(1), 256, 0, st, a);
+    if (p.batch <= kPageThreads && (shared || p.capacity <= kOneGroup)) {
+        const int groups = std::min((p.capacity + kPageThreads - 1) / kPageThreads, kMostGroups);
+        return launch_kernel(extend_scan_kernel<true, kPageThreads>, dim3(shared ? std::max(groups, 1) : 1), kPageThreads, 0, st, a);
+    }
+    const grinqh_status status = launch_kernel(extend_scan_kernel<false, kPageThreads>, dim3(1), kPageThreads, 0, st, a);
     if (status != GRINQH_OK) return status;
+    if (p.capacity == 0) return GRINQH_OK;
     return launch_kernel(extend_tokens_kernel, dim3((p.capacity + kSpreadThreads - 1) / kSpreadThreads), kSpreadThreads, 0, st, a);
 }
 

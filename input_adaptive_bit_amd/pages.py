@@ -46,24 +46,46 @@ def _table(t, batch, device):
     return t.data_ptr(), t.stride(0) if batch > 1 else t.shape[1], t.shape[1]
 
 
+def _plan(page_table, seq_lens, n_new, free_pages, n_free):
+    """(device, batch, columns, the leading fields of ExtendArgs) of the tensors that a plan reads."""
+    try:
+        device, (batch,) = seq_lens.device, seq_lens.shape
+        index, (rows, columns), (stride, s1) = device.index, page_table.shape, page_table.stride()
+        fits = rows == batch and (s1 == 1 or columns < 2) and (batch < 2 or stride >= columns) and n_new.numel() == batch
+        for t in (page_table, seq_lens, n_new, free_pages, n_free):
+            fits = fits and t.dtype is _I32 and t.get_device() == index and (t is page_table or t.is_contiguous())
+        fits = fits and seq_lens.is_cuda and free_pages.numel() >= 1 and n_free.numel() >= 1
+    except (AttributeError, TypeError, ValueError):
+        fits = False
+    if fits:
+        return device, batch, columns, (page_table.data_ptr(), stride if batch > 1 else columns, seq_lens.data_ptr(),
+                                        n_new.data_ptr(), free_pages.data_ptr(), n_free.data_ptr())
+    device = _tensor(seq_lens, "seq_lens")                    # one by one, to say what does not
+    batch = seq_lens.numel()
+    _tensor(n_new, "n_new", device)
+    if n_new.numel() != batch:
+        raise ValueError("n_new must be as long as seq_lens")
+    table, stride, columns = _table(page_table, batch, device)
+    return device, batch, columns, (table, stride, *(_plain(t, name, _I32, device, count) for name, t, count in (
+        ("seq_lens", seq_lens, batch), ("n_new", n_new, batch), ("free_pages", free_pages, 1), ("n_free", n_free, 1))))
+
+
 def grinqh_kv_extend(page_table, seq_lens, n_new, free_pages, n_free, page_size: int, step: Step, workspace,
                      stream=None) -> None:
     """page_table: int32 [batch][max_pages]; seq_lens, n_new: int32 [batch]; free_pages: int32 [n_pages];
     n_free: int32 [1]; step: the tensors to write (step.seq_lens and step.n_free may be seq_lens and n_free)."""
-    device = _tensor(seq_lens, "seq_lens")
-    batch, room = seq_lens.numel(), step.slots.numel()
-    if step.positions.numel() != room or n_new.numel() != batch:
-        raise ValueError("n_new must be as long as seq_lens, and positions as slots")
-    table, stride, columns = _table(page_table, batch, device)
+    device, batch, columns, inputs = _plan(page_table, seq_lens, n_new, free_pages, n_free)
+    room = step.slots.numel()
+    if step.positions.numel() != room:
+        raise ValueError("step.positions must be as long as step.slots")
     _tensor(workspace, "workspace", device)
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    i32 = [_plain(t, name, _I32, device, count) for name, t, count in (
-        ("seq_lens", seq_lens, batch), ("n_new", n_new, batch), ("free_pages", free_pages, 1), ("n_free", n_free, 1),
+    lens, left, refused, cu_q, cu_k, positions = (_plain(t, name, _I32, device, count) for name, t, count in (
         ("step.seq_lens", step.seq_lens, batch), ("step.n_free", step.n_free, 1), ("step.refused", step.refused, 1),
-        ("step.cu_q", step.cu_q, batch + 1), ("step.cu_k", step.cu_k, batch + 1), ("step.positions", step.positions, room))]
-    a = ExtendArgs(table, stride, *i32[:4], _fit(batch), columns, _fit(page_size), _fit(free_pages.numel()), _fit(room), *i32[4:9],
-                   _plain(step.slots, "step.slots", _I64, device, room), i32[9], workspace.data_ptr(), workspace.nbytes)
+        ("step.cu_q", step.cu_q, batch + 1), ("step.cu_k", step.cu_k, batch + 1), ("step.positions", step.positions, room)))
+    a = ExtendArgs(*inputs, _fit(batch), _fit(columns), _fit(page_size), _fit(free_pages.numel()), _fit(room), lens, left, refused, cu_q, cu_k,
+                   _plain(step.slots, "step.slots", _I64, device, room), positions, workspace.data_ptr(), workspace.nbytes)
     _run("grinqh_kv_extend", device, stream, ctypes.byref(a))
 
 
@@ -95,21 +117,26 @@ def kv_extend(page_table, seq_lens, n_new, free_pages, n_free, page_size: int, c
     """Pages for n_new[b] tokens behind the seq_lens[b] cached ones of every sequence: writes the new pages into
     page_table and returns what the step's other calls take (allocates it; slots and positions hold `capacity` tokens).
     With in_place, seq_lens and n_free themselves are updated."""
-    device = _tensor(seq_lens, "seq_lens")
+    device, batch, columns, inputs = _plan(page_table, seq_lens, n_new, free_pages, n_free)
     if not 0 <= capacity <= 1 << 24:
         raise GrinqhError(GRINQH_EINVAL, "grinqh_kv_extend")
-    batch = seq_lens.numel()
-    # one allocation: slots first, the workspace (8 bytes a sequence and 16), then what is 4 bytes wide
+    # One allocation: slots (8 bytes each), the workspace (on 16 bytes, 8 a sequence and 16), then what is 4 bytes wide.
+    # The call needs addresses only, and the library refuses every count that the types could not hold.
     ws = 2 * batch + 4
-    tail = 2 * capacity + (2 * capacity & 2)                 # the workspace lies on 16 bytes
-    at = tail + ws
-    sizes = (capacity, batch + 1, batch + 1, 0 if in_place else batch, 0 if in_place else 1, 1)
-    both = _empty((at + sum(sizes),), _I32, device, stream)
-    parts = torch.split(both, (2 * capacity, tail - 2 * capacity, ws, *sizes))
-    slots, positions, cu_q, cu_k, lens, left, refused = parts[0].view(_I64), *parts[3:]
-    step = Step(slots, positions, cu_q, cu_k, seq_lens if in_place else lens, n_free if in_place else left, refused)
-    grinqh_kv_extend(page_table, seq_lens, n_new, free_pages, n_free, page_size, step, parts[2], stream)
-    return step
+    sizes = (2 * capacity, 2 * capacity & 2, ws, capacity, batch + 1, batch + 1, 0 if in_place else batch, 0 if in_place else 1, 1)
+    both = _empty((sum(sizes),), _I32, device, stream)
+    slots, _, _, positions, cu_q, cu_k, lens, left, refused = both.split(sizes)
+    start = both.data_ptr()
+    space = start + 4 * (sizes[0] + sizes[1])
+    at = [space + 4 * ws]                                     # positions, cu_q, cu_k, lens, left, refused
+    for size in sizes[3:8]:
+        at.append(at[-1] + 4 * size)
+    if in_place:
+        lens, left, at[3], at[4] = seq_lens, n_free, inputs[2], inputs[5]
+    a = ExtendArgs(*inputs, _fit(batch), _fit(columns), _fit(page_size), _fit(free_pages.numel()), capacity, at[3], at[4], at[5], at[1], at[2],
+                   start, at[0], space, 4 * ws)
+    _run("grinqh_kv_extend", device, stream, ctypes.byref(a))
+    return Step(slots.view(_I64), positions, cu_q, cu_k, lens, left, refused)
 
 
 def kv_release(page_table, seq_lens, finished, free_pages, n_free, page_size: int, stream=None) -> None:

@@ -84,6 +84,25 @@ def test_what_does_not_fit_is_refused_and_the_rest_served(dev):
         same(run(dev, table, lens, new, free, n_free, 16, capacity), O.extend(table, lens, new, free, n_free, 16, capacity))
 
 
+@pytest.mark.parametrize("batch", [7, 300, 1500])
+@pytest.mark.parametrize("capacity", [100, 9000])
+def test_sums_past_the_types_end(dev, batch, capacity):
+    """Lengths and counts whose sums pass 32 bits many times over: the ends stop at the largest number, and the sequences
+    ahead of those counts are served as ever."""
+    rng = np.random.default_rng(batch)
+    lens, new = rng.integers(0, 40, batch), rng.integers(0, 3, batch)
+    held = lens.copy()
+    for at in (batch // 2, batch // 2 + 1, batch - 2, batch - 1):
+        lens[at], new[at] = (2 ** 31 - 1, 0) if at % 2 else (3, 2 ** 31 - 1)
+        held[at] = 0
+    lens[batch // 2 + 2], new[batch // 2 + 2] = 0, 5
+    held[batch // 2 + 2] = 0
+    table, free, n_free = pool(rng, held, 16, 4, 2 * batch)
+    for in_place in (False, True):
+        say(f"kv_extend batch={batch} capacity={capacity} in place={in_place}")
+        same(run(dev, table, lens, new, free, n_free, 16, capacity, in_place), O.extend(table, lens, new, free, n_free, 16, capacity))
+
+
 def test_numbers_that_name_no_page(dev):
     """A table or list with entries outside the pool, and a count outside the list: no slot comes of them."""
     rng = np.random.default_rng(1)
