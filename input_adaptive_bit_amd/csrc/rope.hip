@@ -8,10 +8,16 @@
 // two of fp32): the mean comes from exchanges between them, the other half of a
 // rotated pair from the lane that holds it, and a row of the cache is quantised
 // from the same registers (kv_store.hpp).  Angles are the same for all heads of a
-// token, so such a group of lanes stays with one token and takes several of its
-// rows.  An angle's turns are counted in fp64 and only the fraction of a turn is
+// token: a workgroup takes some tokens, or a part of the heads of one, and works
+// its angles out once, one a thread, into LDS.
+// An angle's turns are counted in fp64 and only the fraction of a turn is
 // rounded to fp32 (at position 10^5 a 32-bit product would be off by 0.01
 // radian); sine and cosine are of that fraction.
+//
+// Memory bounds it: 16381 tokens of 64 + 8 heads of 128 bf16, normed, into an 8-bit
+// cache, 670 MB, take 143 us (4.7 TB/s; a large copy reaches 5.25).  Angles worked out
+// by the lanes that use them, eight rows to each, took 194 us: 300 vector
+// instructions for a row, a third of them for angles, IEEE roots and divisions.
 #include <algorithm>
 
 #include "internal.h"
@@ -24,7 +30,8 @@ namespace {
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kRopeThreads = 256;
-constexpr int kMaxRopeGroups = 1 << 20;            // workgroups; more items than they hold go round again
+constexpr int kMostAngles = 512;                   // of a workgroup: 4 to 16 tokens
+constexpr int kFill = 2048;                        // workgroups that fill the card: eight to a CU
 
 struct RopeArgs {
     KvDims d;
@@ -39,7 +46,8 @@ struct RopeArgs {
     const double* freqs;
     const void* weight[2];
     int64_t n_tokens;
-    int n_q, n_kv, rows, parts;                    // rows of a token, and how many lane groups share them
+    int n_q, n_kv, rows;                           // rows: of a token
+    int tokens, step_tokens, step_rows;            // of a workgroup; to a lane group's next row
     int rope_dim, neighbours, weight_dtype;
     float eps;
 };
@@ -69,9 +77,11 @@ template <typename T>
 __device__ __forceinline__ RawRow<T> narrow(float (&w)[kPerLane]) {
     RawRow<T> raw;
     if constexpr (sizeof(T) == 2) {
+        typedef float two __attribute__((ext_vector_type(2)));
+        typedef __bf16 two_bf16 __attribute__((ext_vector_type(2)));
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            raw.v[0][i] = f32_to_bf16(w[2 * i]) | static_cast<uint32_t>(f32_to_bf16(w[2 * i + 1])) << 16;
+        for (int i = 0; i < 4; ++i)                            // one instruction, to nearest even
+            raw.v[0][i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((two{w[2 * i], w[2 * i + 1]}), two_bf16));
         widen<T>(raw, w);
     } else {
 #pragma unroll
@@ -80,129 +90,160 @@ __device__ __forceinline__ RawRow<T> narrow(float (&w)[kPerLane]) {
     return raw;
 }
 
+template <typename T>
+__device__ __forceinline__ RawRow<T> load_raw(const void* at) {
+    RawRow<T> raw;
+#pragma unroll
+    for (unsigned i = 0; i < sizeof(T) / 2; ++i) raw.v[i] = static_cast<const u32x4*>(at)[i];
+    return raw;
+}
+
+// Turns of an angle and weights, as a lane of a row reads them: its 8 values' first
+// four from one stretch and its last four from another, lane after lane.
+__device__ __forceinline__ int in_halves(int i, int count) { return (i & 4 ? count / 2 : 0) + (i >> 3) * 4 + (i & 3); }
+__device__ __forceinline__ void read_eight(const float* halves, int count, int lane, float (&v)[kPerLane]) {
+    typedef float f32x4 __attribute__((ext_vector_type(4)));
+    const f32x4 a = reinterpret_cast<const f32x4*>(halves)[lane], b = reinterpret_cast<const f32x4*>(halves + count / 2)[lane];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] = a[i];
+        v[4 + i] = b[i];
+    }
+}
+
 template <int D, typename T, int BITS>
 __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a) {
-    constexpr int kLanes = D / kPerLane, kItems = kRopeThreads / kLanes;
-    const int lane = threadIdx.x % kLanes;
-    const int64_t items = a.n_tokens * a.parts, step = static_cast<int64_t>(gridDim.x) * kItems;
+    constexpr int kLanes = D / kPerLane, kItems = kRopeThreads / kLanes, kTokens = kMostAngles / (D / 2);
+    __shared__ __attribute__((aligned(16))) float cosines[kMostAngles], sines[kMostAngles], weights[2][D];
+    __shared__ int64_t slots[kTokens];
+    const int lane = threadIdx.x % kLanes, pairs = a.rope_dim / 2;
+    const int64_t token0 = static_cast<int64_t>(blockIdx.x) * a.tokens;
+    const int tokens = static_cast<int>(min(static_cast<int64_t>(a.tokens), a.n_tokens - token0));
+    // The group's rows: (t, r), every kItems gridDim.y-th of the workgroup's.
+    const int rows = a.rows;
+    int r = threadIdx.x / kLanes + kItems * blockIdx.y, t = r / rows;
+    r -= t * rows;
+    const auto load = [&](int t, int r) {
+        const int which = r < a.n_q ? 0 : r < a.n_q + a.n_kv ? 1 : 2, first = which == 0 ? 0 : which == 1 ? a.n_q : a.n_q + a.n_kv;
+        const T* base = static_cast<const T*>(which == 0 ? a.src[0] : which == 1 ? a.src[1] : a.src[2]);
+        const int64_t stride = which == 0 ? a.src_stride[0] : which == 1 ? a.src_stride[1] : a.src_stride[2];
+        return load_raw<T>(base + (token0 + t) * stride + (r - first) * D + lane * kPerLane);
+    };
+    RawRow<T> next;
+    if (t < tokens) next = load(t, r);                         // under way while the angles are worked out
+    for (int i = threadIdx.x; i < tokens * pairs; i += kRopeThreads) {
+        const int of = i / pairs, j = i - of * pairs;
+        const double turns = a.positions[token0 + of] * a.freqs[j] * 0.15915494309189533577;          // 1 / (2 pi)
+        float s, c;
+        sincospif(static_cast<float>(2.0 * (turns - rint(turns))), &s, &c);
+        const int at = of * pairs + (a.neighbours ? j : in_halves(j, pairs));
+        sines[at] = s;
+        cosines[at] = c;
+    }
+    if (threadIdx.x < D) {
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+            if (a.weight[w] != nullptr)
+                weights[w][in_halves(threadIdx.x, D)] = a.weight_dtype == GRINQH_BF16
+                    ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(a.weight[w])[threadIdx.x]) << 16)
+                    : static_cast<const float*>(a.weight[w])[threadIdx.x];
+    }
+    if (BITS != 0 && threadIdx.x < tokens) slots[threadIdx.x] = a.slots[token0 + threadIdx.x];
+    __syncthreads();
+
     // Where the other half of this lane's pairs is, and its sign.
     const int across = a.rope_dim / (2 * kPerLane);
     const bool turned = lane * kPerLane < a.rope_dim, second = lane >= across;
-    const int partner = !turned || a.neighbours ? lane : second ? lane - across : lane + across;
-    const float sign = second ? 1.f : -1.f;
-
-    for (int64_t item = static_cast<int64_t>(blockIdx.x) * kItems + threadIdx.x / kLanes; item < items; item += step) {
-        const int64_t token = item / a.parts;
-        const int part = static_cast<int>(item - token * a.parts);
-        const auto row_of = [&](int r, int which, int first) {
-            return static_cast<const T*>(a.src[which]) + token * a.src_stride[which] + (r - first) * D + lane * kPerLane;
-        };
-        const auto load = [&](int r) {
-            const T* p = r < a.n_q ? row_of(r, 0, 0) : r < a.n_q + a.n_kv ? row_of(r, 1, a.n_q) : row_of(r, 2, a.n_q + a.n_kv);
-            RawRow<T> raw;
+    const int partner_at = ((threadIdx.x & 63) + (!turned ? 0 : second ? -across : across)) * 4;
+    // Eight lanes on (heads of 128, all turned): a rotation within 16 lanes, without LDS.
+    const auto from_partner = [&](float v) {
+        const int bits = __float_as_int(v);
+        return __int_as_float(across == 8 ? __builtin_amdgcn_update_dpp(bits, bits, 0x128, 0xF, 0xF, false)
+                                          : __builtin_amdgcn_ds_bpermute(partner_at, bits));
+    };
+    while (t < tokens) {
+        RawRow<T> raw = next;
+        int next_t = t + a.step_tokens, next_r = r + a.step_rows;
+        if (next_r >= rows) {
+            next_r -= rows;
+            ++next_t;
+        }
+        if (next_t < tokens) next = load(next_t, next_r);
+        const bool is_q = r < a.n_q, is_v = r >= a.n_q + a.n_kv;
+        float w[kPerLane];
+        widen<T>(raw, w);
+        if (!is_v) {
+            if ((is_q ? a.weight[0] : a.weight[1]) != nullptr) {
+                float sum = 0.f, g[kPerLane];
+                read_eight(weights[is_q ? 0 : 1], D, lane, g);
 #pragma unroll
-            for (unsigned i = 0; i < sizeof(T) / 2; ++i) raw.v[i] = reinterpret_cast<const u32x4*>(p)[i];
-            return raw;
-        };
-        RawRow<T> next = load(part);
-        float cs[kPerLane], sn[kPerLane];
-        if (turned) {
-            const double position = a.positions[token];
-            const double* freq = a.freqs + (a.neighbours ? lane * (kPerLane / 2) : (second ? lane - across : lane) * kPerLane);
+                for (int i = 0; i < kPerLane; ++i) sum = __builtin_fmaf(w[i], w[i], sum);
+                sum = over_row<D>(sum, [](float x, float y) { return x + y; });
+                const float scale = rsqrtf(sum * (1.f / D) + a.eps);
 #pragma unroll
-            for (int i = 0; i < kPerLane; ++i) {
-                if (i >= kPerLane / 2 && a.neighbours) break;
-                const double turns = position * freq[i] * 0.15915494309189533577;          // 1 / (2 pi)
-                sincospif(static_cast<float>(2.0 * (turns - rint(turns))), &sn[i], &cs[i]);
+                for (int i = 0; i < kPerLane; ++i) w[i] = w[i] * scale * g[i];
+            }
+            if (a.neighbours) {
+                if (turned) {
+                    typedef float f32x4 __attribute__((ext_vector_type(4)));
+                    const f32x4 c = reinterpret_cast<const f32x4*>(cosines + t * pairs)[lane], s = reinterpret_cast<const f32x4*>(sines + t * pairs)[lane];
+#pragma unroll
+                    for (int i = 0; i < kPerLane; i += 2) {
+                        const float x = w[i], y = w[i + 1];
+                        w[i] = __builtin_fmaf(x, c[i / 2], -(y * s[i / 2]));
+                        w[i + 1] = __builtin_fmaf(y, c[i / 2], x * s[i / 2]);
+                    }
+                }
+            } else {
+                float other[kPerLane];
+#pragma unroll
+                for (int i = 0; i < kPerLane; ++i) other[i] = from_partner(w[i]);
+                if (turned) {
+                    float c[kPerLane], s[kPerLane];
+                    read_eight(cosines + t * pairs, pairs, second ? lane - across : lane, c);
+                    read_eight(sines + t * pairs, pairs, second ? lane - across : lane, s);
+                    const float sign = second ? 1.f : -1.f;
+#pragma unroll
+                    for (int i = 0; i < kPerLane; ++i) w[i] = __builtin_fmaf(w[i], c[i], sign * (other[i] * s[i]));
+                }
+            }
+            raw = narrow<T>(w);
+            T* to = static_cast<T*>(is_q ? a.dst[0] : a.dst[1]);
+            if (to != nullptr) {
+                to += (token0 + t) * (is_q ? a.dst_stride[0] : a.dst_stride[1]) + (is_q ? r : r - a.n_q) * D + lane * kPerLane;
+#pragma unroll
+                for (unsigned i = 0; i < sizeof(T) / 2; ++i) reinterpret_cast<u32x4*>(to)[i] = raw.v[i];
             }
         }
-        const int64_t slot = BITS == 0 ? 0 : a.slots[token];
-
-        for (int r = part; r < a.rows; r += a.parts) {
-            RawRow<T> raw = next;
-            if (r + a.parts < a.rows) next = load(r + a.parts);
-            const bool is_q = r < a.n_q, is_v = r >= a.n_q + a.n_kv;
-            float w[kPerLane];
-            widen<T>(raw, w);
-            if (!is_v) {
-                const void* weight = a.weight[is_q ? 0 : 1];
-                if (weight != nullptr) {
-                    float sum = 0.f;
-#pragma unroll
-                    for (int i = 0; i < kPerLane; ++i) sum = __builtin_fmaf(w[i], w[i], sum);
-#pragma unroll
-                    for (int m = 1; m < kLanes; m <<= 1) sum += __shfl_xor(sum, m, kLanes);
-                    const float scale = 1.f / sqrtf(sum * (1.f / D) + a.eps);
-                    float g[kPerLane];
-                    if (a.weight_dtype == GRINQH_BF16) {
-                        RawRow<uint16_t> raw_g;
-                        raw_g.v[0] = reinterpret_cast<const u32x4*>(weight)[lane];
-                        widen<uint16_t>(raw_g, g);
-                    } else {
-                        RawRow<float> raw_g;
-                        raw_g.v[0] = reinterpret_cast<const u32x4*>(weight)[2 * lane];
-                        raw_g.v[1] = reinterpret_cast<const u32x4*>(weight)[2 * lane + 1];
-                        widen<float>(raw_g, g);
-                    }
-#pragma unroll
-                    for (int i = 0; i < kPerLane; ++i) w[i] = w[i] * scale * g[i];
-                }
-                if (a.neighbours) {
-                    if (turned) {
-#pragma unroll
-                        for (int i = 0; i < kPerLane; i += 2) {
-                            const float x = w[i], y = w[i + 1], c = cs[i / 2], s = sn[i / 2];
-                            w[i] = __builtin_fmaf(x, c, -(y * s));
-                            w[i + 1] = __builtin_fmaf(y, c, x * s);
-                        }
-                    }
-                } else {
-                    float other[kPerLane];
-#pragma unroll
-                    for (int i = 0; i < kPerLane; ++i) other[i] = __shfl(w[i], partner, kLanes);
-                    if (turned) {
-#pragma unroll
-                        for (int i = 0; i < kPerLane; ++i) w[i] = __builtin_fmaf(w[i], cs[i], sign * (other[i] * sn[i]));
-                    }
-                }
-                raw = narrow<T>(w);
-                T* to = static_cast<T*>(a.dst[is_q ? 0 : 1]);
-                if (to != nullptr) {
-                    to += token * a.dst_stride[is_q ? 0 : 1] + (is_q ? r : r - a.n_q) * D + lane * kPerLane;
-#pragma unroll
-                    for (unsigned i = 0; i < sizeof(T) / 2; ++i) reinterpret_cast<u32x4*>(to)[i] = raw.v[i];
-                }
-            }
-            if constexpr (BITS != 0) {
-                if (is_q) continue;
-                const int which = is_v ? 1 : 0;
-                const int64_t row = kv_row(a.d, slot, r - a.n_q - which * a.n_kv);
-                if (row < 0) continue;
+        if constexpr (BITS != 0) {
+            const int which = is_v ? 1 : 0;
+            const int64_t row = is_q ? -1 : kv_row(a.d, slots[t], r - a.n_q - which * a.n_kv);
+            if (row >= 0) {
+                uint8_t* codes = is_v ? a.codes[1] : a.codes[0];
                 if constexpr (BITS == 16) {
-                    if constexpr (sizeof(T) == 4) {
-                        const RawRow<uint16_t> kept = narrow<uint16_t>(w);
-                        *reinterpret_cast<u32x4*>(a.codes[which] + row * (D * 2) + lane * 16) = kept.v[0];
-                    } else {
-                        *reinterpret_cast<u32x4*>(a.codes[which] + row * (D * 2) + lane * 16) = raw.v[0];
-                    }
+                    if constexpr (sizeof(T) == 4) raw.v[0] = narrow<uint16_t>(w).v[0];
+                    *reinterpret_cast<u32x4*>(codes + row * (D * 2) + lane * 16) = raw.v[0];
                 } else {
-                    store_quantised_row<D, BITS>(w, a.codes[which], a.grid[which], row, lane);
+                    store_quantised_row<D, BITS>(w, codes, is_v ? a.grid[1] : a.grid[0], row, lane);
                 }
             }
         }
+        t = next_t;
+        r = next_r;
     }
 }
 
 template <int D, typename T, int BITS>
 grinqh_status rope_launch(RopeArgs& a, hipStream_t stream) {
-    constexpr int kItems = kRopeThreads / (D / kPerLane);
-    // Few tokens: a group of lanes for every row.  Many: up to eight rows to a
-    // group, as long as there are two thousand workgroups, so that angles are worked out once for them.
-    const int64_t wanted = (int64_t{2048} * kItems + a.n_tokens - 1) / a.n_tokens;
-    a.parts = static_cast<int>(std::min<int64_t>(a.rows, std::max<int64_t>(wanted, (a.rows + 7) / 8)));
-    const int64_t groups = (a.n_tokens * a.parts + kItems - 1) / kItems;
-    return launch_kernel(rope_kernel<D, T, BITS>, dim3(static_cast<unsigned>(std::min<int64_t>(groups, kMaxRopeGroups))),
-                         kRopeThreads, 0, stream, a);
+    constexpr int kItems = kRopeThreads / (D / kPerLane), kTokens = kMostAngles / (D / 2);
+    // About five rows to a group of lanes: a workgroup's tokens where there are
+    // many, a token's heads over several workgroups where those leave CUs idle.
+    a.tokens = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({kTokens, 5 * kItems / a.rows, a.n_tokens / kFill})));
+    const int64_t groups = (a.n_tokens + a.tokens - 1) / a.tokens;
+    const int parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((a.rows + kItems - 1) / kItems, kFill / groups)));
+    a.step_tokens = parts * kItems / a.rows;
+    a.step_rows = parts * kItems % a.rows;
+    return launch_kernel(rope_kernel<D, T, BITS>, dim3(static_cast<unsigned>(groups), parts), kRopeThreads, 0, stream, a);
 }
 
 template <int D, typename T>
