@@ -12,9 +12,9 @@
 // instructions (codes_to_bf16); products of those with bf16 activations are
 // exact.  With the weights as the first operand a lane holds four outputs of one
 // row (16x16x32 MFMA), and S comes from the same instruction with a first operand
-// of ones, in the same place.  Scales and zero points: each lane has one pair
-// of the tile's (up to four groups x four outputs a quad of lanes), and a broadcast
-// within the 16 lanes of a row (DPP) hands them out.
+// of ones, in the same place.  Scales and zero points: each lane loads one pair
+// of the tile's (up to four groups x four outputs a quad of lanes), and LDS or a
+// broadcast within 16 lanes (DPP) hands them out.
 //
 // fp32 activations are split into three bf16 (8 + 8 + 8 bits, exact but for what
 // lies below the smallest bf16), which take three neighbouring columns: five rows a pass.
@@ -28,9 +28,11 @@ namespace {
 constexpr int kStreamTilesY = 1 << 15;             // row tiles in a launch's second dimension
 constexpr int kDepth = 4;                          // tiles of codes that a wave has under way (and fp32 tiles split at a time)
 
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
 template <int N>
-__device__ __forceinline__ float row_bcast(float v) {                          // lane N of each 16
-    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x150 + N, 0xF, 0xF, false));
+__device__ __forceinline__ uint32_t row_bcast(uint32_t v) {                    // lane N of each 16
+    return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0x150 + N, 0xF, 0xF, true));
 }
 
 // Three bf16 that add up to x, each as the upper half of a word.  Truncation: no
@@ -81,42 +83,38 @@ __device__ __forceinline__ void load_codes(Codes<R>& c, const WeightAt<R>& at, i
     }
 }
 
-// Adds a tile's products to y[row tile][block of 16 rows]: lane 16 q + c has outputs 4 q .. 4 q + 3 of row c.
-template <int GROUP, int R, int NB>
-__device__ __forceinline__ void multiply(f32x4 (&y)[R][NB], const Codes<R>& c, const bf16x8 (&x)[NB][4]) {
+// Adds a tile's products to y[row tile]: lane 16 q + c has outputs 4 q .. 4 q + 3 of
+// row c.  A group's sum begins at -15.5 S, so what is left is s times it and z
+// times S, with s and z as they are packed (`grid` gives the four pairs): mixed
+// multiply-adds take fp16 operands.
+template <int GROUP, int R, typename Grid>
+__device__ __forceinline__ void multiply(f32x4 (&y)[R], const u32x4 (&code)[R], const bf16x8 (&x)[4], Grid grid) {
     constexpr int NG = kTileIn / GROUP, STEPS = 4 / NG;
     const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
     const uint32_t sixteens = bf16_sixteens();
-    f32x4 sum[NB][NG];
+    f32x4 sum[NG];
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
+    for (int g = 0; g < NG; ++g) {
+        sum[g] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            sum[b][g] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int m = g * STEPS; m < (g + 1) * STEPS; ++m)
-                sum[b][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, x[b][m], sum[b][g], 0, 0, 0);
-        }
+        for (int m = g * STEPS; m < (g + 1) * STEPS; ++m)
+            sum[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, x[m], sum[g], 0, 0, 0);
+    }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         bf16x8 w[4];
 #pragma unroll
-        for (int m = 0; m < 4; ++m) w[m] = codes_to_bf16(c.code[r][m], sixteens);
-        const float s = f16_to_f32(static_cast<uint16_t>(c.grid[r]));
-        const float z = __builtin_fmaf(-kCodeBias, s, f16_to_f32(static_cast<uint16_t>(c.grid[r] >> 16)));
+        for (int m = 0; m < 4; ++m) w[m] = codes_to_bf16(code[r][m], sixteens);
         const auto of_group = [&](auto group) {
             constexpr int G = decltype(group)::value;
-            const float s4[4] = {row_bcast<4 * G>(s), row_bcast<4 * G + 1>(s), row_bcast<4 * G + 2>(s), row_bcast<4 * G + 3>(s)};
-            const float z4[4] = {row_bcast<4 * G>(z), row_bcast<4 * G + 1>(z), row_bcast<4 * G + 2>(z), row_bcast<4 * G + 3>(z)};
+            const u32x4 pairs = grid(r, group);
+            f32x4 t = sum[G] * -kCodeBias;
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                f32x4 t{0.f, 0.f, 0.f, 0.f};
+            for (int m = G * STEPS; m < (G + 1) * STEPS; ++m) t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[m], x[m], t, 0, 0, 0);
 #pragma unroll
-                for (int m = G * STEPS; m < (G + 1) * STEPS; ++m)
-                    t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[m], x[b][m], t, 0, 0, 0);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    y[r][b][i] = __builtin_fmaf(s4[i], t[i], __builtin_fmaf(z4[i], sum[b][G][0], y[r][b][i]));
+            for (int i = 0; i < 4; ++i) {
+                const f16x2 sz = __builtin_bit_cast(f16x2, static_cast<uint32_t>(pairs[i]));
+                y[r][i] = __builtin_fmaf(static_cast<float>(sz[0]), t[i], __builtin_fmaf(static_cast<float>(sz[1]), sum[G][0], y[r][i]));
             }
         };
         of_group(std::integral_constant<int, 0>());
@@ -152,19 +150,19 @@ __device__ __forceinline__ void store_outputs(const FourbitArgs& a, int vector_s
 
 // bf16 activations.  What a wave works on goes through a piece of LDS of its own:
 // rows read in the operand's order would ask for 16 lines an instruction, lane
-// after lane in another one (64 rows 4096 to 14336 took 37 us, 23 so); brought into
+// after lane in another one (64 rows 4096 to 14336 took 37 us so, 23 through LDS); brought into
 // LDS four whole lines at a time, and with them the codes, D tiles are under way
 // without a register held.  XR: rows in fours (4 XR of them).
 template <int R, int XR>
 struct WaveStage {
+    static_assert(XR == 1 || XR == 2 || XR == 4, "16 rows at most, by halves");
     static constexpr int kCodes = XR * 1024, kGrid = kCodes + R * 1024, kBytes = kGrid + R * 256, kLoads = XR + 2 * R;
 };
 
 template <int GROUP, int R, int XR, int W, int D>
-__global__ __launch_bounds__(W * kWave) void fourbit_wave_kernel(FourbitArgs a, int vector_store) {
+__global__ __launch_bounds__(W * kWave, 2) void fourbit_wave_kernel(FourbitArgs a, int vector_store) {
     using S = WaveStage<R, XR>;
-    constexpr int NB = (XR + 3) / 4;
-    constexpr int kRed = W * R * NB * 1024;
+    constexpr int kRed = W * R * 1024;
     __shared__ __attribute__((aligned(1024))) char lds[W * D * S::kBytes > kRed ? W * D * S::kBytes : kRed];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const RunTile run = find_run_tile(a, 4 * XR, blockIdx.z * kStreamTilesY + blockIdx.y, lane);
@@ -194,11 +192,9 @@ __global__ __launch_bounds__(W * kWave) void fourbit_wave_kernel(FourbitArgs a, 
     };
 #pragma unroll
     for (int d = 0; d < D; ++d) bring(d, wave + d * W);
-    f32x4 y[R][NB];
+    f32x4 y[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int b = 0; b < NB; ++b) y[r][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int r = 0; r < R; ++r) y[r] = f32x4{0.f, 0.f, 0.f, 0.f};
     int stage = 0;
     for (int kt = wave; kt < a.k_tiles; kt += W) {
         constexpr int kUnderWay = (D - 1) * S::kLoads;             // loads that may be: those of the stages behind this one
@@ -206,40 +202,38 @@ __global__ __launch_bounds__(W * kWave) void fourbit_wave_kernel(FourbitArgs a, 
         __builtin_amdgcn_s_waitcnt(0x0F70 | (kUnderWay & 15) | (kUnderWay >> 4) << 14);
         asm volatile("" ::: "memory");
         const char* from_lds = mine + stage * S::kBytes;
-        Codes<R> c;
-        bf16x8 x[NB][4];
+        constexpr int NG = kTileIn / GROUP;
+        u32x4 code[R], grid[R][NG];
+        bf16x8 x[4];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            c.code[r] = *reinterpret_cast<const u32x4*>(from_lds + S::kCodes + r * 1024 + lane * 16);
-            c.grid[r] = *reinterpret_cast<const uint32_t*>(from_lds + S::kGrid + r * 256 + lane * 4);
+            code[r] = *reinterpret_cast<const u32x4*>(from_lds + S::kCodes + r * 1024 + lane * 16);
+#pragma unroll
+            for (int g = 0; g < NG; ++g) grid[r][g] = *reinterpret_cast<const u32x4*>(from_lds + S::kGrid + r * 256 + quad * 64 + g * 16);
         }
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-                x[b][m] = *reinterpret_cast<const bf16x8*>(from_lds + chunk_at(XR == 1 ? col & 3 : 16 * b + col, 4 * m + quad));
+        for (int m = 0; m < 4; ++m)                                // the rows again in the columns past them
+            x[m] = *reinterpret_cast<const bf16x8*>(from_lds + chunk_at(col & (4 * XR - 1), 4 * m + quad));
         __builtin_amdgcn_s_waitcnt(0xC07F);                        // lgkmcnt(0): the stage has been read and may be filled again
         asm volatile("" ::: "memory");
         bring(stage, kt + D * W);
         stage = stage + 1 == D ? 0 : stage + 1;
-        multiply<GROUP, R, NB>(y, c, x);
+        multiply<GROUP, R>(y, code, x, [&](int r, auto g) { return grid[r][decltype(g)::value]; });
     }
     __builtin_amdgcn_s_waitcnt(0x0F70);                            // vmcnt(0): nothing is brought into LDS any more
     __syncthreads();
     f32x4* red = reinterpret_cast<f32x4*>(lds);
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int b = 0; b < NB; ++b) red[(wave * R * NB + r * NB + b) * kWave + lane] = y[r][b];
+    for (int r = 0; r < R; ++r) red[(wave * R + r) * kWave + lane] = y[r];
     __syncthreads();
-    for (int rb = wave; rb < R * NB; rb += W) {
-        f32x4 sum = red[rb * kWave + lane];
+    for (int r = wave; r < R; r += W) {
+        f32x4 sum = red[r * kWave + lane];
 #pragma unroll
-        for (int w = 1; w < W; ++w) sum += red[(w * R * NB + rb) * kWave + lane];
-        const int t = 16 * (rb % NB) + col, j = (tile0 + rb / NB) * kTileOut + 4 * quad;
-        if (t >= run.count || j >= a.d_out) continue;
-        if (source_row(a, run.row + t) < 0) sum = f32x4{0.f, 0.f, 0.f, 0.f};
-        store_outputs(a, vector_store, run.row + t, j, sum);
+        for (int w = 1; w < W; ++w) sum += red[(w * R + r) * kWave + lane];
+        const int j = (tile0 + r) * kTileOut + 4 * quad;
+        if (col >= run.count || j >= a.d_out) continue;
+        if (source_row(a, run.row + col) < 0) sum = f32x4{0.f, 0.f, 0.f, 0.f};
+        store_outputs(a, vector_store, run.row + col, j, sum);
     }
 }
 
@@ -248,7 +242,7 @@ __global__ __launch_bounds__(W * kWave) void fourbit_wave_kernel(FourbitArgs a, 
 // time (eight values a lane) and passes them to the operand's order through a
 // piece of LDS of its own.
 template <int GROUP, int MT, int W>
-__global__ __launch_bounds__(W * kWave) void fourbit_stream_f32_kernel(FourbitArgs a, int vector_store) {
+__global__ __launch_bounds__(W * kWave, 2) void fourbit_stream_f32_kernel(FourbitArgs a, int vector_store) {
     constexpr int kCols = 3 * MT;
     __shared__ u32x4 parts[W][kDepth * 16 * kCols];        // [tile][16-byte chunk of its inputs][column]
     __shared__ f32x4 red[W][kWave];
@@ -283,7 +277,7 @@ __global__ __launch_bounds__(W * kWave) void fourbit_stream_f32_kernel(FourbitAr
     };
     load_x(wave);
 
-    f32x4 y[1][1] = {{f32x4{0.f, 0.f, 0.f, 0.f}}};
+    f32x4 y[1] = {f32x4{0.f, 0.f, 0.f, 0.f}};
     for (int kt = wave; kt < a.k_tiles; kt += kDepth * W) {
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
@@ -304,16 +298,20 @@ __global__ __launch_bounds__(W * kWave) void fourbit_stream_f32_kernel(FourbitAr
         for (int d = 0; d < kDepth; ++d) {
             const int now = kt + d * W;
             if (now < a.k_tiles) {
-                bf16x8 x[1][4];
+                bf16x8 x[4];
 #pragma unroll
                 for (int m = 0; m < 4; ++m)
-                    x[0][m] = __builtin_bit_cast(bf16x8, parts[wave][(16 * d + 4 * m + quad) * kCols + min(col, kCols - 1)]);
-                multiply<GROUP, 1, 1>(y, ring[d], x);
+                    x[m] = __builtin_bit_cast(bf16x8, parts[wave][(16 * d + 4 * m + quad) * kCols + min(col, kCols - 1)]);
+                const uint32_t mine = ring[d].grid[0];
+                multiply<GROUP, 1>(y, ring[d].code, x, [&](int, auto g) {
+                    constexpr int at = 4 * decltype(g)::value;
+                    return u32x4{row_bcast<at>(mine), row_bcast<at + 1>(mine), row_bcast<at + 2>(mine), row_bcast<at + 3>(mine)};
+                });
                 if (now + kDepth * W < a.k_tiles) load_codes<GROUP>(ring[d], at, now + kDepth * W);
             }
         }
     }
-    red[wave][lane] = y[0][0];
+    red[wave][lane] = y[0];
     __syncthreads();
     if (wave != 0) return;
     f32x4 sum = red[0][lane];
@@ -356,14 +354,31 @@ int64_t expected_tiles(const FourbitArgs& a, int tm) {
 // Which kernel, by the sizes that the host knows.  Times in us on 256 CUs, groups
 // of 128, of codes that come from memory:
 //                          wave kernel   64-row tiles   128-row tiles
-//   4096 to 4096, 256 rows     22.6          38.8           59
-//   4096 to 14336, 128 rows    42.8          40.0           61
-//   4096 to 14336, 256 rows    73            42.6           63
-//   4096 to 14336, 1024 rows   280           168            141
-//   14336 to 4096, 1024 rows   230           151            198
-// A step of 128 inputs takes a 64-row tile 1.3 us and a 128-row tile 2.1, whether
+//   4096 to 4096, 512 rows     37             41             61
+//   4096 to 4096, 1024 rows    73             47             63
+//   4096 to 14336, 128 rows    36             40             61
+//   4096 to 14336, 192 rows    55             41             62
+//   4096 to 14336, 1024 rows   267            157            131
+// A step of 128 inputs takes a 64-row tile 1.25 us and a 128-row tile 2, whether
 // few of them run or one on every CU; the wave kernel takes 0.15 ns for 16 rows x
-// 16 outputs x 128 inputs where there are enough of them to fill the card.
+// 16 outputs x 128 inputs where there are enough of them to fill the card.  Smaller
+// groups cost all of them 8 and 35 % more.
+//
+// Of the wave kernels, the wider and taller one where it leaves work for every CU (us;
+// R W: outputs in sixteens and waves of a workgroup):
+//                                  tiles   1 8    2 8    2 4    4 4
+//   1 row 4096 to 4096               256   3.9    5.0    5.3    7.3
+//   8 rows 4096 to 8192              512   6.4    5.6    5.8    7.6
+//   8 rows 4096 to 14336             896   10.7   8.7    8.2    8.3
+//   8 rows 8192 to 28672, g 64      1792   37     29     28.7   27.5
+//   16 rows 4096 to 4096             256   4.6    5.7    5.9    7.8
+//   16 rows 4096 to 8192             512   8.3    6.2    6.3    8.0
+//   16 rows 2048 to 11008, g 64      688   9.2    7.9    6.3    6.2
+//   16 rows 8192 to 28672, g 64     1792   51     39     35     30
+//   64 rows 4096 to 4096            1024          9.7    8.0    7.7
+// and of four, eight and sixteen rows the fewest that hold a call's: one row 4096 to
+// 4096 takes 3.9, 4.0 and 4.3 us, 16 rows to 64 experts 4096 to 1024 9.3 us in
+// eights and 9.9 in sixteens, 516 rows to 64 experts 73 in eights and 51 in sixteens.
 template <int GROUP>
 grinqh_status stream_group(const FourbitArgs& a, int x_dtype, int vector_store, hipStream_t stream) {
     const int64_t rows = a.n_rows / a.n_experts;                   // of an expert, on average
@@ -371,23 +386,19 @@ grinqh_status stream_group(const FourbitArgs& a, int x_dtype, int vector_store, 
         if (rows <= 1) return stream_f32_launch<GROUP, 1, 16>(a, vector_store, stream);
         return stream_f32_launch<GROUP, 5, 8>(a, vector_store, stream);
     }
-    const int64_t pieces = expected_tiles(a, 16) * a.row_tiles;
     const auto rounds = [&](int tm) { return (expected_tiles(a, tm) * ((a.d_out + 255) / 256) + 255) / 256; };
-    const double waves = 0.15e-3 * pieces, small = 1.3 * rounds(64), large = 2.1 * rounds(128);
+    const auto tiles = [&](int tm) { return expected_tiles(a, tm) * a.row_tiles; };
+    const double waves = 0.15e-3 * tiles(16), small = 1.25 * rounds(64), large = 2.0 * rounds(128);
     if (std::min(small, large) < waves) return launch_fourbit_tile(a, GROUP, small <= large ? 64 : 128, stream);
-    // Up to four rows: a quarter of the rows' traffic, and the least to do before the
-    // first product (one row 4096 to 4096: 4.3 us, 5.0 through 16 rows).
-    if (rows <= 4 && (a.ends == nullptr || rows <= 2)) {
-        if (a.row_tiles * expected_tiles(a, 4) <= 512) return wave_launch<GROUP, 1, 1, 8, 4>(a, vector_store, stream);
-        return wave_launch<GROUP, 1, 1, 4, 4>(a, vector_store, stream);        // 8192 to 28672: 25 us, 27 with eight waves
+    if (a.ends == nullptr ? rows <= 8 : rows <= 2) {
+        if (a.ends == nullptr && rows <= 4 && tiles(4) <= 320) return wave_launch<GROUP, 1, 1, 8, 4>(a, vector_store, stream);
+        if (tiles(8) <= 320) return wave_launch<GROUP, 1, 2, 8, 3>(a, vector_store, stream);
+        if (tiles(8) <= 576) return wave_launch<GROUP, 2, 2, 8, 2>(a, vector_store, stream);
+        return wave_launch<GROUP, 2, 2, 4, 2>(a, vector_store, stream);
     }
-    // Wider and taller where that leaves work for every CU (16 rows, R1 / R2 / R4: 4096
-    // to 4096 5.3 / 6.2 / 9.2, 4096 to 14336 16 / 10.3 / 10.0).
-    if (pieces <= 320) return wave_launch<GROUP, 1, 4, 8, 2>(a, vector_store, stream);
-    if (pieces <= 640) return wave_launch<GROUP, 2, 4, 8, 2>(a, vector_store, stream);
-    if (rows <= 16) return wave_launch<GROUP, 4, 4, 4, 2>(a, vector_store, stream);
-    if (pieces <= 1280) return wave_launch<GROUP, 2, 8, 4, 2>(a, vector_store, stream);
-    return wave_launch<GROUP, 4, 8, 4, 2>(a, vector_store, stream);
+    if (tiles(16) <= 320) return wave_launch<GROUP, 1, 4, 8, 2>(a, vector_store, stream);
+    if (tiles(16) <= 576) return wave_launch<GROUP, 2, 4, 8, 2>(a, vector_store, stream);
+    return wave_launch<GROUP, 4, 4, 4, 2>(a, vector_store, stream);
 }
 
 // Host checks of a product, and its kernel.
