@@ -205,6 +205,7 @@ class KVCache:
         self.n_kv_heads, self.head_dim = layout.n_kv_heads, layout.head_dim
         self._pools = KVPools(*pools)
         self._refs = ctypes.byref(layout), ctypes.byref(self._pools)
+        self._pointers = ctypes.pointer(layout), ctypes.pointer(self._pools)
 
 
 def new_kv_cache(n_kv_heads: int, head_dim: int, page_size: int, n_pages: int, bits: int, device=None) -> KVCache:

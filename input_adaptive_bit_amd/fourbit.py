@@ -180,12 +180,18 @@ def fourbit_quantize(w, group: int, stream=None) -> FourbitWeight:
     return fourbit_pack(q.view(w.shape), s.view(shape), z.view(shape))
 
 
+def _outputs(x, n, width, dtype, device, stream):
+    if stream is None and dtype in (None, x.dtype) and x.dtype is torch.bfloat16 and x.device == device:
+        return x.new_empty((n, width))           # the shorter way there
+    return _empty((n, width), dtype or torch.bfloat16, device, stream)
+
+
 def fourbit_linear(weight: FourbitWeight, x, out_dtype=None, stream=None):
     """y [tokens][d_out] = x [tokens][d_in] times the weights (allocates y; bf16 unless asked otherwise)."""
     device = weight.device
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError(f"x must be a [tokens][{weight.d_in}] tensor")
-    y = _empty((x.shape[0], weight.d_out), out_dtype or torch.bfloat16, device, stream)
+    y = _outputs(x, x.shape[0], weight.d_out, out_dtype, device, stream)
     grinqh_fourbit_linear(weight, x, y, stream)
     return y
 
@@ -197,6 +203,6 @@ def expert_linear(weight: FourbitWeight, x, ends, rows=None, out_dtype=None, str
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError(f"x must be a [rows][{weight.d_in}] tensor")
     n = x.shape[0] if rows is None else rows.numel()
-    y = _empty((n, weight.d_out), out_dtype or torch.bfloat16, device, stream)
+    y = _outputs(x, n, weight.d_out, out_dtype, device, stream)
     grinqh_expert_linear(weight, x, ends, y, rows, stream)
     return y

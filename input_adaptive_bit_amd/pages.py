@@ -51,10 +51,11 @@ def _plan(page_table, seq_lens, n_new, free_pages, n_free):
     try:
         device, (batch,) = seq_lens.device, seq_lens.shape
         index, (rows, columns), (stride, s1) = device.index, page_table.shape, page_table.stride()
-        fits = rows == batch and (s1 == 1 or columns < 2) and (batch < 2 or stride >= columns) and n_new.numel() == batch
-        for t in (page_table, seq_lens, n_new, free_pages, n_free):
-            fits = fits and t.dtype is _I32 and t.get_device() == index and (t is page_table or t.is_contiguous())
-        fits = fits and seq_lens.is_cuda and free_pages.numel() >= 1 and n_free.numel() >= 1
+        fits = (rows == batch and (s1 == 1 or columns < 2) and (batch < 2 or stride >= columns) and n_new.numel() == batch
+                and page_table.dtype is seq_lens.dtype is n_new.dtype is free_pages.dtype is n_free.dtype is _I32
+                and page_table.get_device() == n_new.get_device() == free_pages.get_device() == n_free.get_device() == index
+                and seq_lens.is_contiguous() and n_new.is_contiguous() and free_pages.is_contiguous() and n_free.is_contiguous()
+                and seq_lens.is_cuda and free_pages.numel() >= 1 and n_free.numel() >= 1)
     except (AttributeError, TypeError, ValueError):
         fits = False
     if fits:
@@ -120,21 +121,27 @@ def kv_extend(page_table, seq_lens, n_new, free_pages, n_free, page_size: int, c
     device, batch, columns, inputs = _plan(page_table, seq_lens, n_new, free_pages, n_free)
     if not 0 <= capacity <= 1 << 24:
         raise GrinqhError(GRINQH_EINVAL, "grinqh_kv_extend")
-    # One allocation: slots (8 bytes each), the workspace (on 16 bytes, 8 a sequence and 16), then what is 4 bytes wide.
+    # One allocation: slots (8 bytes each), what is 4 bytes wide, then the workspace (8 bytes a sequence and 16, on 16 bytes).
     # The call needs addresses only, and the library refuses every count that the types could not hold.
-    ws = 2 * batch + 4
-    sizes = (2 * capacity, 2 * capacity & 2, ws, capacity, batch + 1, batch + 1, 0 if in_place else batch, 0 if in_place else 1, 1)
-    both = _empty((sum(sizes),), _I32, device, stream)
-    slots, _, _, positions, cu_q, cu_k, lens, left, refused = both.split(sizes)
+    kept = 0 if in_place else batch
+    before = 3 * capacity + 2 * batch + kept + (3 if in_place else 4)
+    ws = -before % 4 + 2 * batch + 4
+    both = _empty((before + ws,), _I32, device, stream)
+    slots, positions, cu_q, cu_k, lens, left, refused, _ = both.split_with_sizes(
+        (2 * capacity, capacity, batch + 1, batch + 1, kept, 0 if in_place else 1, 1, ws))
     start = both.data_ptr()
-    space = start + 4 * (sizes[0] + sizes[1])
-    at = [space + 4 * ws]                                     # positions, cu_q, cu_k, lens, left, refused
-    for size in sizes[3:8]:
-        at.append(at[-1] + 4 * size)
+    to_positions = start + 8 * capacity
+    to_q = to_positions + 4 * capacity
+    to_k = to_q + 4 * batch + 4
+    to_lens = to_k + 4 * batch + 4
+    to_left = to_lens + 4 * kept
+    space = start + 4 * (before + -before % 4)
     if in_place:
-        lens, left, at[3], at[4] = seq_lens, n_free, inputs[2], inputs[5]
-    a = ExtendArgs(*inputs, _fit(batch), _fit(columns), _fit(page_size), _fit(free_pages.numel()), capacity, at[3], at[4], at[5], at[1], at[2],
-                   start, at[0], space, 4 * ws)
+        lens, left, to_lens, to_left, to_refused = seq_lens, n_free, inputs[2], inputs[5], to_left
+    else:
+        to_refused = to_left + 4
+    a = ExtendArgs(*inputs, _fit(batch), _fit(columns), _fit(page_size), _fit(free_pages.numel()), capacity, to_lens, to_left,
+                   to_refused, to_q, to_k, start, to_positions, space, 8 * batch + 16)
     _run("grinqh_kv_extend", device, stream, ctypes.byref(a))
     return Step(slots.view(_I64), positions, cu_q, cu_k, lens, left, refused)
 

@@ -113,7 +113,7 @@ def grinqh_qk_rope(q, k, positions, freqs, q_out, k_out, q_weight=None, k_weight
                  freqs.data_ptr(), min(2 * freqs.numel(), 1 << 30), bool(neighbours), q_out.data_ptr(),
                  None if k_out is None else k_out.data_ptr(), os, kos)
     if cache is not None:
-        a.cache, a.pools, a.slots = ctypes.pointer(cache.layout), ctypes.pointer(cache._pools), slots.data_ptr()
+        (a.cache, a.pools), a.slots = cache._pointers, slots.data_ptr()
     _run("grinqh_qk_rope", device, stream, ctypes.byref(a))
 
 
@@ -124,9 +124,13 @@ def qk_rope(q, k, positions, freqs, q_weight=None, k_weight=None, eps: float = 1
     position; pairs are (p, p + rope_dim / 2), or with neighbours (2p, 2p + 1).  With a
     cache, keys and values (v) also go into their slots; keys=False then leaves
     the rotated keys to the cache alone (k is None in the result)."""
-    device = _tensor(q, "q")
-    _tensor(k, "k", device)
-    q_out = _empty(q.shape, q.dtype, device, stream)
-    k_out = _empty(k.shape, k.dtype, device, stream) if keys else None
+    if stream is None and isinstance(q, torch.Tensor) and isinstance(k, torch.Tensor) and q.is_cuda and k.is_cuda:
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)       # the shorter way there
+        k_out = torch.empty_like(k, memory_format=torch.contiguous_format) if keys else None
+    else:
+        device = _tensor(q, "q")
+        _tensor(k, "k", device)
+        q_out = _empty(q.shape, q.dtype, device, stream)
+        k_out = _empty(k.shape, k.dtype, device, stream) if keys else None
     grinqh_qk_rope(q, k, positions, freqs, q_out, k_out, q_weight, k_weight, eps, neighbours, cache, v, slots, stream)
     return q_out, k_out
