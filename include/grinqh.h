@@ -515,8 +515,8 @@ grinqh_status grinqh_fourbit_pack(const grinqh_fourbit_layout* L, const uint8_t*
  *   y          [n_tokens][d_out] of y_dtype, contiguous, overwritten; bf16 output is
  *              the fp32 result rounded to nearest even.
  * Codes enter the products exactly and activations as they are (fp32 ones as
- * the sum of three bf16; many tokens of fp32 are worked on five at a time, so a
- * long prompt is better in bf16); sums are fp32, and the same call gives the
+ * the sum of three bf16; many tokens of fp32 are worked on sixteen at a time, so
+ * a long prompt is better in bf16); sums are fp32, and the same call gives the
  * same bits.  An infinite or NaN activation makes its token's outputs
  * non-finite and no other's, and so may one past 2^115.  y must not overlap
  * anything that is read. */

@@ -17,7 +17,8 @@
 // broadcast within 16 lanes (DPP) hands them out.
 //
 // fp32 activations are split into three bf16 (8 + 8 + 8 bits, exact but for what
-// lies below the smallest bf16), which take three neighbouring columns: five rows a pass.
+// lies below the smallest bf16): each part a product of its own, or for few rows and
+// outputs three neighbouring columns of one.
 #include <algorithm>
 
 #include "fourbit_common.hpp"
@@ -35,16 +36,25 @@ __device__ __forceinline__ uint32_t row_bcast(uint32_t v) {                    /
     return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0x150 + N, 0xF, 0xF, true));
 }
 
-// Three bf16 that add up to x, each as the upper half of a word.  Truncation: no
-// part rounds up past the largest float.  What is not finite is all in the first.
-__device__ __forceinline__ void split(float x, uint32_t (&part)[3]) {
-    const uint32_t bits = __float_as_uint(x), hi = bits & 0xFFFF0000u;
-    const float rest = x - __uint_as_float(hi);
-    const uint32_t mid = __float_as_uint(rest) & 0xFFFF0000u;
-    const bool finite = (bits & 0x7F800000u) != 0x7F800000u;
-    part[0] = x != x ? 0x7FC00000u : hi;                                       // a NaN's bits may all lie in the lower half
-    part[1] = finite ? mid : 0u;
-    part[2] = finite ? __float_as_uint(rest - __uint_as_float(mid)) & 0xFFFF0000u : 0u;
+// Eight floats as the sum of three bf16 each, cut off one after another: the upper
+// halves of x, of what is left, and of what is left then.
+__device__ __forceinline__ void split_eight(const f32x4& low, const f32x4& high, bf16x8& a, bf16x8& b, bf16x8& c) {
+    u32x4 part[3];
+    uint32_t word[3][2];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float x = i < 4 ? low[i & 3] : high[i & 3];
+        const float rest = x - __uint_as_float(__float_as_uint(x) & 0xFFFF0000u);
+        word[0][i & 1] = __float_as_uint(x);
+        word[1][i & 1] = __float_as_uint(rest);
+        word[2][i & 1] = __float_as_uint(rest - __uint_as_float(__float_as_uint(rest) & 0xFFFF0000u));
+        if (i & 1)
+#pragma unroll
+            for (int p = 0; p < 3; ++p) part[p][i >> 1] = __builtin_amdgcn_perm(word[p][1], word[p][0], 0x07060302u);
+    }
+    a = __builtin_bit_cast(bf16x8, part[0]);
+    b = __builtin_bit_cast(bf16x8, part[1]);
+    c = __builtin_bit_cast(bf16x8, part[2]);
 }
 
 // Codes of a tile of R x 16 outputs, and this lane's (s, z) pair of each.
@@ -87,8 +97,9 @@ __device__ __forceinline__ void load_codes(Codes<R>& c, const WeightAt<R>& at, i
 // row c.  A group's sum begins at -15.5 S, so what is left is s times it and z
 // times S, with s and z as they are packed (`grid` gives the four pairs): mixed
 // multiply-adds take fp16 operands.
-template <int GROUP, int R, typename Grid>
-__device__ __forceinline__ void multiply(f32x4 (&y)[R], const u32x4 (&code)[R], const bf16x8 (&x)[4], Grid grid) {
+// P: bf16 that an activation is the sum of, the largest first.
+template <int GROUP, int R, int P, typename Grid>
+__device__ __forceinline__ void multiply(f32x4 (&y)[R], const u32x4 (&code)[R], const bf16x8 (&x)[P][4], Grid grid) {
     constexpr int NG = kTileIn / GROUP, STEPS = 4 / NG;
     const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
     const uint32_t sixteens = bf16_sixteens();
@@ -97,8 +108,8 @@ __device__ __forceinline__ void multiply(f32x4 (&y)[R], const u32x4 (&code)[R], 
     for (int g = 0; g < NG; ++g) {
         sum[g] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int m = g * STEPS; m < (g + 1) * STEPS; ++m)
-            sum[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, x[m], sum[g], 0, 0, 0);
+        for (int i = P * g * STEPS; i < P * (g + 1) * STEPS; ++i)
+            sum[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, x[P - 1 - i % P][i / P], sum[g], 0, 0, 0);
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -110,7 +121,8 @@ __device__ __forceinline__ void multiply(f32x4 (&y)[R], const u32x4 (&code)[R], 
             const u32x4 pairs = grid(r, group);
             f32x4 t = sum[G] * -kCodeBias;
 #pragma unroll
-            for (int m = G * STEPS; m < (G + 1) * STEPS; ++m) t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[m], x[m], t, 0, 0, 0);
+            for (int i = P * G * STEPS; i < P * (G + 1) * STEPS; ++i)
+                t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i / P], x[P - 1 - i % P][i / P], t, 0, 0, 0);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const f16x2 sz = __builtin_bit_cast(f16x2, static_cast<uint32_t>(pairs[i]));
@@ -155,27 +167,34 @@ __device__ __forceinline__ void store_outputs(const FourbitArgs& a, int vector_s
 // without a register held.  XR: rows in fours (4 XR of them).
 template <int R, int XR>
 struct WaveStage {
-    static_assert(XR == 1 || XR == 2 || XR == 4, "16 rows at most, by halves");
     static constexpr int kCodes = XR * 1024, kGrid = kCodes + R * 1024, kBytes = kGrid + R * 256, kLoads = XR + 2 * R;
 };
 
-template <int GROUP, int R, int XR, int W, int D>
+template <int GROUP, typename T, int R, int XR, int W, int D>
 __global__ __launch_bounds__(W * kWave, 2) void fourbit_wave_kernel(FourbitArgs a, int vector_store) {
     using S = WaveStage<R, XR>;
     constexpr int kRed = W * R * 1024;
     __shared__ __attribute__((aligned(1024))) char lds[W * D * S::kBytes > kRed ? W * D * S::kBytes : kRed];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const RunTile run = find_run_tile(a, 4 * XR, blockIdx.z * kStreamTilesY + blockIdx.y, lane);
+    constexpr bool kF32 = sizeof(T) == 4;
+    constexpr int kLineLanes = kF32 ? 32 : 16, kPiece = 16 / sizeof(T);        // lanes that bring a row's 128 inputs, of a lane
+    constexpr int kRows = XR * kWave / kLineLanes;
+    static_assert(kRows <= 16 && (kRows & (kRows - 1)) == 0, "rows that divide the columns of a matrix tile");
+    const RunTile run = find_run_tile(a, kRows, blockIdx.z * kStreamTilesY + blockIdx.y, lane);
     if (run.count <= 0) return;
     const int col = lane & 15, quad = lane >> 4, tile0 = blockIdx.x * R;
     const WeightAt<R> at = weight_at<GROUP, R>(a, run.expert, tile0, lane);
     // Rows past the run read its last one, rows gathered from nowhere the first of
     // x (and are stored as zeros); inputs past the last read the row's last
     // ones, and the padded groups' s and z of zero take them out.
-    const uint16_t* from[XR];
+    const T* from[XR];
+    int piece[XR];
 #pragma unroll
-    for (int i = 0; i < XR; ++i)
-        from[i] = static_cast<const uint16_t*>(a.x) + max(source_row(a, run.row + min(4 * i + quad, run.count - 1)), 0) * a.x_stride;
+    for (int i = 0; i < XR; ++i) {
+        const int r = i * (kWave / kLineLanes) + lane / kLineLanes;
+        from[i] = static_cast<const T*>(a.x) + max(source_row(a, run.row + min(r, run.count - 1)), 0) * a.x_stride;
+        piece[i] = kPiece * (lane % kLineLanes ^ (r & 15));
+    }
     char* mine = lds + wave * (D * S::kBytes);
     const uint32_t lds0 = lds_address(mine);
     const auto bring = [&](int stage, int kt) {
@@ -183,7 +202,7 @@ __global__ __launch_bounds__(W * kWave, 2) void fourbit_wave_kernel(FourbitArgs 
         const uint32_t to = lds0 + stage * S::kBytes;
 #pragma unroll
         for (int i = 0; i < XR; ++i)
-            load_to_lds(from[i] + min(kt * kTileIn + 8 * (col ^ ((4 * i + quad) & 15)), a.d_in - 8), to + i * 1024);
+            load_to_lds(from[i] + min(kt * kTileIn + piece[i], a.d_in - kPiece), to + i * 1024);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             load_to_lds(at.codes[r] + static_cast<int64_t>(kt) * 1024, to + S::kCodes + r * 1024);
@@ -204,21 +223,30 @@ __global__ __launch_bounds__(W * kWave, 2) void fourbit_wave_kernel(FourbitArgs 
         const char* from_lds = mine + stage * S::kBytes;
         constexpr int NG = kTileIn / GROUP;
         u32x4 code[R], grid[R][NG];
-        bf16x8 x[4];
+        bf16x8 x[kF32 ? 3 : 1][4];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             code[r] = *reinterpret_cast<const u32x4*>(from_lds + S::kCodes + r * 1024 + lane * 16);
 #pragma unroll
             for (int g = 0; g < NG; ++g) grid[r][g] = *reinterpret_cast<const u32x4*>(from_lds + S::kGrid + r * 256 + quad * 64 + g * 16);
         }
+        const int row = col & (kRows - 1);                         // the rows again in the columns past them
 #pragma unroll
-        for (int m = 0; m < 4; ++m)                                // the rows again in the columns past them
-            x[m] = *reinterpret_cast<const bf16x8*>(from_lds + chunk_at(col & (4 * XR - 1), 4 * m + quad));
+        for (int m = 0; m < 4; ++m) {
+            if constexpr (kF32) {
+                const char* at = from_lds + row * 512;
+                const f32x4 low = *reinterpret_cast<const f32x4*>(at + (8 * m + 2 * quad ^ row) * 16);
+                const f32x4 high = *reinterpret_cast<const f32x4*>(at + (8 * m + 2 * quad + 1 ^ row) * 16);
+                split_eight(low, high, x[0][m], x[1][m], x[2][m]);
+            } else {
+                x[0][m] = *reinterpret_cast<const bf16x8*>(from_lds + chunk_at(row, 4 * m + quad));
+            }
+        }
         __builtin_amdgcn_s_waitcnt(0xC07F);                        // lgkmcnt(0): the stage has been read and may be filled again
         asm volatile("" ::: "memory");
         bring(stage, kt + D * W);
         stage = stage + 1 == D ? 0 : stage + 1;
-        multiply<GROUP, R>(y, code, x, [&](int r, auto g) { return grid[r][decltype(g)::value]; });
+        multiply<GROUP, R, kF32 ? 3 : 1>(y, code, x, [&](int r, auto g) { return grid[r][decltype(g)::value]; });
     }
     __builtin_amdgcn_s_waitcnt(0x0F70);                            // vmcnt(0): nothing is brought into LDS any more
     __syncthreads();
@@ -263,15 +291,15 @@ __global__ __launch_bounds__(W * kWave, 2) void fourbit_stream_f32_kernel(Fourbi
         const int src = t < run.count ? source_row(a, run.row + t) : -1;
         from[t] = src < 0 ? nullptr : static_cast<const float*>(a.x) + src * a.x_stride + 8 * col;
     }
-    u32x4 raw[MT][2];
+    f32x4 raw[MT][2];
     const auto load_x = [&](int kt) {
         const int k = (kt + quad * W) * kTileIn;
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
-            raw[t][0] = raw[t][1] = u32x4{0u, 0u, 0u, 0u};
+            raw[t][0] = raw[t][1] = f32x4{0.f, 0.f, 0.f, 0.f};
             if (from[t] != nullptr && k + 8 * col < a.d_in) {
-                raw[t][0] = *reinterpret_cast<const u32x4*>(from[t] + k);
-                raw[t][1] = *reinterpret_cast<const u32x4*>(from[t] + k + 4);
+                raw[t][0] = *reinterpret_cast<const f32x4*>(from[t] + k);
+                raw[t][1] = *reinterpret_cast<const f32x4*>(from[t] + k + 4);
             }
         }
     };
@@ -281,29 +309,22 @@ __global__ __launch_bounds__(W * kWave, 2) void fourbit_stream_f32_kernel(Fourbi
     for (int kt = wave; kt < a.k_tiles; kt += kDepth * W) {
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
-            u32x4 part[3];
+            bf16x8 part[3];
+            split_eight(raw[t][0], raw[t][1], part[0], part[1], part[2]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t even[3], odd[3];
-                split(__uint_as_float(raw[t][i >> 1][2 * (i & 1)]), even);
-                split(__uint_as_float(raw[t][i >> 1][2 * (i & 1) + 1]), odd);
-#pragma unroll
-                for (int p = 0; p < 3; ++p) part[p][i] = even[p] >> 16 | odd[p];
-            }
-#pragma unroll
-            for (int p = 0; p < 3; ++p) parts[wave][lane * kCols + 3 * t + p] = part[p];
+            for (int p = 0; p < 3; ++p) parts[wave][lane * kCols + 3 * t + p] = __builtin_bit_cast(u32x4, part[p]);
         }
         load_x(kt + kDepth * W);
 #pragma unroll
         for (int d = 0; d < kDepth; ++d) {
             const int now = kt + d * W;
             if (now < a.k_tiles) {
-                bf16x8 x[4];
+                bf16x8 x[1][4];
 #pragma unroll
                 for (int m = 0; m < 4; ++m)
-                    x[m] = __builtin_bit_cast(bf16x8, parts[wave][(16 * d + 4 * m + quad) * kCols + min(col, kCols - 1)]);
+                    x[0][m] = __builtin_bit_cast(bf16x8, parts[wave][(16 * d + 4 * m + quad) * kCols + min(col, kCols - 1)]);
                 const uint32_t mine = ring[d].grid[0];
-                multiply<GROUP, 1>(y, ring[d].code, x, [&](int, auto g) {
+                multiply<GROUP, 1, 1>(y, ring[d].code, x, [&](int, auto g) {
                     constexpr int at = 4 * decltype(g)::value;
                     return u32x4{row_bcast<at>(mine), row_bcast<at + 1>(mine), row_bcast<at + 2>(mine), row_bcast<at + 3>(mine)};
                 });
@@ -337,7 +358,11 @@ dim3 stream_grid(const FourbitArgs& a, int rows, int outputs) {
 
 template <int GROUP, int R, int XR, int W, int D>
 grinqh_status wave_launch(const FourbitArgs& a, int vector_store, hipStream_t stream) {
-    return launch_kernel(fourbit_wave_kernel<GROUP, R, XR, W, D>, stream_grid(a, 4 * XR, R), W * kWave, 0, stream, a, vector_store);
+    return launch_kernel(fourbit_wave_kernel<GROUP, uint16_t, R, XR, W, D>, stream_grid(a, 4 * XR, R), W * kWave, 0, stream, a, vector_store);
+}
+template <int GROUP, int R, int XR, int W, int D>
+grinqh_status wave_f32_launch(const FourbitArgs& a, int vector_store, hipStream_t stream) {
+    return launch_kernel(fourbit_wave_kernel<GROUP, float, R, XR, W, D>, stream_grid(a, 2 * XR, R), W * kWave, 0, stream, a, vector_store);
 }
 
 template <int GROUP, int MT, int W>
@@ -379,15 +404,33 @@ int64_t expected_tiles(const FourbitArgs& a, int tm) {
 // and of four, eight and sixteen rows the fewest that hold a call's: one row 4096 to
 // 4096 takes 3.9, 4.0 and 4.3 us, 16 rows to 64 experts 4096 to 1024 9.3 us in
 // eights and 9.9 in sixteens, 516 rows to 64 experts 73 in eights and 51 in sixteens.
+//
+// fp32 (us): the kernel that splits in few lanes where a CU's waves work on one tile
+// of outputs, else the wave kernel, of 8 or 16 rows, one or four sixteens of outputs wide.
+//                                  tiles   few lanes   1 wide   4 wide
+//   1 row 4096 to 4096               256   4.3         7.5      11.6
+//   1 row 4096 to 8192               512   7.7         13.1     11.7
+//   1 row 4096 to 14336              896   12.7        23.8     12.3
+//   5 rows 4096 to 4096              256   5.5         7.4      11.4
+//   5 rows 4096 to 8192              512   10.6        12.9     11.6
+//   5 rows 4096 to 14336             896   19.3        23.9     12.0
+//   16 rows 4096 to 4096             256               8.6      13.0
+//   16 rows 4096 to 14336            896               27       13.3
 template <int GROUP>
 grinqh_status stream_group(const FourbitArgs& a, int x_dtype, int vector_store, hipStream_t stream) {
     const int64_t rows = a.n_rows / a.n_experts;                   // of an expert, on average
+    const auto tiles = [&](int tm) { return expected_tiles(a, tm) * a.row_tiles; };
     if (x_dtype == GRINQH_F32) {
-        if (rows <= 1) return stream_f32_launch<GROUP, 1, 16>(a, vector_store, stream);
-        return stream_f32_launch<GROUP, 5, 8>(a, vector_store, stream);
+        if (rows <= 1 && tiles(1) <= 640) return stream_f32_launch<GROUP, 1, 16>(a, vector_store, stream);
+        if (rows <= 5 && tiles(5) <= 640) return stream_f32_launch<GROUP, 5, 8>(a, vector_store, stream);
+        if (a.ends == nullptr ? rows <= 8 : rows <= 2) {
+            if (tiles(8) <= 400) return wave_f32_launch<GROUP, 1, 4, 8, 2>(a, vector_store, stream);
+            return wave_f32_launch<GROUP, 4, 4, 4, 2>(a, vector_store, stream);
+        }
+        if (tiles(16) <= 400) return wave_f32_launch<GROUP, 1, 8, 8, 2>(a, vector_store, stream);
+        return wave_f32_launch<GROUP, 4, 8, 4, 2>(a, vector_store, stream);
     }
     const auto rounds = [&](int tm) { return (expected_tiles(a, tm) * ((a.d_out + 255) / 256) + 255) / 256; };
-    const auto tiles = [&](int tm) { return expected_tiles(a, tm) * a.row_tiles; };
     const double waves = 0.15e-3 * tiles(16), small = 1.25 * rounds(64), large = 2.0 * rounds(128);
     if (std::min(small, large) < waves) return launch_fourbit_tile(a, GROUP, small <= large ? 64 : 128, stream);
     if (a.ends == nullptr ? rows <= 8 : rows <= 2) {

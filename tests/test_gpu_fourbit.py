@@ -100,6 +100,15 @@ def test_sizes_of_real_layers(dev, n, d_in, d_out, group):
     check_linear(dev, np.random.default_rng(n), n, d_in, d_out, group, "bf16", "f32")
 
 
+@pytest.mark.parametrize("x_dtype,n", [("bf16", 3), ("bf16", 7), ("bf16", 13), ("bf16", 90), ("f32", 1), ("f32", 4), ("f32", 7), ("f32", 13),
+                                       ("f32", 40)])
+@pytest.mark.parametrize("d_out,d_in,group", [(401, 288, 32), (8002, 192, 64), (12003, 256, 128)])
+def test_few_and_many_outputs(dev, x_dtype, n, d_out, d_in, group):
+    """Which kernel runs depends on the outputs too: narrow, wider and wide ones, with rows that do not fill them."""
+    say(f"fourbit_linear n={n} {d_in}->{d_out} group={group} {x_dtype}")
+    check_linear(dev, np.random.default_rng(n), n, d_in, d_out, group, x_dtype, "f32")
+
+
 def test_quantised_weights_are_the_rtn_of_each_group(dev):
     """fourbit_quantize against the weights' own rounding, and the product against both."""
     import input_adaptive_bit_amd as G
@@ -117,6 +126,21 @@ def test_quantised_weights_are_the_rtn_of_each_group(dev):
     again = G.fourbit_quantize(to_type(w, "bf16", dev), 64, stream=other)
     other.synchronize()
     assert torch.equal(again.codes, packed.codes) and torch.equal(again.grid, packed.grid)
+
+
+@pytest.mark.parametrize("x_dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [6, 14])
+def test_rows_behind_the_last_do_not_matter(dev, x_dtype, n):
+    """Columns that no row fills hold some row again: whatever lies behind x has no effect, and nothing behind y changes."""
+    import input_adaptive_bit_amd as G
+    import torch
+    rng = np.random.default_rng(n)
+    q, s, z = make(rng, 1, 256, 9000, 64)
+    w = pack(q[0], s[0], z[0], dev)
+    x = to_type(activations(rng, n + 40, 256, x_dtype), x_dtype, dev)
+    y = G.fourbit_linear(w, x[:n].clone(), torch.float32)
+    x[n:] = float("nan")
+    assert torch.equal(G.fourbit_linear(w, x[:n], torch.float32), y)
 
 
 def ends_of(counts, lead=0):
