@@ -277,13 +277,13 @@ __global__ __launch_bounds__(kTileThreads) void fourbit_tile_kernel(FourbitArgs 
 #pragma unroll
         for (int g = 0; g < NG; ++g) scale[g] = scale_next[g];
         turn = next_turn;
-        // Before the others may go on: the rows brought in the step before are in LDS
-        // (of the loads to memory only this step's may be under way), and so are the
-        // sums (of the LDS operations only the last four, all of them reads).
+        // Before the others may go on: the rows that this step brought are in LDS
+        // (the next step sums them up and reads its last operands from them), and so
+        // are the sums (of the LDS operations only the last four may be under way,
+        // all of them reads).
         asm volatile("" ::: "memory");
-        constexpr int kLoads = S::kSteps + 2 + NG;
-        static_assert(kLoads < 16 && 2 * TC <= 4, "counts that the wait can name, and reads at the end of a step");
-        __builtin_amdgcn_s_waitcnt(0x0070 | 4 << 8 | kLoads);
+        static_assert(2 * TC <= 4, "reads at the end of a step");
+        __builtin_amdgcn_s_waitcnt(0x0070 | 4 << 8);
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
     }
@@ -294,9 +294,8 @@ __global__ __launch_bounds__(kTileThreads) void fourbit_tile_kernel(FourbitArgs 
 
     // Out: 32 rows at a time through LDS, so that a wave stores whole stretches of
     // them (2048 rows 4096 to 14336: 278 us, 289 element by element).  The rows lie 32 bytes apart from multiples of 256: a lane
-    // pair's rows, 4 apart, fall on different banks.
-    __builtin_amdgcn_s_waitcnt(0x0F70);                            // vmcnt(0): no rows are brought any more
-    asm volatile("" ::: "memory");
+    // pair's rows, 4 apart, fall on different banks.  No rows are brought any more:
+    // the last step has waited for them.
     constexpr int kOutStride = S::TN * 4 + 32;
     static_assert(32 * kOutStride <= 3 * S::kBytes, "the rows' buffers hold 32 rows of the result");
     char* out = &xs[0][0];
@@ -325,7 +324,7 @@ grinqh_status tile_launch(const FourbitArgs& a, hipStream_t stream) {
     using S = TileShape<GROUP, TB>;
     const int64_t m = a.ends == nullptr ? (a.n_rows + S::TM - 1) / S::TM : a.n_rows / S::TM + std::min(a.n_rows, a.n_experts);
     const int64_t n = (a.d_out + S::TN - 1) / S::TN, groups = (m * n + kXcds - 1) / kXcds * kXcds;
-    if (groups > (int64_t{1} << 22)) return GRINQH_EINVAL;
+    if (groups >= int64_t{1} << 23) return GRINQH_EINVAL;          // more results than the card holds
     const bool f32 = a.y_dtype == GRINQH_F32;
     const int whole_stores = a.d_out % (f32 ? 4 : 8) == 0 && aligned_to(a.y, 16);
     return launch_kernel(fourbit_tile_kernel<GROUP, TB>, dim3(static_cast<unsigned>(groups)), kTileThreads, 0, stream, a,

@@ -31,6 +31,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kRopeThreads = 256;
 constexpr int kMostAngles = 512;                   // of a workgroup: 4 to 16 tokens
+constexpr int kMostGroups = 1 << 22;               // of a launch
 constexpr int kFill = 2048;                        // workgroups that fill the card: eight to a CU
 
 struct RopeArgs {
@@ -238,7 +239,9 @@ grinqh_status rope_launch(RopeArgs& a, hipStream_t stream) {
     constexpr int kItems = kRopeThreads / (D / kPerLane), kTokens = kMostAngles / (D / 2);
     // About five rows to a group of lanes: a workgroup's tokens where there are
     // many, a token's heads over several workgroups where those leave CUs idle.
-    a.tokens = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({kTokens, 5 * kItems / a.rows, a.n_tokens / kFill})));
+    static_assert(int64_t{kTokens} * kMostGroups >= kMaxPacked, "a launch holds every call's tokens");
+    a.tokens = static_cast<int>(std::max({int64_t{1}, (a.n_tokens + kMostGroups - 1) / kMostGroups,
+                                          std::min<int64_t>({kTokens, 5 * kItems / a.rows, a.n_tokens / kFill})}));
     const int64_t groups = (a.n_tokens + a.tokens - 1) / a.tokens;
     const int parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((a.rows + kItems - 1) / kItems, kFill / groups)));
     a.step_tokens = parts * kItems / a.rows;
