@@ -557,8 +557,9 @@ grinqh_status grinqh_expert_linear(const grinqh_fourbit_layout* L, const grinqh_
  *   (a, b) <- (a cos t - b sin t, b cos t + a sin t),   t = position * freqs[p],
  * for the p-th of rope_dim / 2 pairs of the first rope_dim channels: (p, p +
  * rope_dim / 2), or with neighbours nonzero (2p, 2p + 1).  The other channels
- * are only normed.  Sums are fp32, angles fp64 up to the last turn; the result
- * is rounded once to dtype.  With a cache, the keys as rounded and the values as
+ * are only normed.  Sums are fp32 (a normed row whose squares pass fp32's range
+ * comes out as zeros, one of zeros with eps 0 as NaN), angles fp64 up to the
+ * last turn; the result is rounded once to dtype.  With a cache, the keys as rounded and the values as
  * they are go into their slots as grinqh_kv_write would put them.
  *   q, k       [n_tokens][heads][head_dim] of dtype, 16-byte aligned, tokens
  *              q_stride and k_stride elements apart (multiples of 16 bytes, from

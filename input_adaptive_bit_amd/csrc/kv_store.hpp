@@ -9,10 +9,10 @@ namespace grinqh {
 
 constexpr int kPerLane = 8;               // values of a row per lane
 
+// v of the lane that CTRL names, one for every lane.
 template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {
-    const int bits = __float_as_int(v);
-    return __int_as_float(__builtin_amdgcn_update_dpp(bits, bits, CTRL, 0xF, 0xF, false));
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, true));
 }
 
 // op over the D / 8 lanes of a row, the same bits in each of them.

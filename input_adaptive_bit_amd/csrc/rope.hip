@@ -15,9 +15,10 @@
 // radian); sine and cosine are of that fraction.
 //
 // Memory bounds it: 16381 tokens of 64 + 8 heads of 128 bf16, normed, into an 8-bit
-// cache, 670 MB, take 143 us (4.7 TB/s; a large copy reaches 5.25).  Angles worked out
-// by the lanes that use them, eight rows to each, took 194 us: 300 vector
-// instructions for a row, a third of them for angles, IEEE roots and divisions.
+// cache, 670 MB, take 129 us (5.2 TB/s, a large copy's rate), with 150 vector
+// instructions for a row of queries.  At 230 (addresses in 64 bits, signs of sines
+// by choice, copies around lane permutations) it was 145 us, with angles worked out
+// by the lanes that use them, IEEE roots and divisions 194.
 #include <algorithm>
 
 #include "internal.h"
@@ -112,10 +113,16 @@ __device__ __forceinline__ void read_eight(const float* halves, int count, int l
     }
 }
 
+// One of three values that are there already: a choice between what they are read
+// from would become an address that differs between lanes.
+template <typename V>
+__device__ __forceinline__ V pick(bool first, bool second, V a, V b, V c) { return first ? a : second ? b : c; }
+
 template <int D, typename T, int BITS>
 __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a) {
     constexpr int kLanes = D / kPerLane, kItems = kRopeThreads / kLanes, kTokens = kMostAngles / (D / 2);
-    __shared__ __attribute__((aligned(16))) float cosines[kMostAngles], sines[kMostAngles], weights[2][D];
+    // sines[1]: negative, for the lanes that hold a pair's first half
+    __shared__ __attribute__((aligned(16))) float cosines[kMostAngles], sines[2][kMostAngles], weights[2][D];
     __shared__ int64_t slots[kTokens];
     const int lane = threadIdx.x % kLanes, pairs = a.rope_dim / 2;
     const int64_t token0 = static_cast<int64_t>(blockIdx.x) * a.tokens;
@@ -124,11 +131,25 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a) {
     const int rows = a.rows;
     int r = threadIdx.x / kLanes + kItems * blockIdx.y, t = r / rows;
     r -= t * rows;
+    // Places within the workgroup's tokens: 16 strides of 2^24 floats fit 32 bits.
+    struct Rows {
+        char* at;
+        uint32_t stride;
+    };
+    const auto rows_of = [&](const void* base, int64_t stride) {
+        return Rows{static_cast<char*>(const_cast<void*>(base)) + token0 * stride * static_cast<int>(sizeof(T)), static_cast<uint32_t>(stride)};
+    };
+    const Rows q = rows_of(a.src[0], a.src_stride[0]), k = rows_of(a.src[1], a.src_stride[1]), v = rows_of(a.src[2], a.src_stride[2]);
+    const Rows q_out = rows_of(a.dst[0], a.dst_stride[0]), k_out = rows_of(a.dst[1], a.dst_stride[1]);
+    const auto place = [&](int t, int head, uint32_t stride) {
+        return (static_cast<uint32_t>(t) * stride + static_cast<uint32_t>(head * D + lane * kPerLane)) * static_cast<uint32_t>(sizeof(T));
+    };
+    const int first_v = a.n_q + a.n_kv;
     const auto load = [&](int t, int r) {
-        const int which = r < a.n_q ? 0 : r < a.n_q + a.n_kv ? 1 : 2, first = which == 0 ? 0 : which == 1 ? a.n_q : a.n_q + a.n_kv;
-        const T* base = static_cast<const T*>(which == 0 ? a.src[0] : which == 1 ? a.src[1] : a.src[2]);
-        const int64_t stride = which == 0 ? a.src_stride[0] : which == 1 ? a.src_stride[1] : a.src_stride[2];
-        return load_raw<T>(base + (token0 + t) * stride + (r - first) * D + lane * kPerLane);
+        const bool is_q = r < a.n_q, is_v = r >= first_v;
+        const char* at = pick(is_q, is_v, q.at, v.at, k.at);
+        const uint32_t stride = pick(is_q, is_v, q.stride, v.stride, k.stride);
+        return load_raw<T>(at + place(t, r - pick(is_q, is_v, 0, first_v, a.n_q), stride));
     };
     RawRow<T> next;
     if (t < tokens) next = load(t, r);                         // under way while the angles are worked out
@@ -138,7 +159,8 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a) {
         float s, c;
         sincospif(static_cast<float>(2.0 * (turns - rint(turns))), &s, &c);
         const int at = of * pairs + (a.neighbours ? j : in_halves(j, pairs));
-        sines[at] = s;
+        sines[0][at] = s;
+        sines[1][at] = -s;
         cosines[at] = c;
     }
     if (threadIdx.x < D) {
@@ -156,12 +178,6 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a) {
     const int across = a.rope_dim / (2 * kPerLane);
     const bool turned = lane * kPerLane < a.rope_dim, second = lane >= across;
     const int partner_at = ((threadIdx.x & 63) + (!turned ? 0 : second ? -across : across)) * 4;
-    // Eight lanes on (heads of 128, all turned): a rotation within 16 lanes, without LDS.
-    const auto from_partner = [&](float v) {
-        const int bits = __float_as_int(v);
-        return __int_as_float(across == 8 ? __builtin_amdgcn_update_dpp(bits, bits, 0x128, 0xF, 0xF, false)
-                                          : __builtin_amdgcn_ds_bpermute(partner_at, bits));
-    };
     while (t < tokens) {
         RawRow<T> raw = next;
         int next_t = t + a.step_tokens, next_r = r + a.step_rows;
@@ -170,11 +186,11 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a) {
             ++next_t;
         }
         if (next_t < tokens) next = load(next_t, next_r);
-        const bool is_q = r < a.n_q, is_v = r >= a.n_q + a.n_kv;
+        const bool is_q = r < a.n_q, is_v = r >= first_v;
         float w[kPerLane];
         widen<T>(raw, w);
         if (!is_v) {
-            if ((is_q ? a.weight[0] : a.weight[1]) != nullptr) {
+            if (pick(is_q, false, a.weight[0] != nullptr, a.weight[1] != nullptr, a.weight[1] != nullptr)) {
                 float sum = 0.f, g[kPerLane];
                 read_eight(weights[is_q ? 0 : 1], D, lane, g);
 #pragma unroll
@@ -187,7 +203,7 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a) {
             if (a.neighbours) {
                 if (turned) {
                     typedef float f32x4 __attribute__((ext_vector_type(4)));
-                    const f32x4 c = reinterpret_cast<const f32x4*>(cosines + t * pairs)[lane], s = reinterpret_cast<const f32x4*>(sines + t * pairs)[lane];
+                    const f32x4 c = reinterpret_cast<const f32x4*>(cosines + t * pairs)[lane], s = reinterpret_cast<const f32x4*>(sines[0] + t * pairs)[lane];
 #pragma unroll
                     for (int i = 0; i < kPerLane; i += 2) {
                         const float x = w[i], y = w[i + 1];
@@ -196,22 +212,27 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a) {
                     }
                 }
             } else {
-                float other[kPerLane];
+                // The other half's value times the sine.  Eight lanes on (heads of
+                // 128, all turned): a rotation within 16 lanes, without LDS.
+                float c[kPerLane], s[kPerLane];
+                const int of = t * pairs, at = !turned ? 0 : second ? lane - across : lane;
+                read_eight(cosines + of, pairs, at, c);
+                read_eight(sines[second ? 0 : 1] + of, pairs, at, s);
+                if (across == 8) {
 #pragma unroll
-                for (int i = 0; i < kPerLane; ++i) other[i] = from_partner(w[i]);
-                if (turned) {
-                    float c[kPerLane], s[kPerLane];
-                    read_eight(cosines + t * pairs, pairs, second ? lane - across : lane, c);
-                    read_eight(sines + t * pairs, pairs, second ? lane - across : lane, s);
-                    const float sign = second ? 1.f : -1.f;
+                    for (int i = 0; i < kPerLane; ++i) s[i] *= dpp<0x128>(w[i]);
+                } else {
 #pragma unroll
-                    for (int i = 0; i < kPerLane; ++i) w[i] = __builtin_fmaf(w[i], c[i], sign * (other[i] * s[i]));
+                    for (int i = 0; i < kPerLane; ++i)
+                        s[i] *= __int_as_float(__builtin_amdgcn_ds_bpermute(partner_at, __float_as_int(w[i])));
                 }
+#pragma unroll
+                for (int i = 0; i < kPerLane; ++i) w[i] = turned ? __builtin_fmaf(w[i], c[i], s[i]) : w[i];
             }
             raw = narrow<T>(w);
-            T* to = static_cast<T*>(is_q ? a.dst[0] : a.dst[1]);
-            if (to != nullptr) {
-                to += (token0 + t) * (is_q ? a.dst_stride[0] : a.dst_stride[1]) + (is_q ? r : r - a.n_q) * D + lane * kPerLane;
+            if (is_q || a.dst[1] != nullptr) {
+                char* to = pick(is_q, false, q_out.at, k_out.at, k_out.at) +
+                           place(t, is_q ? r : r - a.n_q, pick(is_q, false, q_out.stride, k_out.stride, k_out.stride));
 #pragma unroll
                 for (unsigned i = 0; i < sizeof(T) / 2; ++i) reinterpret_cast<u32x4*>(to)[i] = raw.v[i];
             }
@@ -220,12 +241,12 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a) {
             const int which = is_v ? 1 : 0;
             const int64_t row = is_q ? -1 : kv_row(a.d, slots[t], r - a.n_q - which * a.n_kv);
             if (row >= 0) {
-                uint8_t* codes = is_v ? a.codes[1] : a.codes[0];
+                uint8_t* codes = pick(is_v, false, a.codes[1], a.codes[0], a.codes[0]);
                 if constexpr (BITS == 16) {
                     if constexpr (sizeof(T) == 4) raw.v[0] = narrow<uint16_t>(w).v[0];
                     *reinterpret_cast<u32x4*>(codes + row * (D * 2) + lane * 16) = raw.v[0];
                 } else {
-                    store_quantised_row<D, BITS>(w, codes, is_v ? a.grid[1] : a.grid[0], row, lane);
+                    store_quantised_row<D, BITS>(w, codes, pick(is_v, false, a.grid[1], a.grid[0], a.grid[0]), row, lane);
                 }
             }
         }
