@@ -15,7 +15,7 @@
 //
 // What bounds them.  Memory: 16381 tokens of 8 fp32 heads of 128 at 8 bits are
 // written in 36 us (169 MB, 4.7 TB/s) and read back as bf16 in 19 us (101 MB, 5.4
-// TB/s); the IEEE division of each value is hidden.  A single token is a launch.
+// TB/s), with one division a row (kv_store.hpp).  A single token is a launch.
 #include <algorithm>
 #include <type_traits>
 

@@ -19,6 +19,8 @@
 // place cannot be read by other workgroups meanwhile, and of more sequences the
 // scan itself takes longer than a launch: then one workgroup scans, and a second
 // launch does the tokens (up to 4096 of few sequences: that same workgroup).
+// 48 sequences of a token each take 3.2 us, 700 of 512 tokens 6.8 in one launch and
+// 7.5 in two, 3000 of 100 tokens 11 (a captured launch of nothing takes 2.4).
 #include <algorithm>
 
 #include "internal.h"
