@@ -109,6 +109,90 @@ def test_few_and_many_outputs(dev, x_dtype, n, d_out, d_in, group):
     check_linear(dev, np.random.default_rng(n), n, d_in, d_out, group, x_dtype, "f32")
 
 
+# Sizes whose products go through the tiles of 64 rows and of 128 rows: enough of them to fill the card.
+TILED = [(1100, 2047), (2040, 4090)]
+
+
+@pytest.mark.parametrize("n,d_out", TILED)
+@pytest.mark.parametrize("group,d_in", [(32, 32), (32, 288), (64, 192), (64, 704), (128, 128), (128, 384), (128, 1152)])
+def test_tiles_of_many_rows(dev, n, d_out, group, d_in):
+    say(f"fourbit_linear n={n} {d_in}->{d_out} group={group}")
+    for y_dtype in ("f32", "bf16"):
+        check_linear(dev, np.random.default_rng(d_in), n, d_in, d_out, group, "bf16", y_dtype)
+
+
+@pytest.mark.parametrize("n,d_out", TILED)
+def test_tiles_of_strided_rows_results_off_alignment_and_values_that_are_not_finite(dev, n, d_out):
+    import input_adaptive_bit_amd as G
+    import torch
+    rng = np.random.default_rng(n)
+    q, s, z = make(rng, 1, 320, d_out, 64)
+    w = pack(q[0], s[0], z[0], dev)
+    x = to_type(activations(rng, n, 320, "bf16"), "bf16", dev)
+    want = G.fourbit_linear(w, x, torch.float32)
+    wide = torch.full((n + 50, 320 + 72), float("nan"), dtype=torch.bfloat16, device=dev)
+    wide[:n, 64:384] = x
+    flat = torch.full((n * d_out + 9,), 7.0, dtype=torch.float32, device=dev)
+    for at in (0, 1, 5):
+        y = flat[at:at + n * d_out].view(n, d_out)
+        G.grinqh_fourbit_linear(w, wide[:n, 64:384], y)
+        assert torch.equal(y, want) and (flat[:at] == 7).all() and (flat[at + n * d_out:] == 7).all()
+        flat.fill_(7.0)
+    x[3, 7], x[64, 319], x[n - 1, 0] = float("inf"), float("nan"), float("-inf")
+    got = G.fourbit_linear(w, x, torch.float32)
+    bad = [3, 64, n - 1]
+    keep = torch.ones(n, dtype=torch.bool, device=dev)
+    keep[bad] = False
+    assert not torch.isfinite(got[bad]).any() and torch.equal(got[keep], want[keep])
+
+
+@pytest.mark.parametrize("counts,d_out", [([700, 0, 600], 2050), ([1500, 540], 4000)])
+@pytest.mark.parametrize("gathered", [False, True])
+def test_tiles_of_experts(dev, counts, d_out, gathered):
+    import input_adaptive_bit_amd as G
+    import torch
+    rng = np.random.default_rng(d_out)
+    q, s, z = make(rng, len(counts), 256, d_out, 32)
+    w = pack(q, s, z, dev)
+    n = sum(counts) + 6                                                            # rows of no run at both ends
+    ends = np.concatenate([[2], 2 + np.cumsum(counts)]).astype(np.int32)
+    n_x = 300 if gathered else n - 9                                               # fewer rows of x than of y: zeros
+    x = activations(rng, n_x, 256, "bf16")
+    rows = rng.integers(-20, n_x + 20, n).astype(np.int32) if gathered else None
+    y = torch.full((n, d_out), 7.0, dtype=torch.float32, device=dev)
+    G.grinqh_expert_linear(w, to_type(x, "bf16", dev), torch.from_numpy(ends).to(dev), y,
+                           None if rows is None else torch.from_numpy(rows).to(dev))
+    want, size, written = O.experts(x, ends, rows, n, q, s, z, 32)
+    got = y.cpu().numpy()
+    assert (got[~written] == 7).all() and not written.all()
+    inside(got[written], want[written], bound(size[written], want[written], 32, 256, "f32"))
+
+
+def test_tiles_in_a_graph_give_the_same_bits(dev):
+    import input_adaptive_bit_amd as G
+    import torch
+    rng = np.random.default_rng(8)
+    q, s, z = make(rng, 1, 1024, 4096, 64)
+    w = pack(q[0], s[0], z[0], dev)
+    x = to_type(activations(rng, 2048, 1024, "bf16"), "bf16", dev)
+    y, t = torch.empty(2048, 4096, device=dev), torch.empty(1100, 4096, device=dev)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        G.grinqh_fourbit_linear(w, x, y)
+        G.grinqh_fourbit_linear(w, x[:1100], t)
+    other = torch.cuda.Stream()
+    for turn in range(4):
+        x.mul_(-0.5)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = y.clone(), t.clone()
+        other.wait_stream(torch.cuda.current_stream())
+        G.grinqh_fourbit_linear(w, x, y)                                           # two calls at once
+        G.grinqh_fourbit_linear(w, x[:1100], t, stream=other)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], y) and torch.equal(got[1], t)
+
+
 def test_quantised_weights_are_the_rtn_of_each_group(dev):
     """fourbit_quantize against the weights' own rounding, and the product against both."""
     import input_adaptive_bit_amd as G
