@@ -146,21 +146,25 @@ def test_tiles_of_strided_rows_results_off_alignment_and_values_that_are_not_fin
     assert not torch.isfinite(got[bad]).any() and torch.equal(got[keep], want[keep])
 
 
-@pytest.mark.parametrize("counts,d_out", [([700, 0, 600], 2050), ([1500, 540], 4000)])
+@pytest.mark.parametrize("counts,d_out", [([1, 0, 2, 19] + [0] * 60, 430), ([1, 0, 2, 9] + [0] * 60, 820), ([0, 3, 1, 1] * 16, 1023),
+                                          ([12, 33, 0, 7], 3000), ([17, 33, 0, 50], 5001), ([700, 0, 600], 2050), ([1500, 540], 4000)])
+@pytest.mark.parametrize("x_dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("gathered", [False, True])
-def test_tiles_of_experts(dev, counts, d_out, gathered):
+def test_experts_of_many_outputs(dev, x_dtype, counts, d_out, gathered):
+    """Few rows to many experts, more rows to few, tiles of many rows."""
     import input_adaptive_bit_amd as G
     import torch
+    say(f"expert_linear counts={counts[:4]} d_out={d_out} {x_dtype} gathered={gathered}")
     rng = np.random.default_rng(d_out)
     q, s, z = make(rng, len(counts), 256, d_out, 32)
     w = pack(q, s, z, dev)
     n = sum(counts) + 6                                                            # rows of no run at both ends
     ends = np.concatenate([[2], 2 + np.cumsum(counts)]).astype(np.int32)
-    n_x = 300 if gathered else n - 9                                               # fewer rows of x than of y: zeros
-    x = activations(rng, n_x, 256, "bf16")
+    n_x = 300 if gathered else n - 4                                               # fewer rows of x than of y: zeros
+    x = activations(rng, n_x, 256, x_dtype)
     rows = rng.integers(-20, n_x + 20, n).astype(np.int32) if gathered else None
     y = torch.full((n, d_out), 7.0, dtype=torch.float32, device=dev)
-    G.grinqh_expert_linear(w, to_type(x, "bf16", dev), torch.from_numpy(ends).to(dev), y,
+    G.grinqh_expert_linear(w, to_type(x, x_dtype, dev), torch.from_numpy(ends).to(dev), y,
                            None if rows is None else torch.from_numpy(rows).to(dev))
     want, size, written = O.experts(x, ends, rows, n, q, s, z, 32)
     got = y.cpu().numpy()

@@ -97,6 +97,43 @@ def test_the_cache_holds_the_rotated_keys_and_the_values(dev, bits, dtype, n, he
             assert torch.equal(c.k_grid, caches[0].k_grid) and torch.equal(c.v_grid, caches[0].v_grid)
 
 
+@pytest.mark.parametrize("n,heads,kv,dim,turned,dtype,neighbours,bits", [
+    (33001, 1, 1, 64, 64, "bf16", False, 0), (9001, 2, 1, 64, 32, "f32", True, 8), (20003, 3, 1, 128, 128, "bf16", False, 8),
+    (9001, 2, 2, 128, 48, "f32", False, 16), (9002, 1, 1, 256, 256, "bf16", False, 4), (4099, 5, 1, 256, 128, "bf16", True, 16),
+    (40000, 1, 1, 128, 0, "bf16", False, 16)])
+def test_many_tokens_at_once(dev, n, heads, kv, dim, turned, dtype, neighbours, bits):
+    """Several tokens to a workgroup: the bits of the same tokens a hundred at a time, and within the bound of the formula."""
+    import input_adaptive_bit_amd as G
+    import torch
+    say(f"qk_rope n={n} heads={heads}/{kv} dim={dim} turned={turned} {dtype} neighbours={neighbours} bits={bits}")
+    rng = np.random.default_rng(n)
+    rows = inputs(rng, n, heads, kv, dim, dtype)
+    x = to_type(rows, dtype, dev)
+    positions = rng.integers(0, 140000, n).astype(np.int32)
+    freqs, w = frequencies(turned), A.bf16(1 + 0.2 * rng.standard_normal(dim).astype(np.float32))
+    at, f, weight = torch.from_numpy(positions).to(dev), torch.from_numpy(freqs).to(dev), to_type(w, "bf16", dev)
+    slots = torch.from_numpy(rng.permutation(n + 50)[:n]).to(dev)
+    caches = [G.new_kv_cache(kv, dim, 16, n // 16 + 1, bits, dev) if bits else None for _ in range(2)]
+
+    def call(a, b, cache):
+        more = {"cache": cache, "v": x[a:b, heads + kv:], "slots": slots[a:b]} if bits else {}
+        return G.qk_rope(x[a:b, :heads], x[a:b, heads:heads + kv], at[a:b], f, weight, None, eps=1e-5, neighbours=neighbours, **more)
+
+    q, k = call(0, n, caches[0])
+    for a in range(0, n, max(100, n // 12)):
+        b = min(a + 100, n)
+        got = call(a, b, caches[1])
+        assert torch.equal(got[0], q[a:b]) and torch.equal(got[1], k[a:b])
+    if bits:
+        G.kv_write(caches[1], k, x[:, heads + kv:], slots)
+        assert torch.equal(caches[0].k_codes, caches[1].k_codes) and torch.equal(caches[0].v_codes, caches[1].v_codes)
+        if bits < 16:
+            assert torch.equal(caches[0].k_grid, caches[1].k_grid) and torch.equal(caches[0].v_grid, caches[1].v_grid)
+    some = np.concatenate([np.arange(0, n, 37), np.arange(n - 20, n)])
+    check(q[some], rows[some][:, :heads], positions[some], freqs, w, 1e-5, neighbours, dtype, "q")
+    check(k[some], rows[some][:, heads:heads + kv], positions[some], freqs, None, 1e-5, neighbours, dtype, "k")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("neighbours", [False, True])
 @pytest.mark.parametrize("n", [1, 9, 200])
