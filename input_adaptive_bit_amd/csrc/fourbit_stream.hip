@@ -265,6 +265,15 @@ __global__ __launch_bounds__(W * kWave, 2) void fourbit_wave_kernel(FourbitArgs 
     }
 }
 
+// What some lanes of a wave wrote to LDS is there for its other lanes to read, and
+// what they read for others to overwrite.  The wave's LDS operations are carried out in
+// their order, so this keeps the compiler from changing it and is no instruction.
+__device__ __forceinline__ void between_lanes() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // fp32 activations of up to MT rows: the three parts of a row take three
 // neighbouring columns.  A wave splits the activations of kDepth of its tiles at a
 // time (eight values a lane) and passes them to the operand's order through a
@@ -314,6 +323,7 @@ __global__ __launch_bounds__(W * kWave, 2) void fourbit_stream_f32_kernel(Fourbi
 #pragma unroll
             for (int p = 0; p < 3; ++p) parts[wave][lane * kCols + 3 * t + p] = __builtin_bit_cast(u32x4, part[p]);
         }
+        between_lanes();
         load_x(kt + kDepth * W);
 #pragma unroll
         for (int d = 0; d < kDepth; ++d) {
@@ -331,6 +341,7 @@ __global__ __launch_bounds__(W * kWave, 2) void fourbit_stream_f32_kernel(Fourbi
                 if (now + kDepth * W < a.k_tiles) load_codes<GROUP>(ring[d], at, now + kDepth * W);
             }
         }
+        between_lanes();                                       // all of it has been read: the next tiles may go there
     }
     red[wave][lane] = y[0];
     __syncthreads();
