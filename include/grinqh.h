@@ -500,8 +500,9 @@ size_t grinqh_fourbit_grid_bytes(const grinqh_fourbit_layout* L);
  *   s, z   fp16 [n_experts][d_out][d_in / group].
  *   codes, grid   out, 16-byte aligned, fully overwritten, padding included.
  * With grinqh_quantize_rtn(group, n_experts * d_out * d_in / group, 4, ...) on
- * the bf16 weights as they lie, its q, s and z are this call's.  The outputs
- * must not overlap each other or the inputs. */
+ * the bf16 weights as they lie (in several calls where that is more than 2^30),
+ * its q, s and z are this call's.  The outputs must not overlap each other or
+ * the inputs. */
 grinqh_status grinqh_fourbit_pack(const grinqh_fourbit_layout* L, const uint8_t* q, const uint16_t* s,
                                   const uint16_t* z, uint8_t* codes, uint16_t* grid, void* stream);
 

@@ -17,11 +17,13 @@ except ImportError:                              # the host calls below need no 
     torch = None
 
 from .attention import _empty, _fit, _float_code, _plain, _run, _tensor
-from .grinqh import GRINQH_EINVAL, ExpertArgs, FourbitLayout, GrinqhError, _check, load, quantize_rtn
+from .grinqh import GRINQH_EINVAL, ExpertArgs, FourbitLayout, GrinqhError, _check, load
 
 if torch is not None:
     from .attention import _CODES
     _I32, _U8, _F16 = torch.int32, torch.uint8, torch.float16
+
+_MOST_ROWS = 1 << 30                             # that a call of grinqh_quantize_rtn takes
 
 
 # ------------------------------------------------------------------ host ----
@@ -166,18 +168,19 @@ def fourbit_pack(q, s, z, stream=None) -> FourbitWeight:
 def fourbit_quantize(w, group: int, stream=None) -> FourbitWeight:
     """Rounds bf16 weights [d_out][d_in] or [n_experts][d_out][d_in] to nearest, group by
     group (grinqh_quantize_rtn at 4 bits), and packs them."""
-    _tensor(w, "w")
+    device = _tensor(w, "w")
     if w.dim() not in (2, 3) or group < 1 or w.shape[-1] % group != 0:
         raise ValueError(f"w must be [d_out][d_in] or [n_experts][d_out][d_in] with whole groups of {group}, not {list(w.shape)}")
-    if stream is not None:
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=w.device)
-        with torch.cuda.stream(stream):          # what lies between the two calls belongs to that stream
-            return fourbit_quantize(w, group)
-    with torch.cuda.device(w.device):
-        q, s, z = quantize_rtn(w.view(-1, group), 4)
     shape = (*w.shape[:-1], w.shape[-1] // group)
-    return fourbit_pack(q.view(w.shape), s.view(shape), z.view(shape))
+    rows = w.numel() // group
+    at = _plain(w, "w", torch.bfloat16, device, w.numel())
+    q = _empty(w.shape, _U8, device, stream)
+    s, z = (_empty(shape, _F16, device, stream) for _ in range(2))
+    for first in range(0, rows, _MOST_ROWS):
+        n = min(rows - first, _MOST_ROWS)
+        _run("grinqh_quantize_rtn", device, stream, group, n, 4, at + 2 * first * group, q.data_ptr() + first * group,
+             s.data_ptr() + 2 * first, z.data_ptr() + 2 * first)
+    return fourbit_pack(q, s, z, stream)
 
 
 def _outputs(x, n, width, dtype, device, stream):

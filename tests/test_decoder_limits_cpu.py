@@ -1,0 +1,52 @@
+"""What the 4-bit products' and the pages' calls do at the ends of their ranges,
+without a GPU."""
+
+import pytest
+
+import input_adaptive_bit_amd as G
+from tests.test_decoder_cpu import Fake
+
+
+# ----------------------------------------------------------------- weights --
+
+def test_weights_of_very_many_groups_are_rounded_in_pieces(monkeypatch):
+    """grinqh_quantize_rtn takes 2^30 rows; 1024 experts of 4096 to 16384 in groups of 32 have twice as many."""
+    import torch
+    from input_adaptive_bit_amd import fourbit
+    sent, packed = [], []
+    monkeypatch.setattr(torch, "Tensor", Fake)
+    monkeypatch.setattr(fourbit, "_run", lambda name, device, stream, *a: sent.append((name, stream, *a)))
+    monkeypatch.setattr(fourbit, "_empty", lambda shape, dtype, device, stream: Fake(*shape, dtype=dtype))
+    monkeypatch.setattr(fourbit, "fourbit_pack", lambda q, s, z, stream: packed.append((q, s, z, stream)))
+    for shape, group in (((1024, 16384, 4096), 32), ((2 ** 20, 2 ** 15 + 32), 32), ((40, 256), 128)):
+        rows = Fake(*shape).numel() // group
+        fourbit.fourbit_quantize(Fake(*shape), group, 7)
+        at = 0
+        for name, stream, d_in, n, bits, w, q, s, z in sent:
+            assert (name, stream, d_in, bits) == ("grinqh_quantize_rtn", 7, group, 4) and 1 <= n <= 1 << 30
+            assert (w - 4096, q - 4096, s - 4096, z - 4096) == (2 * at * group, at * group, 2 * at, 2 * at)
+            at += n
+        assert at == rows
+        q, s, z, stream = packed.pop()
+        assert stream == 7 and q.shape == shape and s.shape == z.shape == (*shape[:-1], shape[-1] // group)
+        sent.clear()
+
+
+def test_weights_that_cannot_be_rounded_are_refused(monkeypatch):
+    import torch
+    from input_adaptive_bit_amd import attention, fourbit
+    sent = []
+    monkeypatch.setattr(torch, "Tensor", Fake)
+    monkeypatch.setattr(fourbit, "_empty", lambda shape, dtype, device, stream: Fake(*shape, dtype=dtype))
+    monkeypatch.setattr(attention, "load", lambda: type("Lib", (), {"grinqh_quantize_rtn": lambda *a: sent.append(a)}))
+    for bad in (Fake(64, 128, dtype=torch.float32), Fake(64, 128, dtype=torch.float16)):
+        with pytest.raises(TypeError):
+            fourbit.fourbit_quantize(bad, 32)
+    for bad, group in ((Fake(64, 128, stride=(1, 64)), 32), (Fake(64, 128, stride=(256, 1)), 128), (Fake(128), 32), (Fake(64, 120), 32),
+                       (Fake(64, 128), 0)):
+        with pytest.raises(ValueError):
+            fourbit.fourbit_quantize(bad, group)
+    far = type("Stream", (), {"cuda_stream": 5, "device": torch.device("cuda:1")})
+    with pytest.raises(ValueError, match="stream"):
+        fourbit.fourbit_quantize(Fake(64, 128), 32, far)
+    assert not sent
