@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "device_common.hpp"
 #include "grinqh.h"
 #include "internal.h"
@@ -124,7 +126,15 @@ __device__ __forceinline__ int chunk_at(int r, int c) { return r * 256 + ((c ^ (
 
 bool valid_fourbit_layout(const grinqh_fourbit_layout* L);
 
-// The kernel for many rows (fourbit_tile.hip; bf16 activations), in tiles of 64 or 128.
+// Tiles of tm rows that a call can have: at most one more for every expert that can have rows.
+inline int64_t most_row_tiles(const FourbitArgs& a, int tm) {
+    return a.ends == nullptr ? (a.n_rows + tm - 1) / tm : a.n_rows / tm + std::min(a.n_rows, a.n_experts);
+}
+
+// The kernel for many rows (fourbit_tile.hip; bf16 activations), in tiles of 64 or
+// 128 rows x kTileColumns outputs, up to kMaxTileGroups of them (a launch has less than 2^32 work items).
+constexpr int kTileColumns = 256;
+constexpr int64_t kMaxTileGroups = (int64_t{1} << 23) - 16;
 grinqh_status launch_fourbit_tile(const FourbitArgs& a, int group, int rows, hipStream_t stream);
 
 }  // namespace grinqh

@@ -19,6 +19,8 @@
 // fp32 activations are split into three bf16 (8 + 8 + 8 bits, exact but for what
 // lies below the smallest bf16): each part a product of its own, or for few rows and
 // outputs three neighbouring columns of one.
+#include <math.h>
+
 #include <algorithm>
 
 #include "fourbit_common.hpp"
@@ -360,9 +362,8 @@ __global__ __launch_bounds__(W * kWave, 2) void fourbit_stream_f32_kernel(Fourbi
     if (col % 3 == 0 && col / 3 < run.count && j < a.d_out) store_outputs(a, vector_store, run.row + col / 3, j, sum);
 }
 
-// At most a tile more for every expert that can have rows.
 dim3 stream_grid(const FourbitArgs& a, int rows, int outputs) {
-    const int64_t tiles = a.ends == nullptr ? (a.n_rows + rows - 1) / rows : a.n_rows / rows + std::min(a.n_rows, a.n_experts);
+    const int64_t tiles = most_row_tiles(a, rows);
     return dim3((a.row_tiles + outputs - 1) / outputs, static_cast<unsigned>(std::min<int64_t>(tiles, kStreamTilesY)),
                 static_cast<unsigned>((tiles + kStreamTilesY - 1) / kStreamTilesY));
 }
@@ -398,7 +399,8 @@ int64_t expected_tiles(const FourbitArgs& a, int tm) {
 // A step of 128 inputs takes a 64-row tile 1.25 us and a 128-row tile 2, whether
 // few of them run or one on every CU; the wave kernel takes 0.15 ns for 16 rows x
 // 16 outputs x 128 inputs where there are enough of them to fill the card.  Smaller
-// groups cost all of them 8 and 35 % more.
+// groups cost all of them 8 and 35 % more.  Tiles that would be more than a launch
+// holds (results of well over 100 GB) are not taken: the wave kernel's grid has three dimensions.
 //
 // Of the wave kernels, the wider and taller one where it leaves work for every CU (us;
 // R W: outputs in sixteens and waves of a workgroup):
@@ -441,8 +443,11 @@ grinqh_status stream_group(const FourbitArgs& a, int x_dtype, int vector_store, 
         if (tiles(16) <= 400) return wave_f32_launch<GROUP, 1, 8, 8, 2>(a, vector_store, stream);
         return wave_f32_launch<GROUP, 4, 8, 4, 2>(a, vector_store, stream);
     }
-    const auto rounds = [&](int tm) { return (expected_tiles(a, tm) * ((a.d_out + 255) / 256) + 255) / 256; };
-    const double waves = 0.15e-3 * tiles(16), small = 1.25 * rounds(64), large = 2.0 * rounds(128);
+    const int64_t columns = (a.d_out + kTileColumns - 1) / kTileColumns;
+    const auto steps = [&](int tm, double step) {
+        return most_row_tiles(a, tm) * columns > kMaxTileGroups ? INFINITY : step * ((expected_tiles(a, tm) * columns + 255) / 256);
+    };
+    const double waves = 0.15e-3 * tiles(16), small = steps(64, 1.25), large = steps(128, 2.0);
     if (std::min(small, large) < waves) return launch_fourbit_tile(a, GROUP, small <= large ? 64 : 128, stream);
     if (a.ends == nullptr ? rows <= 8 : rows <= 2) {
         if (a.ends == nullptr && rows <= 4 && tiles(4) <= 320) return wave_launch<GROUP, 1, 1, 8, 4>(a, vector_store, stream);

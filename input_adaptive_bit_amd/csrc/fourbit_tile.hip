@@ -19,8 +19,6 @@
 // at every step's barrier.
 // Tried: rows through registers 289 us, twice the outputs a wave with half the rows
 // 301 us.
-#include <algorithm>
-
 #include "fourbit_common.hpp"
 
 namespace grinqh {
@@ -322,9 +320,8 @@ __global__ __launch_bounds__(kTileThreads) void fourbit_tile_kernel(FourbitArgs 
 template <int GROUP, int TB>
 grinqh_status tile_launch(const FourbitArgs& a, hipStream_t stream) {
     using S = TileShape<GROUP, TB>;
-    const int64_t m = a.ends == nullptr ? (a.n_rows + S::TM - 1) / S::TM : a.n_rows / S::TM + std::min(a.n_rows, a.n_experts);
-    const int64_t n = (a.d_out + S::TN - 1) / S::TN, groups = (m * n + kXcds - 1) / kXcds * kXcds;
-    if (groups >= int64_t{1} << 23) return GRINQH_EINVAL;          // more results than the card holds
+    static_assert(S::TN == kTileColumns && kTileThreads * (kMaxTileGroups + kXcds) < int64_t{1} << 32, "what the caller has counted");
+    const int64_t m = most_row_tiles(a, S::TM), n = (a.d_out + S::TN - 1) / S::TN, groups = (m * n + kXcds - 1) / kXcds * kXcds;
     const bool f32 = a.y_dtype == GRINQH_F32;
     const int whole_stores = a.d_out % (f32 ? 4 : 8) == 0 && aligned_to(a.y, 16);
     return launch_kernel(fourbit_tile_kernel<GROUP, TB>, dim3(static_cast<unsigned>(groups)), kTileThreads, 0, stream, a,

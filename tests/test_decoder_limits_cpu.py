@@ -50,3 +50,27 @@ def test_weights_that_cannot_be_rounded_are_refused(monkeypatch):
     with pytest.raises(ValueError, match="stream"):
         fourbit.fourbit_quantize(Fake(64, 128), 32, far)
     assert not sent
+
+
+# ---------------------------------------------------------------- products --
+
+def _no_gpu():
+    import torch
+    return not torch.cuda.is_available()
+
+
+@pytest.mark.skipif(not _no_gpu(), reason="without a GPU a call that passes its checks ends at the launch; with one it would run on these addresses")
+@pytest.mark.parametrize("experts,rows,d_in,d_out", [(1024, 65536, 32, 1 << 20), (1024, 66000, 32, (1 << 20) - 3), (2, 1 << 20, 64, 1 << 18),
+                                                     (1, 1 << 20, 32, 1 << 20), (1, 40, 32, 16), (8, 4094, 4096, 14336)])
+def test_no_size_of_the_layout_is_refused(experts, rows, d_in, d_out):
+    """Experts' runs that could have more tiles than a launch has workgroups are a call like any other."""
+    import ctypes
+    from input_adaptive_bit_amd import grinqh as B
+    L = G.grinqh_fourbit_layout_init(d_in, d_out, 32, experts)
+    at = [(i + 1) << 44 for i in range(6)]                                             # places that nothing overlaps
+    for x_dtype in (B.GRINQH_BF16, B.GRINQH_F32):
+        a = B.ExpertArgs(at[0], d_in, x_dtype, rows, at[1], at[2], rows, at[3], at[4], at[5], B.GRINQH_BF16)
+        assert B.load().grinqh_expert_linear(ctypes.byref(L), ctypes.byref(a), None) in (B.GRINQH_ENODEV, B.GRINQH_EDEVICE)
+        if experts == 1:
+            status = B.load().grinqh_fourbit_linear(ctypes.byref(L), at[0], x_dtype, d_in, rows, at[3], at[4], at[5], B.GRINQH_BF16, None)
+            assert status in (B.GRINQH_ENODEV, B.GRINQH_EDEVICE)
