@@ -519,8 +519,9 @@ grinqh_status grinqh_fourbit_pack(const grinqh_fourbit_layout* L, const uint8_t*
  * the sum of three bf16; many tokens of fp32 are worked on sixteen at a time, so
  * a long prompt is better in bf16); sums are fp32, and the same call gives the
  * same bits.  An infinite or NaN activation makes its token's outputs
- * non-finite and no other's, and so may one past 2^115.  y must not overlap
- * anything that is read. */
+ * non-finite and no other's, and so may one past 2^115, or a sum of
+ * |x| (s (16 + q) + |z - 15.5 s|) past fp32's range, where y itself would not
+ * reach it.  y must not overlap anything that is read. */
 grinqh_status grinqh_fourbit_linear(const grinqh_fourbit_layout* L, const void* x, grinqh_dtype x_dtype,
                                     int64_t x_stride, int32_t n_tokens, const uint8_t* codes,
                                     const uint16_t* grid, void* y, grinqh_dtype y_dtype, void* stream);
