@@ -615,12 +615,13 @@ grinqh_status grinqh_qk_rope(const grinqh_rope_args* args, void* stream);
  *
  * grinqh_kv_extend makes room for n_new[b] new tokens behind the seq_lens[b]
  * cached ones of every sequence b (negative counts as 0) and writes what
- * the other calls of the step take.  Sequences are served in order: one whose
- * pages, with those of the sequences before it (served or not), are more than
- * the list holds is refused, and so is one that would pass max_pages or whose
- * tokens do not fit into capacity; a refused sequence keeps its length and
- * pages, and its new tokens have no slots.  A sequence without new tokens is
- * never refused.
+ * the other calls of the step take.  A sequence that no step could serve, because
+ * it would pass max_pages or needs more than n_pages new ones, is refused and its
+ * pages count for nobody.  The others are served in order: one whose pages, with
+ * those of the sequences before it (served or not), are more than the list holds
+ * is refused, and so is one whose tokens do not fit into capacity.  A refused
+ * sequence keeps its length and pages, and its new tokens have no slots.  A
+ * sequence without new tokens is never refused.
  *   page_table  int32 [batch][max_pages], rows table_stride entries apart: entries
  *               of new pages are written, the others left.
  *   new_lens    int32 [batch] out: lengths with the new tokens (may be seq_lens).

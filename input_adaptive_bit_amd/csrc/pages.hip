@@ -160,11 +160,13 @@ __global__ __launch_bounds__(THREADS) void extend_scan_kernel(PagesArgs a) {
         const bool there = b < p.batch;
         const uint32_t old = there ? max(p.seq_lens[b], 0) : 0, fresh = there ? max(p.n_new[b], 0) : 0;
         const uint32_t held = pages_of(old), wanted = pages_of(old + fresh), need = wanted - held;
+        // What no step could serve asks for no pages: else the sequences behind it
+        // would be refused for its sake, step after step.
+        const bool possible = wanted <= static_cast<uint32_t>(p.max_pages) && need <= static_cast<uint32_t>(p.n_pages);
         Pair all;
-        const Pair upto = add(asked, group_sum_up_to<WAVES>(Pair{need, fresh}, waves[0], all));
+        const Pair upto = add(asked, group_sum_up_to<WAVES>(Pair{possible ? need : 0u, fresh}, waves[0], all));
         asked = add(asked, all);
-        const bool granted = fresh == 0 || (upto.a <= n_free && wanted <= static_cast<uint32_t>(p.max_pages) &&
-                                            upto.b <= static_cast<uint32_t>(p.capacity));
+        const bool granted = fresh == 0 || (possible && upto.a <= n_free && upto.b <= static_cast<uint32_t>(p.capacity));
         // Pages are taken by their place among those of all sequences, served or
         // not: the pages of one that is refused for its own sake stay unused in
         // the list only if none behind it are taken, so places are counted again

@@ -108,9 +108,10 @@ def extend(table, lens, new, free, n_free: int, page: int, capacity: int):
     for b in range(batch):
         old, fresh = max(int(lens[b]), 0), max(int(new[b]), 0)
         held, total = -(-old // page), -(-(old + fresh) // page)
-        wanted_pages += total - held
+        possible = total <= columns and total - held <= n_pages          # by some step, if not by this one
+        wanted_pages += total - held if possible else 0
         begin = cu_q[-1]
-        granted = fresh == 0 or (wanted_pages <= n_free and total <= columns and begin + fresh <= capacity)
+        granted = fresh == 0 or (possible and wanted_pages <= n_free and begin + fresh <= capacity)
         if granted:
             for i in range(held, total):
                 table[b, i] = free[n_free - 1 - taken]

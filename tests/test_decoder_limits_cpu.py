@@ -74,3 +74,21 @@ def test_no_size_of_the_layout_is_refused(experts, rows, d_in, d_out):
         if experts == 1:
             status = B.load().grinqh_fourbit_linear(ctypes.byref(L), at[0], x_dtype, d_in, rows, at[3], at[4], at[5], B.GRINQH_BF16, None)
             assert status in (B.GRINQH_ENODEV, B.GRINQH_EDEVICE)
+
+
+# ------------------------------------------------------------------- pages --
+
+def test_a_request_that_can_never_be_served_takes_nothing_from_those_behind_it():
+    """Pages of 16, 3 columns, a pool of 6 pages with 2 unused: 49 tokens pass the columns, 7 pages pass the pool."""
+    from oracle import decoder_oracle as O
+    free = [5, 3, -1, -1, -1, -1]
+    got = O.extend([[-1] * 3] * 4, [0, 0, 0, 0], [49, 16, 0, 10], free, 2, 16, 80)
+    assert got["refused"] == 1 and got["seq_lens"].tolist() == [0, 16, 0, 10] and got["n_free"] == 0
+    assert got["table"].tolist() == [[-1] * 3, [3, -1, -1], [-1] * 3, [5, -1, -1]]
+    assert got["slots"].tolist() == [-1] * 49 + list(range(48, 64)) + list(range(80, 90)) + [-1] * 5
+    assert got["cu_q"].tolist() == [0, 49, 65, 65, 75] and got["cu_k"].tolist() == [0, 0, 16, 16, 26]
+    got = O.extend([[-1] * 9] * 3, [0, 0, 0], [97, 33, 16], free, 2, 16, 200)
+    # seven pages are more than the pool has; three are more than the list holds, and come before the next request
+    assert got["refused"] == 3 and got["seq_lens"].tolist() == [0, 0, 0]
+    got = O.extend([[-1] * 9] * 3, [0, 0, 0], [97, 17, 16], free, 2, 16, 200)
+    assert got["refused"] == 2 and got["seq_lens"].tolist() == [0, 17, 0] and got["table"][1].tolist() == [3, 5] + [-1] * 7

@@ -8,6 +8,7 @@ from oracle import decoder_oracle as O
 from tests.attention_util import inside, to_type
 from tests.gpu_util import require_gpu, say
 from tests.test_gpu_fourbit import activations, bound, check_linear, make, pack
+from tests.test_gpu_pages import pool, run, same
 
 pytestmark = pytest.mark.gpu
 
@@ -169,3 +170,31 @@ def test_the_largest_activations(dev, x_dtype, group, d_in, n, d_out):
     y = G.fourbit_linear(pack(q[0], s[0], z[0], dev), to_type(x, x_dtype, dev), torch.float32).cpu().numpy()
     want, size = O.linear(x, q[0], s[0], z[0], group)
     inside(y, want, bound(size, want, group, d_in, "f32"))
+
+
+# ------------------------------------------------------------------- pages --
+
+@pytest.mark.parametrize("batch", [5, 300, 1500])
+@pytest.mark.parametrize("capacity", [2000, 60000])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_requests_that_can_never_be_served_starve_nobody(dev, batch, capacity, in_place):
+    """Requests past the table's columns, and past the whole pool, among ordinary ones that the list can serve."""
+    rng = np.random.default_rng(batch)
+    lens, new = rng.integers(0, 60, batch), rng.integers(1, 20, batch)
+    if capacity == 2000:
+        new = np.where(np.arange(batch) < 60, new, 0)
+    new[0], new[2] = 1000, 161                                                        # 63 and 11 pages of 16
+    lens[0], lens[2] = 0, 0
+    for columns, n_pages, spare in ((10, None, 3 * batch), (100, None, 3 * batch), (100, None, 2), (10, None, 7)):
+        table, free, n_free = pool(rng, lens, 16, columns, spare, n_pages)
+        want = O.extend(table, lens, new, free, n_free, 16, capacity)
+        say(f"kv_extend batch={batch} capacity={capacity} columns={columns} free={n_free} refused={want['refused']}")
+        got = run(dev, table, lens, new, free, n_free, 16, capacity, in_place)
+        same(got, want)
+        if columns == 10 and spare > batch:
+            assert got["refused"] == 2 and (got["seq_lens"][3:] == (lens + new)[3:]).all()
+    few = np.array([0, 0, 3, 16][:batch])
+    for n_free in (0, 1, 2, 5):                                                       # a pool of five pages
+        table, free = np.full((4, 9), -1, np.int32), np.array([4, 0, 2, 1, 3], np.int32)
+        table[2, 0], table[3, 0] = 1, 3
+        same(run(dev, table, few, [81, 17, 14, 1], free, n_free, 16, 200, in_place), O.extend(table, few, [81, 17, 14, 1], free, n_free, 16, 200))
