@@ -13,12 +13,12 @@
 // next products run.  z S is one more matrix instruction a group, of z and S
 // cut into bf16 parts.
 //
-// 2048 rows 4096 to 14336: 270 us, 0.89 PFLOP/s, where a large bf16 product of the
+// 2048 rows 4096 to 14336: 266 us, 0.90 PFLOP/s, where a large bf16 product of the
 // library reaches 1.37.  A step of 128 rows takes 2.1 us, 1.0 of them matrix
 // instructions: scaling, unpacking and LDS reads share the issue of waves that meet
 // at every step's barrier.
-// Tried: rows through registers 289 us, twice the outputs a wave with half the rows
-// 301 us.
+// Tried, before results were stored in whole stretches: rows through registers
+// 289 us, twice the outputs a wave with half the rows 301 us.
 #include "fourbit_common.hpp"
 
 namespace grinqh {
@@ -291,7 +291,7 @@ __global__ __launch_bounds__(kTileThreads) void fourbit_tile_kernel(FourbitArgs 
         for (int i = 0; i < 16; ++i) y[TC + t][i] = __builtin_fmaf(s, p[1][t][i], y[TC + t][i]);
 
     // Out: 32 rows at a time through LDS, so that a wave stores whole stretches of
-    // them (2048 rows 4096 to 14336: 278 us, 289 element by element).  The rows lie 32 bytes apart from multiples of 256: a lane
+    // them (2048 rows 4096 to 14336: 266 us, 288 element by element).  The rows lie 32 bytes apart from multiples of 256: a lane
     // pair's rows, 4 apart, fall on different banks.  No rows are brought any more:
     // the last step has waited for them.
     constexpr int kOutStride = S::TN * 4 + 32;

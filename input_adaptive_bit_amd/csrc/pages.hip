@@ -3,8 +3,8 @@
 //
 // With h = ceil(len / page) pages held, t = ceil((len + new) / page) needed and
 // need = t - h, sequence b takes the pages
-//   free[n_free - 1 - (sum_{c < b} need_c + i)],  i = 0 .. need - 1,
-// if the sums of need up to b fit.  So one scan over the sequences decides all
+//   free[n_free - 1 - (sum_{c < b, served} need_c + i)],  i = 0 .. need - 1,
+// if the sum of need over all up to b, served or not, is no more than n_free.  So one scan over the sequences decides all
 // of it (fourfold: pages, new tokens, granted pages, lengths), and then every new token can be
 // worked on alone: its sequence by a search in the ends, its page from the table
 // (the page that was begun before) or from the list.  The token that begins a
