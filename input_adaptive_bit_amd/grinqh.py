@@ -431,8 +431,9 @@ def grinqh_quantize_rtn(w, b_max: int, q, s, z, stream=None) -> None:
     _need(q, "q", (torch.uint8,), d_out * d_in)
     _need(s, "s", (torch.float16,), 2 * d_out)
     _need(z, "z", (torch.float16,), 2 * d_out)
-    _check(load().grinqh_quantize_rtn(d_in, d_out, int(b_max), _ptr(w), _ptr(q), _ptr(s), _ptr(z), _stream(stream)),
-           "grinqh_quantize_rtn")
+    top = (1 << 31) - 1                          # ctypes would drop the higher bits, and the library refuses this
+    _check(load().grinqh_quantize_rtn(min(d_in, top), min(d_out, top), int(b_max), _ptr(w), _ptr(q), _ptr(s), _ptr(z),
+                                      _stream(stream)), "grinqh_quantize_rtn")
 
 
 def grinqh_prefill_workspace_bytes(M: int) -> int:

@@ -92,3 +92,18 @@ def test_a_request_that_can_never_be_served_takes_nothing_from_those_behind_it()
     assert got["refused"] == 3 and got["seq_lens"].tolist() == [0, 0, 0]
     got = O.extend([[-1] * 9] * 3, [0, 0, 0], [97, 17, 16], free, 2, 16, 200)
     assert got["refused"] == 2 and got["seq_lens"].tolist() == [0, 17, 0] and got["table"][1].tolist() == [3, 5] + [-1] * 7
+
+
+def test_row_counts_past_32_bits_are_refused(monkeypatch):
+    """2^32 + 5 rows of one weight are not five."""
+    import torch
+    from input_adaptive_bit_amd import grinqh
+    monkeypatch.setattr(torch, "Tensor", Fake)
+    size_of = {torch.bfloat16: 2, torch.uint8: 1, torch.float16: 2}
+    monkeypatch.setattr(Fake, "element_size", lambda self: size_of[self.dtype], raising=False)
+    for d_out, d_in in ((2 ** 32 + 5, 1), (2 ** 31, 32), (2 ** 30 + 1, 32), (5, 2 ** 32 + 16)):
+        n = d_out * d_in
+        q, s = Fake(n, dtype=torch.uint8), Fake(d_out, dtype=torch.float16)
+        with pytest.raises(G.GrinqhError) as e:
+            grinqh.grinqh_quantize_rtn(Fake(d_out, d_in), 4, q, s, s, stream=3)
+        assert e.value.status == grinqh.GRINQH_EINVAL
