@@ -664,7 +664,8 @@ grinqh_status grinqh_kv_extend(const grinqh_extend_args* args, void* stream);
  * nonzero (uint8 [batch]), the pages that seq_lens[b] tokens take are put behind
  * the list in their order (entries that name no page of the pool are passed
  * over, and what would pass n_pages is dropped), the entries become -1 and the
- * length 0. */
+ * length 0.  Nothing counts how often a page is named: one that two sequences share
+ * would be listed twice, so all but the last give it back as -1. */
 grinqh_status grinqh_kv_release(int32_t* page_table, int64_t table_stride, int32_t* seq_lens,
                                 const uint8_t* finished, int32_t batch, int32_t max_pages, int32_t page_size,
                                 int32_t* free_pages, int32_t* n_free, int32_t n_pages, void* stream);
