@@ -10,8 +10,8 @@
 //       s_j and z_j (a NaN quotient gives 0; a row with s_j = 0 gets q = 0),
 //
 // so that s_j * (q + 1/2) + z_j, the key-design-3 value at b = b_max, is the
-// midpoint of w's interval.  One workgroup per output row (up to 2^20 rows at a
-// time): a min/max pass, then the codes (the row is read again from L2).
+// midpoint of w's interval.  One workgroup per output row: a min/max pass,
+// then the codes (the row is read again from L2).
 #include "internal.h"
 #include "rtn.hpp"
 
@@ -19,18 +19,16 @@ namespace grinqh {
 namespace {
 
 constexpr int kRtnThreads = 256;
-// More rows go round again: a launch of 2^32 work items or more would not be
-// refused, it would run only what its lower 32 bits count.
-constexpr int kMaxRtnGroups = 1 << 20;
+// Rows of a launch.  2^32 work items or more would not be refused: the launch would
+// run what their lower 32 bits count.
+constexpr int kRtnRows = 1 << 23;
 
 __device__ __forceinline__ float bf16_value(uint32_t b) { return __uint_as_float(b << 16); }
 
-// Row j, by a whole workgroup.  red_lo, red_hi and sz may be another row's before and
-// after: a thread writes them only past a barrier that all have come to since
-// they read them.
-__device__ __forceinline__ void rtn_row(const uint16_t* __restrict__ w, int j, int d_in, int b_max, uint8_t* __restrict__ q,
-                                        uint16_t* __restrict__ s_out, uint16_t* __restrict__ z_out, float* red_lo,
-                                        float* red_hi, float* sz) {
+__global__ __launch_bounds__(kRtnThreads) void rtn_kernel(const uint16_t* __restrict__ w, int d_in, int b_max,
+                                                          uint8_t* __restrict__ q, uint16_t* __restrict__ s_out,
+                                                          uint16_t* __restrict__ z_out) {
+    const int j = blockIdx.x;
     const int tid = threadIdx.x;
     const uint16_t* row = w + static_cast<size_t>(j) * d_in;
     uint8_t* qrow = q + static_cast<size_t>(j) * d_in;
@@ -56,6 +54,8 @@ __device__ __forceinline__ void rtn_row(const uint16_t* __restrict__ w, int j, i
             hi = fmaxf(hi, a);
         }
     }
+    __shared__ float red_lo[kRtnThreads], red_hi[kRtnThreads];
+    __shared__ float sz[2];
     red_lo[tid] = lo;
     red_hi[tid] = hi;
     __syncthreads();
@@ -98,14 +98,6 @@ __device__ __forceinline__ void rtn_row(const uint16_t* __restrict__ w, int j, i
     }
 }
 
-__global__ __launch_bounds__(kRtnThreads) void rtn_kernel(const uint16_t* __restrict__ w, int d_in, int d_out, int b_max,
-                                                          uint8_t* __restrict__ q, uint16_t* __restrict__ s_out,
-                                                          uint16_t* __restrict__ z_out) {
-    __shared__ float red_lo[kRtnThreads], red_hi[kRtnThreads];
-    __shared__ float sz[2];
-    for (int j = blockIdx.x; j < d_out; j += gridDim.x) rtn_row(w, j, d_in, b_max, q, s_out, z_out, red_lo, red_hi, sz);
-}
-
 }  // namespace
 }  // namespace grinqh
 
@@ -123,8 +115,13 @@ extern "C" grinqh_status grinqh_quantize_rtn(int32_t d_in, int32_t d_out, int32_
     hipError_t e;
     if (!current_device_info(&dev, &e))
         return (e == hipErrorNoDevice || e == hipErrorInvalidDevice) ? GRINQH_ENODEV : GRINQH_EDEVICE;
-    rtn_kernel<<<static_cast<unsigned>(d_out < kMaxRtnGroups ? d_out : kMaxRtnGroups), kRtnThreads, 0, static_cast<hipStream_t>(stream)>>>(
-        w, d_in, d_out, b_max, q, s, z);
-    e = hipGetLastError();
-    return e == hipSuccess ? GRINQH_OK : GRINQH_EDEVICE;
+    for (int first = 0; first < d_out; first += kRtnRows) {
+        const int rows = d_out - first < kRtnRows ? d_out - first : kRtnRows;
+        const size_t at = static_cast<size_t>(first) * d_in;
+        rtn_kernel<<<static_cast<unsigned>(rows), kRtnThreads, 0, static_cast<hipStream_t>(stream)>>>(
+            w + at, d_in, b_max, q + at, s + first, z + first);
+        e = hipGetLastError();
+        if (e != hipSuccess) return GRINQH_EDEVICE;
+    }
+    return GRINQH_OK;
 }
